@@ -401,7 +401,7 @@ def run(state):
         return refs, table, lens, moves, s["pools"]
     M.pages_free(refs, table, lens, s["done"])
     moves, count = M.pages_compact(refs, table)
-    M.pages_copy(s["pools"], moves)
+    M.pages_copy(s["pools"], moves, count)
     return refs, table, lens, moves, count, s["pools"]
 
 
