@@ -17,16 +17,19 @@ using namespace moe;
 struct moe_handle : public Handle {};
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
 
-moe_status fail(moe_status s, const char* fmt, ...) {
+moe_status moe::fail(moe_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
   return s;
 }
+
+namespace {
+
 
 moe_status cuda_fail(cudaError_t e, const char* what) {
   if (e == cudaErrorMemoryAllocation)

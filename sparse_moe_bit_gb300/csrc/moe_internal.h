@@ -91,6 +91,9 @@ struct Handle {
   cudaStream_t last_stream = nullptr;
 };
 
+// Records the message moe_last_error() returns (per thread) and returns s.
+moe_status fail(moe_status s, const char* fmt, ...);
+
 // Launches kern and returns that launch's own status (cudaGetLastError after a
 // <<<>>> launch would also report, and clear, an error left by an earlier,
 // unrelated launch).

@@ -1,0 +1,469 @@
+// C ABI of the paged-cache operators (include/paged.h): argument checks, the
+// choice of kernel and split, launches on the caller's stream.
+#include <cmath>
+#include <cstring>
+
+#include "paged_internal.h"
+
+using namespace moe;
+
+namespace moe {
+
+namespace {
+__device__ int g_paged_err;
+constexpr int kMaxDevices = 64;
+}  // namespace
+
+int* paged_error_word() {
+  static int* at[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  if (!at[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_paged_err) != cudaSuccess) return nullptr;
+    at[dev] = static_cast<int*>(p);
+  }
+  return at[dev];
+}
+
+int device_sms() {
+  static int sms[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 152;
+  if (!sms[dev]) {
+    int v = 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1)
+      v = 152;
+    sms[dev] = v;
+  }
+  return sms[dev];
+}
+
+}  // namespace moe
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+#define PAGED_CK(call, what)                                                             \
+  do {                                                                                   \
+    const cudaError_t e_ = (call);                                                       \
+    if (e_ != cudaSuccess)                                                               \
+      return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e_));                 \
+  } while (0)
+
+moe_status check_cache(const paged_cache* c, CacheView* v) {
+  if (!c) return fail(MOE_ERR_INVALID_ARG, "cache is NULL");
+  if (c->dtype != PAGED_BF16 && c->dtype != PAGED_F16)
+    return fail(MOE_ERR_INVALID_ARG, "cache dtype %d", c->dtype);
+  if (c->pages < 1 || c->page < 1 || c->heads < 1)
+    return fail(MOE_ERR_INVALID_ARG, "bad cache (pages=%d page=%d heads=%d)", c->pages, c->page,
+                c->heads);
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
+    return fail(MOE_ERR_INVALID_ARG, "cache arrays NULL or not 16-byte aligned");
+  if (c->page_stride < 0 || c->row_stride < 0 || c->head_stride < 0 || c->page_stride % 8 ||
+      c->row_stride % 8 || c->head_stride % 8)
+    return fail(MOE_ERR_INVALID_ARG, "cache strides must be multiples of 8 elements");
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(MOE_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128, 256)", c->dim);
+  v->k = static_cast<uint16_t*>(c->k);
+  v->v = static_cast<uint16_t*>(c->v);
+  v->pages = c->pages;
+  v->page = c->page;
+  v->heads = c->heads;
+  v->dim = c->dim;
+  v->page_stride = c->page_stride;
+  v->row_stride = c->row_stride;
+  v->head_stride = c->head_stride;
+  v->div = make_fastdiv(c->page);
+  return MOE_OK;
+}
+
+moe_status check_batch(const paged_batch* b, int page, BatchView* v) {
+  if (!b) return fail(MOE_ERR_INVALID_ARG, "batch is NULL");
+  if (b->N < 0 || b->T < 0 || b->width < 0 || b->table_stride < 0)
+    return fail(MOE_ERR_INVALID_ARG, "bad batch (N=%d T=%d width=%d)", b->N, b->T, b->width);
+  if (b->N > 0 && b->T > 0 && (!b->cu_q || !b->kv_len || (b->width > 0 && !b->table)))
+    return fail(MOE_ERR_INVALID_ARG, "NULL batch array");
+  if (!aligned(b->cu_q, 4) || !aligned(b->kv_len, 4) || !aligned(b->table, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned batch array");
+  v->table = b->table;
+  v->cu = b->cu_q;
+  v->kv_len = b->kv_len;
+  v->N = b->N;
+  v->T = b->T;
+  v->width = b->width;
+  v->table_stride = b->table_stride;
+  const long long cap = (long long)b->width * page;
+  v->capacity = cap > 0x7fffff00ll ? 0x7fffff00 : (int)cap;
+  return MOE_OK;
+}
+
+moe_status check_rope(int D, const double* freq, int r, float mscale) {
+  if (r < 1 || 2 * r > D || D > 1024)
+    return fail(MOE_ERR_INVALID_ARG, "%d frequencies for heads of %d features", r, D);
+  if (!freq || !aligned(freq, 8)) return fail(MOE_ERR_INVALID_ARG, "freq NULL or misaligned");
+  if (!std::isfinite(mscale)) return fail(MOE_ERR_INVALID_ARG, "mscale is not finite");
+  return MOE_OK;
+}
+
+// Choice of kernel and split for one call; see plan().
+struct Plan {
+  int tiles, chunks, chunk;
+  size_t ws;
+};
+
+// Rows path: 16-row tiles.  Enough chunks that the work items make three
+// waves of the CTAs an SM holds (one of head dim 256, two of 128, three of
+// 64), which evens out ragged contexts; no chunk below 256 keys, where a
+// CTA's start and the join cost more than they spread.
+Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv) {
+  Plan r;
+  const int G = Hq / c.heads;
+  const long long per = b.N > 0 ? (b.T + b.N - 1) / b.N : 0;
+  long long mq = max_q > 0 ? max_q : per;
+  if (mq > b.T) mq = b.T;
+  long long kv = max_kv > 0 ? max_kv : b.capacity;
+  if (kv > b.capacity) kv = b.capacity;
+  long long tiles = (mq * G + kRowTile - 1) / kRowTile;
+  if (tiles < 1) tiles = 1;
+  long long span = kv;
+  if (window > 0 && (long long)window + kRowTile < span) span = (long long)window + kRowTile;
+  const long long items = (long long)b.N * tiles * c.heads;
+  const int occ = c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3);
+  const long long target = 3ll * occ * device_sms();
+  long long chunks = items > 0 ? target / items : 1;
+  if (chunks < 1) chunks = 1;
+  long long chunk = (span + chunks - 1) / chunks;
+  chunk = (chunk + 63) / 64 * 64;
+  if (chunk < 256) chunk = 256;
+  chunks = (span + chunk - 1) / chunk;
+  if (chunks < 1) chunks = 1;
+  r.tiles = (int)tiles;
+  r.chunk = (int)chunk;
+  r.chunks = (int)chunks;
+  r.ws = r.chunks > 1
+             ? (((size_t)b.T * Hq * r.chunks * 8 + 255) / 256 * 256 + (size_t)b.T * Hq * r.chunks * c.dim * 4)
+             : 0;
+  return r;
+}
+
+moe_status check_attention(const paged_cache* cache, const paged_batch* batch, int Hq, int window,
+                           int max_q, int max_kv, CacheView* c, BatchView* b) {
+  moe_status s = check_cache(cache, c);
+  if (s != MOE_OK) return s;
+  s = check_batch(batch, cache->page, b);
+  if (s != MOE_OK) return s;
+  if (Hq < 1 || Hq % cache->heads)
+    return fail(MOE_ERR_INVALID_ARG, "%d query heads on %d key/value heads", Hq, cache->heads);
+  if (window < 0 || max_q < 0 || max_kv < 0)
+    return fail(MOE_ERR_INVALID_ARG, "negative window, max_q or max_kv");
+  if ((long long)batch->T * Hq >= (1ll << 31) - 256)
+    return fail(MOE_ERR_UNSUPPORTED, "T * Hq = %lld", (long long)batch->T * Hq);
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status rope_frequencies(int rot, double base, int scaling, double factor, double original,
+                            double low, double high, double* freq, double* mscale) {
+  if (rot < 2 || rot % 2) return fail(MOE_ERR_INVALID_ARG, "rot=%d", rot);
+  if (!freq || !mscale) return fail(MOE_ERR_INVALID_ARG, "NULL output");
+  if (!(base > 0) || !std::isfinite(base)) return fail(MOE_ERR_INVALID_ARG, "base must be positive");
+  if (scaling < ROPE_SCALE_NONE || scaling > ROPE_SCALE_BANDED)
+    return fail(MOE_ERR_INVALID_ARG, "scaling %d", scaling);
+  if (scaling != ROPE_SCALE_NONE && (!(factor > 0) || !std::isfinite(factor)))
+    return fail(MOE_ERR_INVALID_ARG, "factor must be positive");
+  if (scaling == ROPE_SCALE_NTK && rot < 4)
+    return fail(MOE_ERR_INVALID_ARG, "this scaling needs rot > 2");
+  const bool band = scaling == ROPE_SCALE_YARN || scaling == ROPE_SCALE_BANDED;
+  if (band && (!(original > 0) || !(low > 0) || !(high > low) || !std::isfinite(original) ||
+               !std::isfinite(high)))
+    return fail(MOE_ERR_INVALID_ARG, "original, low and high must be positive with low < high");
+  if (scaling == ROPE_SCALE_YARN && base == 1.0)
+    return fail(MOE_ERR_INVALID_ARG, "base 1 has no ramp");
+  const double two_pi = 6.283185307179586476925;
+  const int r = rot / 2;
+  *mscale = 1.0;
+  if (scaling == ROPE_SCALE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+  // the (fractional) pair that turns `t` times within `original` positions
+  auto pair_of = [&](double t) {
+    return rot * std::log(original / (t * two_pi)) / (2 * std::log(base));
+  };
+  double lo = 0, hi = 1;
+  if (scaling == ROPE_SCALE_YARN) {
+    lo = std::fmax(std::floor(pair_of(high)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(low)), (double)rot - 1);
+    if (hi - lo < 1e-3) hi = lo + 1e-3;
+    if (factor > 1) *mscale = 0.1 * std::log(factor) + 1.0;
+  }
+  for (int i = 0; i < r; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == ROPE_SCALE_YARN) {
+      const double ramp = std::fmin(std::fmax((i - lo) / (hi - lo), 0.0), 1.0);
+      f = f / factor * ramp + f * (1 - ramp);
+    }
+    if (scaling == ROPE_SCALE_BANDED) {
+      const double turns = original * f / two_pi;
+      const double s = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
+      f = f * (s + (1 - s) / factor);
+    }
+    freq[i] = f;
+  }
+  return MOE_OK;
+}
+
+moe_status rope(const void* x, void* out, int dtype, int T, int H, int D, int64_t x_ts,
+                int64_t x_hs, int64_t o_ts, int64_t o_hs, const int32_t* pos, const double* freq,
+                int r, float mscale, int interleaved, int inverse, void* stream) {
+  if (dtype != PAGED_BF16 && dtype != PAGED_F16 && dtype != PAGED_F32)
+    return fail(MOE_ERR_INVALID_ARG, "dtype %d", dtype);
+  if (T < 0 || H < 1 || D < 1) return fail(MOE_ERR_INVALID_ARG, "bad size (T=%d H=%d D=%d)", T, H, D);
+  moe_status s = check_rope(D, freq, r, mscale);
+  if (s != MOE_OK) return s;
+  if (T == 0) return MOE_OK;
+  if (!x || !out || !pos) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  const size_t es = dtype == PAGED_F32 ? 4 : 2;
+  if (!aligned(x, es) || !aligned(out, es) || !aligned(pos, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (x == out && (x_ts != o_ts || x_hs != o_hs))
+    return fail(MOE_ERR_INVALID_ARG, "in place with other strides");
+  if ((long long)H * D > (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "H * D above 2^24");
+  RopeParams p{};
+  p.x = x;
+  p.out = out;
+  p.T = T;
+  p.H = H;
+  p.D = D;
+  p.x_ts = x_ts;
+  p.x_hs = x_hs;
+  p.o_ts = o_ts;
+  p.o_hs = o_hs;
+  p.pos = pos;
+  p.freq = freq;
+  p.r = r;
+  p.mscale = mscale;
+  p.sign = inverse ? -1.f : 1.f;
+  p.interleaved = interleaved != 0;
+  p.in_place = x == out;
+  PAGED_CK(launch_rope(p, dtype, false, static_cast<cudaStream_t>(stream)), "rope launch");
+  return MOE_OK;
+}
+
+moe_status rope_append(const void* q, int64_t q_ts, void* q_out, int Hq, const void* k,
+                       int64_t k_ts, const void* v, int64_t v_ts, const paged_cache* cache,
+                       const paged_batch* batch, const double* freq, int r, float mscale,
+                       int interleaved, void* stream) {
+  RopeParams p{};
+  moe_status s = check_cache(cache, &p.c);
+  if (s != MOE_OK) return s;
+  s = check_batch(batch, cache->page, &p.b);
+  if (s != MOE_OK) return s;
+  if (Hq < 1) return fail(MOE_ERR_INVALID_ARG, "Hq=%d", Hq);
+  s = check_rope(cache->dim, freq, r, mscale);
+  if (s != MOE_OK) return s;
+  if (batch->T == 0 || batch->N == 0) return MOE_OK;
+  if (!q || !q_out || !k || !v) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  if (!aligned(q, 2) || !aligned(q_out, 2) || !aligned(k, 2) || !aligned(v, 2))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if ((long long)(Hq + 2 * cache->heads) * cache->dim > (1 << 24))
+    return fail(MOE_ERR_UNSUPPORTED, "heads * dim above 2^24");
+  const long long D = cache->dim;
+  if (q == q_out && q_ts != Hq * D)
+    return fail(MOE_ERR_INVALID_ARG, "q in place must be dense");
+  p.x = q;
+  p.out = q_out;
+  p.T = batch->T;
+  p.H = Hq;
+  p.D = (int)D;
+  p.x_ts = q_ts;
+  p.x_hs = D;
+  p.o_ts = Hq * D;
+  p.o_hs = D;
+  p.freq = freq;
+  p.r = r;
+  p.mscale = mscale;
+  p.sign = 1.f;
+  p.interleaved = interleaved != 0;
+  p.in_place = q == q_out;
+  p.k = k;
+  p.v = v;
+  p.k_ts = k_ts;
+  p.v_ts = v_ts;
+  p.err = paged_error_word();
+  if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
+  PAGED_CK(launch_rope(p, cache->dtype, true, static_cast<cudaStream_t>(stream)),
+           "rope_append launch");
+  return MOE_OK;
+}
+
+moe_status paged_attention_workspace(const paged_cache* cache, const paged_batch* batch, int Hq,
+                                     int window, int max_q, int max_kv, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  CacheView c;
+  BatchView b;
+  moe_status s = check_attention(cache, batch, Hq, window, max_q, max_kv, &c, &b);
+  if (s != MOE_OK) return s;
+  *bytes = plan(c, b, Hq, window, max_q, max_kv).ws;
+  return MOE_OK;
+}
+
+moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
+                           const paged_cache* cache, const paged_batch* batch, float scale,
+                           int causal, int window, int max_q, int max_kv, void* o, int64_t o_ts,
+                           int64_t o_hs, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  AttnParams p{};
+  moe_status s = check_attention(cache, batch, Hq, window, max_q, max_kv, &p.c, &p.b);
+  if (s != MOE_OK) return s;
+  if (!(scale > 0) || !std::isfinite(scale))
+    return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (batch->T == 0 || batch->N == 0) return MOE_OK;
+  if (!q || !o) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (q_ts % 8 || q_hs % 8 || o_ts % 8 || o_hs % 8 || q_ts < 0 || q_hs < 0 || o_ts < 0 || o_hs < 0)
+    return fail(MOE_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  const Plan r = plan(p.c, p.b, Hq, window, max_q, max_kv);
+  if (r.ws > 0 && (!workspace || workspace_bytes < r.ws))
+    return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, r.ws);
+  if ((long long)p.b.N * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "too many row tiles");
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.q_ts = q_ts;
+  p.q_hs = q_hs;
+  p.o_ts = o_ts;
+  p.o_hs = o_hs;
+  p.Hq = Hq;
+  p.G = Hq / cache->heads;
+  p.divG = make_fastdiv(p.G);
+  p.scale_log2 = scale * 1.44269504088896340736f;
+  p.causal = causal != 0;
+  p.window = window;
+  p.tiles = r.tiles;
+  p.chunks = r.chunks;
+  p.chunk = r.chunk;
+  if (r.chunks > 1) {
+    p.part_ml = static_cast<float2*>(workspace);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                        ((size_t)p.b.T * Hq * r.chunks * 8 + 255) / 256 * 256);
+  }
+  p.err = paged_error_word();
+  if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == PAGED_BF16;
+  PAGED_CK(launch_paged_rows(p, bf, st), "paged_attention launch");
+  if (r.chunks > 1) PAGED_CK(launch_paged_join(p, bf, st), "paged_attention join launch");
+  return MOE_OK;
+}
+
+static moe_status check_pages(const int32_t* refs, int P, const int32_t* table, int64_t ts,
+                              int width, const int32_t* lens, int S) {
+  if (P < 1 || S < 0 || width < 0 || ts < 0)
+    return fail(MOE_ERR_INVALID_ARG, "bad size (P=%d S=%d width=%d)", P, S, width);
+  if ((long long)S * width >= (1ll << 31) || P > (1 << 30))
+    return fail(MOE_ERR_UNSUPPORTED, "S * width = %lld, P = %d", (long long)S * width, P);
+  if (!refs || (S > 0 && (!lens || (width > 0 && !table))))
+    return fail(MOE_ERR_INVALID_ARG, "NULL state array");
+  if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned state array");
+  if (S > 1 && ts < width) return fail(MOE_ERR_INVALID_ARG, "rows of the table overlap");
+  return MOE_OK;
+}
+
+moe_status pages_fork(int32_t* refs, int P, int32_t* table, int64_t ts, int width, int32_t* lens,
+                      int S, const int32_t* src, const int32_t* dst, int F, int32_t* refused,
+                      void* stream) {
+  moe_status s = check_pages(refs, P, table, ts, width, lens, S);
+  if (s != MOE_OK) return s;
+  if (F < 0) return fail(MOE_ERR_INVALID_ARG, "F=%d", F);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!aligned(refused, 4)) return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (F > 0 && (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)))
+    return fail(MOE_ERR_INVALID_ARG, "src or dst NULL or misaligned");
+  if (refused) PAGED_CK(cudaMemsetAsync(refused, 0, 4, st), "clear");
+  if (F == 0) return MOE_OK;
+  PAGED_CK(launch_pages_fork(refs, P, table, ts, width, lens, S, src, dst, F, refused, st),
+           "pages_fork launch");
+  return MOE_OK;
+}
+
+moe_status pages_reserve(int32_t* refs, int P, int32_t* table, int64_t ts, int width,
+                         int32_t* lens, const int32_t* add, int S, int page, int32_t* moves,
+                         int32_t* status, int32_t* scratch, void* stream) {
+  moe_status s = check_pages(refs, P, table, ts, width, lens, S);
+  if (s != MOE_OK) return s;
+  if (page < 1) return fail(MOE_ERR_INVALID_ARG, "page=%d", page);
+  if (!status || !scratch || (S > 0 && (!add || !moves)))
+    return fail(MOE_ERR_INVALID_ARG, "NULL array");
+  if (!aligned(add, 4) || !aligned(moves, 4) || !aligned(status, 4) || !aligned(scratch, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned array");
+  PAGED_CK(launch_pages_reserve(refs, P, table, ts, width, lens, add, S, page, moves, status,
+                                scratch, static_cast<cudaStream_t>(stream)),
+           "pages_reserve launch");
+  return MOE_OK;
+}
+
+moe_status pages_free(int32_t* refs, int P, int32_t* table, int64_t ts, int width, int32_t* lens,
+                      int S, const int32_t* slots, int F, void* stream) {
+  moe_status s = check_pages(refs, P, table, ts, width, lens, S);
+  if (s != MOE_OK) return s;
+  if (F < 0) return fail(MOE_ERR_INVALID_ARG, "F=%d", F);
+  if (F == 0) return MOE_OK;
+  if (!slots || !aligned(slots, 4)) return fail(MOE_ERR_INVALID_ARG, "slots NULL or misaligned");
+  PAGED_CK(launch_pages_free(refs, P, table, ts, width, lens, S, slots, F,
+                             static_cast<cudaStream_t>(stream)),
+           "pages_free launch");
+  return MOE_OK;
+}
+
+moe_status pages_compact(int32_t* refs, int P, int32_t* table, int64_t ts, int width, int S,
+                         int32_t* moves, int32_t* count, int32_t* scratch, void* stream) {
+  moe_status s = check_pages(refs, P, table, ts, width, refs, S);
+  if (s != MOE_OK) return s;
+  if (!moves || !count || !scratch) return fail(MOE_ERR_INVALID_ARG, "NULL array");
+  if (!aligned(moves, 4) || !aligned(count, 4) || !aligned(scratch, 4))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned array");
+  PAGED_CK(launch_pages_compact(refs, P, table, ts, width, S, moves, count, scratch,
+                                static_cast<cudaStream_t>(stream)),
+           "pages_compact launch");
+  return MOE_OK;
+}
+
+moe_status pages_copy(void* pools, int B, int64_t pool_stride, int P, int64_t page_stride,
+                      int64_t page_bytes, const int32_t* moves, int M, const int32_t* count,
+                      void* stream) {
+  if (B < 0 || P < 1 || M < 0 || page_bytes < 0 || pool_stride < 0 || page_stride < 0)
+    return fail(MOE_ERR_INVALID_ARG, "bad size (B=%d P=%d M=%d)", B, P, M);
+  if (page_bytes % 16 || pool_stride % 16 || page_stride % 16 || !aligned(pools, 16))
+    return fail(MOE_ERR_INVALID_ARG, "pools, strides and page bytes must be multiples of 16 bytes");
+  if (P > 1 && page_stride < page_bytes) return fail(MOE_ERR_INVALID_ARG, "pages overlap");
+  if (page_bytes > (1ll << 32)) return fail(MOE_ERR_UNSUPPORTED, "page of %lld bytes", (long long)page_bytes);
+  if (B == 0 || M == 0 || page_bytes == 0) return MOE_OK;
+  if (!pools || !moves || !aligned(moves, 4) || !aligned(count, 4))
+    return fail(MOE_ERR_INVALID_ARG, "NULL or misaligned pointer");
+  PAGED_CK(launch_pages_copy(static_cast<uint8_t*>(pools), B, pool_stride, P, page_stride,
+                             page_bytes, moves, M, count, static_cast<cudaStream_t>(stream)),
+           "pages_copy launch");
+  return MOE_OK;
+}
+
+moe_status paged_get_device_error(void* stream, int* code) {
+  if (!code) return fail(MOE_ERR_INVALID_ARG, "code is NULL");
+  int* w = paged_error_word();
+  if (!w) return fail(MOE_ERR_CUDA, "no CUDA device");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int v = 0;
+  PAGED_CK(cudaMemcpyAsync(&v, w, 4, cudaMemcpyDeviceToHost, st), "read error word");
+  PAGED_CK(cudaMemsetAsync(w, 0, 4, st), "clear error word");
+  PAGED_CK(cudaStreamSynchronize(st), "synchronise");
+  *code = v;
+  return v ? MOE_ERR_DEVICE : MOE_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,153 @@
+// Internal structures of the paged-cache operators (include/paged.h).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "moe_internal.h"
+#include "paged.h"
+
+namespace moe {
+
+// n / d for 0 <= n < 2^31 by one multiplication: mul = ceil(2^(31+s) / d) with
+// 2^s >= d, whose excess over the exact reciprocal stays below one part in
+// 2^31 of a unit.
+struct FastDiv {
+  uint32_t mul = 0;
+  int shift = 0;
+  int d = 1;
+};
+inline FastDiv make_fastdiv(int d) {
+  FastDiv f;
+  f.d = d;
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  f.shift = 31 + s;
+  f.mul = (uint32_t)(((1ull << f.shift) + (uint64_t)d - 1) / (uint64_t)d);
+  return f;
+}
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) {
+  return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.shift);
+}
+
+struct CacheView {
+  uint16_t* k;
+  uint16_t* v;
+  int pages, page, heads, dim;
+  long long page_stride, row_stride, head_stride;
+  FastDiv div;  // by page
+};
+
+struct BatchView {
+  const int32_t* table;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  int N, T, width;
+  long long table_stride;
+  int capacity;  // min(width * page, 2^31 - 1): the longest context a table row holds
+};
+
+// One sequence of a batch with its metadata made safe.
+struct Seq {
+  int t0, nq, kv;  // first new token, new tokens, context
+};
+__device__ __forceinline__ Seq load_seq(const BatchView& b, int n) {
+  Seq s;
+  const int t0 = min(max(b.cu[n], 0), b.T);
+  const int t1 = min(max(b.cu[n + 1], t0), b.T);
+  s.t0 = t0;
+  s.nq = t1 - t0;
+  s.kv = min(max(b.kv_len[n], 0), b.capacity);
+  return s;
+}
+// The sequence of new token t: the last n with cu[n] <= t (-1: none).
+__device__ __forceinline__ int find_seq(const BatchView& b, int t) {
+  int lo = -1, hi = b.N;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---- rotary positions (rope.cu)
+struct RopeParams {
+  // plain: x -> out [T][H][D]; append: x = q -> out, plus k, v -> cache
+  const void* x;
+  void* out;
+  int T, H, D;
+  long long x_ts, x_hs, o_ts, o_hs;
+  const int32_t* pos;  // plain only
+  const double* freq;
+  int r;
+  float mscale, sign;
+  bool interleaved, in_place;
+  // append
+  const void* k;
+  const void* v;
+  long long k_ts, v_ts;
+  CacheView c;
+  BatchView b;
+  int* err;
+  int tokens;  // tokens of a CTA
+};
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool append, cudaStream_t st);
+
+// ---- attention over the paged cache
+struct AttnParams {
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  long long q_ts, q_hs, o_ts, o_hs;
+  int Hq, G;       // query heads; query heads of a key/value head
+  FastDiv divG;
+  CacheView c;
+  BatchView b;
+  float scale_log2;  // scale * log2(e)
+  int causal, window;
+  // split over the keys: chunk c of a row tile covers keys [c, c+1) * chunk
+  // behind its first visible one; the last chunk goes to the end
+  int chunks, chunk;
+  int tiles;       // row tiles of a sequence the grid provides for
+  float* part_o;   // [T * Hq][chunks][D], unnormalised (chunks > 1)
+  float2* part_ml; // [T * Hq][chunks]: running maximum (log2 units) and sum
+  int* err;
+};
+// the first and one past the last key that rows [r0, r1) of a sequence see
+// (r1 > r0; row r is new token r / G)
+__device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int r0, int r1) {
+  const int p0 = s.kv - s.nq + fast_div(r0, p.divG);
+  const int p1 = s.kv - s.nq + fast_div(r1 - 1, p.divG);
+  int lo = 0, hi = s.kv;
+  if (p.causal) hi = min(hi, p1 + 1);
+  if (p.window > 0) lo = max(0, p0 - p.window + 1);
+  return make_int2(lo, max(hi, lo));
+}
+constexpr int kRowTile = 16;
+cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st);
+
+// ---- pages (pages.cu)
+cudaError_t launch_pages_fork(int32_t* refs, int P, int32_t* table, long long ts, int width,
+                              int32_t* lens, int S, const int32_t* src, const int32_t* dst, int F,
+                              int32_t* refused, cudaStream_t st);
+cudaError_t launch_pages_reserve(int32_t* refs, int P, int32_t* table, long long ts, int width,
+                                 int32_t* lens, const int32_t* add, int S, int page,
+                                 int32_t* moves, int32_t* status, int32_t* scratch,
+                                 cudaStream_t st);
+cudaError_t launch_pages_free(int32_t* refs, int P, int32_t* table, long long ts, int width,
+                              int32_t* lens, int S, const int32_t* slots, int F, cudaStream_t st);
+cudaError_t launch_pages_compact(int32_t* refs, int P, int32_t* table, long long ts, int width,
+                                 int S, int32_t* moves, int32_t* count, int32_t* scratch,
+                                 cudaStream_t st);
+cudaError_t launch_pages_copy(uint8_t* pools, int B, long long pool_stride, int P,
+                              long long page_stride, long long page_bytes, const int32_t* moves,
+                              int M, const int32_t* count, cudaStream_t st);
+
+// device address of the error word (paged_api.cu)
+int* paged_error_word();
+// multiprocessors of the current device
+int device_sms();
+
+}  // namespace moe

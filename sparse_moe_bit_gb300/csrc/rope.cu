@@ -1,0 +1,232 @@
+// Rotary positions, alone and with the write of new keys and values into the
+// paged cache (include/paged.h).
+//
+// Pair i of a head at position pos turns by theta = pos f_i.  Only theta
+// modulo one turn matters, and that is exact in integers: with F = the 64-bit
+// fraction of f_i / (2 pi) turns, the low 64 bits of pos * F are the fraction
+// of a turn reached, off by at most pos 2^-53 of the fp64 frequency's own
+// rounding -- where pos * f in fp32 is off by 0.03 rad at 2^20 positions.  Its
+// top 32 bits, as a signed number of half turns, go to sincospif.
+//
+// Bound: HBM, one read and one write of every value.  A CTA takes a few
+// tokens, computes the r angles of each once into shared memory (they serve
+// every head) and then moves 16 bytes of each side of a pair a thread and
+// step.  Vectors need r (half layout) or 2r (interleaved) a multiple of the
+// 16 bytes and aligned rows; everything else takes the same loop one pair at a
+// time.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T e[V];
+};
+
+__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
+  const float x = a * cs.x - b * cs.y;
+  const float y = a * cs.y + b * cs.x;
+  a = x;
+  b = y;
+}
+
+// One head row: features of `src` turned into `dst`; item u of the row's
+// items, V pairs (turning part) or V features (the rest) each.
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void rope_item(const T* src, T* dst, int u, int r, const float2* cs) {
+  using W = Vec<T, V>;
+  const int turns = r / V;  // items of V pairs
+  if (u < turns) {
+    if (INTER) {
+      // V pairs = 2V consecutive features, as two vectors
+      W x0 = reinterpret_cast<const W*>(src)[2 * u], x1 = reinterpret_cast<const W*>(src)[2 * u + 1];
+      T t[2 * V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) t[j] = x0.e[j], t[V + j] = x1.e[j];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float a = to_f(t[2 * j]), b = to_f(t[2 * j + 1]);
+        turn(a, b, cs[u * V + j]);
+        t[2 * j] = from_f<T>(a);
+        t[2 * j + 1] = from_f<T>(b);
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) x0.e[j] = t[j], x1.e[j] = t[V + j];
+      reinterpret_cast<W*>(dst)[2 * u] = x0;
+      reinterpret_cast<W*>(dst)[2 * u + 1] = x1;
+    } else {
+      W a = reinterpret_cast<const W*>(src)[u], b = reinterpret_cast<const W*>(src + r)[u];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float fa = to_f(a.e[j]), fb = to_f(b.e[j]);
+        turn(fa, fb, cs[u * V + j]);
+        a.e[j] = from_f<T>(fa);
+        b.e[j] = from_f<T>(fb);
+      }
+      reinterpret_cast<W*>(dst)[u] = a;
+      reinterpret_cast<W*>(dst + r)[u] = b;
+    }
+  } else {
+    const int i = (2 * r) / V + (u - turns);
+    reinterpret_cast<W*>(dst)[i] = reinterpret_cast<const W*>(src)[i];
+  }
+}
+
+struct Slot {
+  int pos;
+  int seq;         // append: -1 = outside every sequence
+  long long off;   // append: element offset of the token's row in k and v, -1 = none
+};
+
+template <typename T, int V, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  extern __shared__ float2 cs_all[];  // [tokens][r]
+  __shared__ Slot slots[32];
+  const int t0 = blockIdx.x * p.tokens;
+  const int nt = min(p.tokens, p.T - t0);
+  if (threadIdx.x < nt) {
+    Slot s;
+    const int t = t0 + threadIdx.x;
+    if (APPEND) {
+      s.off = -1;
+      s.pos = 0;
+      s.seq = find_seq(p.b, t);
+      if (s.seq >= 0) {
+        const Seq q = load_seq(p.b, s.seq);
+        if (t >= q.t0 && t < q.t0 + q.nq) {
+          s.pos = q.kv - q.nq + (t - q.t0);
+          if (s.pos >= 0) {
+            const int col = fast_div(s.pos, p.c.div);
+            const int pg = p.b.table[s.seq * p.b.table_stride + col];
+            if (pg >= 0 && pg < p.c.pages)
+              s.off = pg * p.c.page_stride + (s.pos - col * p.c.page) * p.c.row_stride;
+            else
+              atomicOr(p.err, PAGED_DEVERR_PAGE);
+          }
+        } else {
+          s.seq = -1;
+        }
+      }
+    } else {
+      s.seq = 0;
+      s.off = -1;
+      s.pos = p.pos[t];
+    }
+    slots[threadIdx.x] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.r; i += kRopeThreads) {
+    const double turns = p.freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    const double frac = turns - floor(turns);
+    const uint64_t F = __double2ull_rz(frac * 18446744073709551616.0);
+    for (int j = 0; j < nt; ++j) {
+      const uint64_t at = (uint64_t)(int64_t)slots[j].pos * F;  // modulo one turn
+      const float half = (float)(int32_t)(at >> 32) * 4.656612873077393e-10f;  // 2^-31
+      float s, c;
+      sincospif(half, &s, &c);
+      cs_all[j * p.r + i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+    }
+  }
+  __syncthreads();
+  const T* x = static_cast<const T*>(p.x);
+  T* out = static_cast<T*>(p.out);
+  const int rot_items = p.r / V;
+  const int all_items = rot_items + (p.D - 2 * p.r) / V;
+  const int q_items = (p.in_place ? rot_items : all_items);  // of a query row
+  const int v_items = APPEND ? p.D / V : 0;
+  const int heads = APPEND ? p.c.heads : 0;
+  const int per_q = p.H * q_items, per_k = heads * all_items, per_v = heads * v_items;
+  const int per_tok = per_q + per_k + per_v;
+  for (int w = threadIdx.x; w < nt * per_tok; w += kRopeThreads) {
+    const int j = w / per_tok;
+    int u = w - j * per_tok;
+    const Slot s = slots[j];
+    const long long t = t0 + j;
+    const float2* cs = cs_all + j * p.r;
+    if (APPEND && s.seq < 0) continue;
+    if (u < per_q) {
+      const int h = u / q_items;
+      rope_item<T, V, INTER>(x + t * p.x_ts + h * p.x_hs, out + t * p.o_ts + h * p.o_hs,
+                             u - h * q_items, p.r, cs);
+    } else if constexpr (APPEND) {
+      if (s.off < 0) continue;
+      u -= per_q;
+      if (u < per_k) {
+        const int h = u / all_items;
+        rope_item<T, V, INTER>(static_cast<const T*>(p.k) + t * p.k_ts + (long long)h * p.D,
+                               reinterpret_cast<T*>(p.c.k) + s.off + h * p.c.head_stride,
+                               u - h * all_items, p.r, cs);
+      } else {
+        u -= per_k;
+        const int h = u / v_items, i = u - h * v_items;
+        using W = Vec<T, V>;
+        const T* src = static_cast<const T*>(p.v) + t * p.v_ts + (long long)h * p.D;
+        T* dst = reinterpret_cast<T*>(p.c.v) + s.off + h * p.c.head_stride;
+        reinterpret_cast<W*>(dst)[i] = reinterpret_cast<const W*>(src)[i];
+      }
+    }
+  }
+}
+
+template <typename T, int V>
+cudaError_t launch_t(const RopeParams& p, bool append, cudaStream_t st) {
+  const int grid = (p.T + p.tokens - 1) / p.tokens;
+  const size_t smem = (size_t)p.tokens * p.r * sizeof(float2);
+  void (*k)(RopeParams);
+  if constexpr (sizeof(T) == 2)
+    k = p.interleaved ? (append ? rope_kernel<T, V, true, true> : rope_kernel<T, V, true, false>)
+                      : (append ? rope_kernel<T, V, false, true> : rope_kernel<T, V, false, false>);
+  else
+    k = p.interleaved ? rope_kernel<T, V, true, false> : rope_kernel<T, V, false, false>;
+  return launch_kernel(k, dim3(grid), dim3(kRopeThreads), smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p0, int dtype, bool append, cudaStream_t st) {
+  RopeParams p = p0;
+  const int es = dtype == PAGED_F32 ? 4 : 2;
+  const int V = 16 / es;
+  // 16-byte vectors: whole vectors in each of the row's parts, aligned rows
+  auto al = [&](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  bool vec = p.r % V == 0 && (p.D - 2 * p.r) % V == 0 && al(p.x) && al(p.out) && p.x_ts % V == 0 &&
+             p.x_hs % V == 0 && p.o_ts % V == 0 && p.o_hs % V == 0;
+  if (append) vec = vec && al(p.k) && al(p.v) && p.k_ts % V == 0 && p.v_ts % V == 0;
+  // tokens of a CTA: one while the CTAs do not fill the machine eight deep
+  // (a small call is over in one token's time), then up to eight, so that the
+  // angles' fp64 conversion and the slot lookup are paid once for several
+  const int sms = device_sms();
+  p.tokens = p.T / (sms * 8);
+  p.tokens = p.tokens < 1 ? 1 : (p.tokens > 8 ? 8 : p.tokens);
+  if (dtype == PAGED_F32)
+    return vec ? launch_t<float, 4>(p, false, st) : launch_t<float, 1>(p, false, st);
+  if (dtype == PAGED_BF16)
+    return vec ? launch_t<__nv_bfloat16, 8>(p, append, st)
+               : launch_t<__nv_bfloat16, 1>(p, append, st);
+  return vec ? launch_t<__half, 8>(p, append, st) : launch_t<__half, 1>(p, append, st);
+}
+
+}  // namespace moe
