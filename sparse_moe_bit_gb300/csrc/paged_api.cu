@@ -109,42 +109,58 @@ moe_status check_rope(int D, const double* freq, int r, float mscale) {
 
 // Choice of kernel and split for one call; see plan().
 struct Plan {
+  bool wide;  // 256-row tiles on the tensor cores, else 16-row tiles
   int tiles, chunks, chunk;
   size_t ws;
 };
 
-// Rows path: 16-row tiles.  Enough chunks that the work items make three
-// waves of the CTAs an SM holds (one of head dim 256, two of 128, three of
-// 64), which evens out ragged contexts; no chunk below 256 keys, where a
-// CTA's start and the join cost more than they spread.
+// 16-row tiles while one holds the longest chunk's rows (each tile reads the
+// keys again), 256-row tiles above.
+//
+// 16-row tiles: enough chunks that the work items make three waves of the CTAs
+// an SM holds (one of head dim 256, two of 128, three of 64), which evens out
+// ragged contexts; no chunk below 256 keys, where a CTA's start and the join
+// cost more than they spread.
+// 256-row tiles: chunks only while the pairs of CTAs leave SMs without work;
+// none below 512 keys.
 Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv) {
   Plan r;
   const int G = Hq / c.heads;
-  const long long per = b.N > 0 ? (b.T + b.N - 1) / b.N : 0;
-  long long mq = max_q > 0 ? max_q : per;
+  long long mq = max_q > 0 ? max_q : b.T;
   if (mq > b.T) mq = b.T;
   long long kv = max_kv > 0 ? max_kv : b.capacity;
   if (kv > b.capacity) kv = b.capacity;
-  long long tiles = (mq * G + kRowTile - 1) / kRowTile;
-  if (tiles < 1) tiles = 1;
+  r.wide = mq * G > kRowTile;
+  const long long rows = r.wide ? kPairRows : kRowTile;
   long long span = kv;
-  if (window > 0 && (long long)window + kRowTile < span) span = (long long)window + kRowTile;
-  const long long items = (long long)b.N * tiles * c.heads;
-  const int occ = c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3);
-  const long long target = 3ll * occ * device_sms();
+  if (window > 0 && window + rows < span) span = window + rows;
+  long long tiles, items, target, least, step;
+  if (r.wide) {
+    tiles = ((long long)b.T * G + rows - 1) / rows + (b.N < b.T ? b.N : b.T);
+    if (b.N == 1) --tiles;
+    items = tiles * c.heads;
+    target = device_sms() / 2;
+    least = 512;
+    step = 128;
+  } else {
+    tiles = (mq * G + rows - 1) / rows;
+    items = (long long)b.N * tiles * c.heads;
+    target = 3ll * (c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3)) * device_sms();
+    least = 256;
+    step = 64;
+  }
   long long chunks = items > 0 ? target / items : 1;
   if (chunks < 1) chunks = 1;
   long long chunk = (span + chunks - 1) / chunks;
-  chunk = (chunk + 63) / 64 * 64;
-  if (chunk < 256) chunk = 256;
+  chunk = (chunk + step - 1) / step * step;
+  if (chunk < least) chunk = least;
   chunks = (span + chunk - 1) / chunk;
   if (chunks < 1) chunks = 1;
-  r.tiles = (int)tiles;
+  r.tiles = (int)(tiles < 1 ? 1 : tiles);
   r.chunk = (int)chunk;
   r.chunks = (int)chunks;
-  r.ws = r.chunks > 1
-             ? (((size_t)b.T * Hq * r.chunks * 8 + 255) / 256 * 256 + (size_t)b.T * Hq * r.chunks * c.dim * 4)
-             : 0;
+  const size_t parts = (size_t)b.T * Hq * r.chunks;
+  r.ws = r.chunks > 1 ? (parts * 8 + 255) / 256 * 256 + parts * c.dim * 4 : 0;
   return r;
 }
 
@@ -330,7 +346,7 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
   const Plan r = plan(p.c, p.b, Hq, window, max_q, max_kv);
   if (r.ws > 0 && (!workspace || workspace_bytes < r.ws))
     return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, r.ws);
-  if ((long long)p.b.N * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
+  if ((r.wide ? 2ll : (long long)p.b.N) * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
     return fail(MOE_ERR_UNSUPPORTED, "too many row tiles");
   p.q = static_cast<const uint16_t*>(q);
   p.o = static_cast<uint16_t*>(o);
@@ -357,7 +373,8 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
   if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == PAGED_BF16;
-  PAGED_CK(launch_paged_rows(p, bf, st), "paged_attention launch");
+  PAGED_CK(r.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
+           "paged_attention launch");
   if (r.chunks > 1) PAGED_CK(launch_paged_join(p, bf, st), "paged_attention join launch");
   return MOE_OK;
 }

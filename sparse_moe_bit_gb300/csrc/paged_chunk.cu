@@ -1,0 +1,637 @@
+// Attention of many query rows over the paged cache on the tensor cores
+// (include/paged.h): chunks of new tokens, from a few tokens of a wide head
+// group to whole prompts.
+//
+// A pair of CTAs (a cluster of two, tcgen05 cta_group::2) takes 256 rows -- row
+// r is token r / G, head r % G of the G query heads on one key/value head --
+// and walks its visible keys in tiles of 128, with the running softmax of
+//   S = Q K^T, m' = max(m, rowmax S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
+//   O = O 2^(m - m') + P V        (S in log2 units; S, m, l, O fp32)
+// Each CTA holds 128 of the rows: its Q in shared memory, its O (D columns)
+// and two S buffers (128 columns each) in TMEM, all 512 columns at D = 256.
+// The pair shares the operands: of a tile each CTA loads 64 keys (half of B's
+// columns in Q K^T) and half of every value's features (half of B's columns in
+// P V), so that a byte of the cache enters one SM for 256 rows.  P goes back to
+// TMEM over the S it came from (16-bit, the MMA's A operand); V is read from
+// shared memory as it lies in the cache, [key][feature] (the "MN-major" form).
+//
+// Bound: the tensor cores (4 D operations per row and key).  Their two products
+// of tile j and the softmax of tile j + 1 overlap: the order of issue is
+// QK(0), QK(1), PV(0), QK(2), PV(1), ...  Eight warps run the softmax, a thread
+// half a row (64 keys) -- a row's two threads exchange their maxima through
+// shared memory -- and the reference maximum only moves when it rises by more
+// than 2^8 (weights then stay below 2^8, which fp32 sums and 16-bit weights
+// carry without loss), so that O in TMEM is hardly ever rescaled.
+//
+// Warps: 0 copies keys, 2 copies values (16-byte asynchronous copies into the
+// swizzled operand layout, rows of a page gathered by the page table; rows
+// behind the end or with a bad page number are not read but zero), 1 issues
+// the MMAs (the even CTA's), 4..11 softmax, correction and epilogue.  Every
+// wait is bounded.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged_internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSoftWarp0 = 4, kSoftWarps = 8;
+constexpr int kTileKeys = 128;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kRise = 8.f;  // log2 units the maximum may lag behind
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int STAGE = 128 * D;  // 64 keys, or half the features of 128 values
+  static constexpr int NST = D == 256 ? 2 : (D == 128 ? 3 : 4);  // stages of K and of V
+  static constexpr int OFF_K = Q_BYTES;
+  static constexpr int OFF_V = OFF_K + NST * STAGE;
+  static constexpr int OFF_BAR = OFF_V + NST * STAGE;
+  static constexpr int NUM_BARS = 1 + 4 * NST + 2 + 2 + 2;
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
+  static constexpr int OFF_MAX = (OFF_MISC + 64 + 15) / 16 * 16;  // float [2][128], double-buffered
+  // never two CTAs on an SM: each takes all of TMEM, and two pairs that held one
+  // SM each would wait for one another
+  static constexpr int SMEM =
+      OFF_MAX + 2 * 2 * 128 * 4 + 1024 > 120000 ? OFF_MAX + 2 * 2 * 128 * 4 + 1024 : 120000;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static constexpr int S_COL = 256;  // TMEM: O at 0, S buffers at 256 and 384
+};
+
+template <int D>
+struct Bars {
+  using C = ChunkCfg<D>;
+  uint32_t base;
+  __device__ uint32_t q_full() const { return base; }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (1 + s); }
+  __device__ uint32_t k_empty(int s) const { return base + 8 * (1 + C::NST + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (1 + 2 * C::NST + s); }
+  __device__ uint32_t v_empty(int s) const { return base + 8 * (1 + 3 * C::NST + s); }
+  __device__ uint32_t s_full(int b) const { return base + 8 * (1 + 4 * C::NST + b); }
+  __device__ uint32_t p_full(int b) const { return base + 8 * (3 + 4 * C::NST + b); }
+  __device__ uint32_t pv_done() const { return base + 8 * (5 + 4 * C::NST); }
+  __device__ uint32_t drain() const { return base + 8 * (6 + 4 * C::NST); }
+};
+
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+// Arrive on an mbarrier of any CTA of the cluster, releasing this thread's
+// writes to the cluster.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+// The whole warp waits; false when the limit has passed or another wait of the
+// CTA has given up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int* err) {
+  bool ok = try_wait_cluster(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    ok = ok || try_wait_cluster(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    int bail = 0;
+    if ((threadIdx.x & 31) == 0) bail = (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs);
+    if (__shfl_sync(0xffffffffu, bail, 0)) {
+      if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        atomicOr(err, PAGED_DEVERR_WAIT_TIMEOUT);
+      }
+      return false;
+    }
+  }
+}
+
+// D (+)= A[smem] * B[smem]^T over the pair, M = 256 (warp-wide form)
+__device__ __forceinline__ void tc_mma_ss_pair_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of a B tile stored [K][N] with N contiguous: rows (one K each) of
+// `row` bytes, 128 (swizzle over 8 rows of 128 bytes) or 64 (over 8 rows of 64
+// bytes).  Stride offset: 8 rows; leading offset: from one row's width of N to
+// the next.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, int row, int lead) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(row * 8 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)(row == 128 ? 2 : 4) << 61);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void pair_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// the two warps that share the rows of one TMEM lane quarter
+__device__ __forceinline__ void quarter_sync(int q) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+}
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int sh_find[4], sh_scan[kThreads / 32];
+  const uint32_t sm = smem_u32(smem);
+  const Bars<D> B{sm + C::OFF_BAR};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  int bid = blockIdx.x >> 1;
+  const int ck = bid % p.chunks;
+  bid /= p.chunks;
+  const int h = bid % p.c.heads;
+  const int want = bid / p.c.heads;  // the want-th row tile of the batch
+
+  // ---- which sequence's which tile: running sum of the sequences' tile counts
+  if (threadIdx.x == 0) sh_find[0] = -1;
+  int before = 0;
+  for (int n0 = 0; n0 < p.b.N; n0 += kThreads) {
+    const int n = n0 + threadIdx.x;
+    const int nt = n < p.b.N ? (load_seq(p.b, n).nq * p.G + 255) / 256 : 0;
+    int inc = nt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    __syncthreads();  // sh_scan of the step before is read
+    if (lane == 31) sh_scan[warp] = inc;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) inc += sh_scan[w];
+      total += sh_scan[w];
+    }
+    inc += before;
+    if (want < inc && want >= inc - nt) {
+      sh_find[0] = n;
+      sh_find[1] = nt - 1 - (want - (inc - nt));  // last tile first: it sees the most keys
+    }
+    before += total;
+    if (want < before) break;  // uniform
+  }
+  __syncthreads();
+  const int n = sh_find[0];
+  if (n < 0) return;  // uniform over the pair: both CTAs look for the same tile
+  const int tile = sh_find[1];
+  const Seq s = load_seq(p.b, n);
+  const int rows = s.nq * p.G;
+  const int r0 = tile * 256, r1 = min(r0 + 256, rows);
+  const int2 kr = key_range(p, s, r0, r1);
+  const int span = kr.y - kr.x;
+  const long long c0 = (long long)ck * p.chunk;
+  const int lo = kr.x + (int)min(c0, (long long)span);
+  const int hi = ck == p.chunks - 1 ? kr.y : kr.x + (int)min(c0 + p.chunk, (long long)span);
+  const int nb = (hi - lo + kTileKeys - 1) / kTileKeys;
+  const int32_t* table = p.b.table + n * p.b.table_stride;
+
+  // this thread's row in the softmax warps (the other warps: unused)
+  const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2;
+  const int trow = quarter * 32 + lane;
+  const int row = r0 + rank * 128 + trow;
+  const bool valid = row < r1;
+  const int tok = valid ? fast_div(row, p.divG) : 0;
+  const int head = h * p.G + (valid ? row - tok * p.G : 0);
+  const long long rid = (long long)(s.t0 + tok) * p.Hq + head;
+
+  if (nb == 0) {  // nothing to see in this chunk (uniform over the pair)
+    if (warp >= kSoftWarp0 && valid) {
+      const int f0 = half * (D / 2);
+      if (p.chunks > 1) {
+        if (half == 0) p.part_ml[rid * p.chunks + ck] = make_float2(kNegInf, 0.f);
+      } else {
+        uint16_t* o = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f0;
+        for (int f = 0; f < D / 2; f += 8) *reinterpret_cast<uint4*>(o + f) = make_uint4(0, 0, 0, 0);
+        if (half == 0 && p.lse) p.lse[rid] = kNegInf;
+      }
+    }
+    return;
+  }
+
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  if (threadIdx.x == 0) {
+    mbar_init(B.q_full(), 2 * kSoftWarps);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(B.k_full(i), 2);
+      mbar_init(B.k_empty(i), 1);
+      mbar_init(B.v_full(i), 2);
+      mbar_init(B.v_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.s_full(i), 1);
+      mbar_init(B.p_full(i), 2 * kSoftWarps);
+    }
+    mbar_init(B.pv_done(), 1);
+    mbar_init(B.drain(), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  // page numbers of this chunk that are bad (then every score is looked at)
+  int bad = 0;
+  for (int c = fast_div(lo, p.c.div) + threadIdx.x; c <= fast_div(hi - 1, p.c.div); c += kThreads) {
+    const int pg = table[c];
+    if (pg < 0 || pg >= p.c.pages) bad = 1;
+  }
+  tc_fence_before();
+  const bool any_bad = __syncthreads_or(bad);
+  if (any_bad && threadIdx.x == 0) atomicOr(p.err, PAGED_DEVERR_PAGE);
+  pair_sync_all();  // the other CTA's barriers are there before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // element offset of key `key`'s row in the cache, -1: none
+  auto lookup = [&](int key) -> long long {
+    if (key >= hi) return -1;
+    const int col = fast_div(key, p.c.div);
+    const int pg = table[col];
+    if (pg < 0 || pg >= p.c.pages) return -1;
+    return pg * p.c.page_stride + (key - col * p.c.page) * p.c.row_stride;
+  };
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------ keys (0) and values (2)
+    const bool is_k = warp == 0;
+    constexpr int KEYS_K = 64, KEYS_V = 128;
+    const uint32_t full0 = mapa_shared(is_k ? B.k_full(0) : B.v_full(0), 0);
+    const uint32_t ring = sm + (is_k ? C::OFF_K : C::OFF_V);
+    const uint16_t* base = is_k ? p.c.k + h * p.c.head_stride
+                                : p.c.v + h * p.c.head_stride + rank * (D / 2);
+    long long off[4];
+    auto look = [&](int j) {
+      const int k0 = lo + j * kTileKeys + (is_k ? rank * KEYS_K : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        off[i] = (j < nb && (!is_k || i < 2)) ? lookup(k0 + 32 * i + lane) : -1;
+    };
+    look(0);
+    int told = 0;  // stages announced
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      const int st = j % C::NST;
+      const uint32_t empty = is_k ? B.k_empty(st) : B.v_empty(st);
+      const uint32_t par = ((j / C::NST) & 1) ^ 1;
+      // a stage that is not free yet: what was copied is announced first
+      if (!__all_sync(0xffffffffu, mbar_try_wait(empty, par)) && told < j) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (; told < j; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
+        told = j;
+      }
+      if (!warp_wait(empty, par, abort_flag, p.err)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = ring + st * C::STAGE;
+      if (is_k) {
+        constexpr int CH = D / 8;        // 16-byte pieces of a key
+        constexpr int RPI = 32 / CH;     // keys a warp copies at once
+#pragma unroll
+        for (int i = 0; i < KEYS_K / RPI; ++i) {
+          const int r = i * RPI + lane / CH, c = lane % CH;
+          const long long o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
+          cp_async16(dst + (c >> 3) * (KEYS_K * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
+        }
+      } else {
+        constexpr int CH = D / 16;       // 16-byte pieces of half a value
+        constexpr int RPI = 32 / CH;
+#pragma unroll
+        for (int i = 0; i < KEYS_V / RPI; ++i) {
+          const int r = i * RPI + lane / CH, c = lane % CH;
+          const long long o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
+          const uint32_t at = D == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                      : (c >> 3) * (KEYS_V * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          cp_async16(dst + at, base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
+        }
+      }
+      cp_async_commit();
+      look(j + 1);
+      if (told < j) {  // the stage before this one (older ones are announced)
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (; told < j; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
+        told = j;
+      }
+    }
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (ok && lane == 0)
+      for (; told < nb; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      const uint32_t id_qk = idesc_f16(256, kTileKeys, BF ? 1 : 0);
+      const uint32_t id_pv = idesc_f16(256, D, BF ? 1 : 0) | (1u << 16);  // B: N contiguous
+      auto qk = [&](int j) -> bool {
+        const int st = j % C::NST;
+        if (!warp_wait(B.k_full(st), (j / C::NST) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + C::S_COL + (j & 1) * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t a = sdesc_k_sw128(sm + (kk >> 2) * (128 * 128)) + 2 * (kk & 3);
+          const uint64_t b =
+              sdesc_k_sw128(sm + C::OFF_K + st * C::STAGE + (kk >> 2) * (64 * 128)) + 2 * (kk & 3);
+          tc_mma_ss_pair_w(d, a, b, id_qk, kk ? 1u : 0u);
+        }
+        tc_commit_pair_mc_w(B.k_empty(st), 3);
+        tc_commit_pair_mc_w(B.s_full(j & 1), 3);
+        return true;
+      };
+      bool ok = warp_wait(B.q_full(), 0, abort_flag, p.err) && qk(0);
+      for (int j = 0; ok && j < nb; ++j) {
+        // S buffer (j + 1) & 1 held P(j - 1), whose product was issued before
+        if (j + 1 < nb && !qk(j + 1)) break;
+        const int st = j % C::NST;
+        if (!warp_wait(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err) ||
+            !warp_wait(B.p_full(j & 1), (j >> 1) & 1, abort_flag, p.err))
+          break;
+        tc_fence_after();
+        const uint32_t a = tmem + C::S_COL + (j & 1) * 128;
+        const uint32_t v = sm + C::OFF_V + st * C::STAGE;
+#pragma unroll
+        for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+          const uint64_t b = D == 64 ? sdesc_mn(v + kk * 16 * 64, 64, 0)
+                                     : sdesc_mn(v + kk * 16 * 128, 128, 128 * 128);
+          tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b, id_pv, (j | kk) ? 1u : 0u);
+        }
+        tc_commit_pair_mc_w(B.v_empty(st), 3);
+        tc_commit_pair_mc_w(B.pv_done(), 3);
+      }
+      tc_commit_pair_mc_w(B.drain(), 3);
+    }
+    // every MMA has finished before TMEM is released
+    if (lane == 0) mbar_wait_bounded(B.drain(), 0, abort_flag, kWaitLimitNs);
+  } else if (warp >= kSoftWarp0) {
+    // ------------------------------------------- softmax, correction, epilogue
+    {
+      // Q: warp w copies rows 16 w .. 16 w + 15 of the CTA's 128
+      constexpr int CH = D / 8, RPI = 32 / CH;
+#pragma unroll 4
+      for (int i = 0; i < 16 / RPI; ++i) {
+        const int r = (warp - kSoftWarp0) * 16 + i * RPI + lane / CH, c = lane % CH;
+        const int gr = r0 + rank * 128 + r;
+        const bool in = gr < r1;
+        const int tk = in ? fast_div(gr, p.divG) : 0;
+        const uint16_t* src =
+            p.q + (in ? (s.t0 + tk) * p.q_ts + (h * p.G + gr - tk * p.G) * p.q_hs : 0) + c * 8;
+        cp_async16(sm + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src,
+                   in ? 16u : 0u);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_release_cluster(mapa_shared(B.q_full(), 0));
+    }
+    // visible keys of the row: [vlo, vhi); rows that do not exist see all (of zeros)
+    int vlo = 0, vhi = 0x7fffffff;
+    if (valid) {
+      const int pos = s.kv - s.nq + tok;
+      vhi = p.causal ? min(s.kv, pos + 1) : s.kv;
+      vlo = p.window > 0 ? pos - p.window + 1 : 0;
+    } else {
+      vhi = s.kv;
+    }
+    int wlo = vlo, whi = vhi;  // the warp's strictest bounds
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      wlo = max(wlo, __shfl_xor_sync(0xffffffffu, wlo, d));
+      whi = min(whi, __shfl_xor_sync(0xffffffffu, whi, d));
+    }
+    float* sh_max = reinterpret_cast<float*>(smem + C::OFF_MAX);  // [buffer][half][row]
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t p_full0 = mapa_shared(B.p_full(0), 0);
+    const float c = p.scale_log2;
+    float m = kNegInf, l = 0.f;  // reference maximum (raw score units), this half's sum
+    // after a wait has given up, the warp runs on without waiting (its partner
+    // may stand at their common barrier) and writes no result
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      const int b = j & 1;
+      ok = ok && warp_wait(B.s_full(b), (j >> 1) & 1, abort_flag, p.err);
+      tc_fence_after();
+      const uint32_t ts = tmem + lanes + C::S_COL + b * 128;
+      uint32_t x[2][32];
+      tmem_ld32(ts + half * 64, x[0]);
+      tmem_ld32(ts + half * 64 + 32, x[1]);
+      tmem_ld_wait();
+      const int k0 = lo + j * kTileKeys + half * 64;
+      if (k0 < wlo || k0 + 64 > min(whi, hi) || any_bad) {
+        const int a = vlo - k0, z = min(vhi, hi) - k0;  // visible: a <= i < z
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          bool vis = i >= a && i < z;
+          if (any_bad) {  // (rare: the page number is looked up again)
+            if (vis) vis = lookup(k0 + i) >= 0;
+          }
+          if (!vis) x[i >> 5][i & 31] = __float_as_uint(kNegInf);
+        }
+      }
+      float mt[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+      for (int i = 0; i < 64; ++i) mt[i & 3] = fmaxf(mt[i & 3], __uint_as_float(x[i >> 5][i & 31]));
+      float mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+      sh_max[(b * 2 + half) * 128 + trow] = mx;
+      quarter_sync(quarter);  // also: both halves hold their scores in registers
+      mx = fmaxf(mx, sh_max[(b * 2 + (half ^ 1)) * 128 + trow]);
+      const bool rise = (mx - m) * c > kRise || (m == kNegInf && mx > m);
+      if (__any_sync(0xffffffffu, rise)) {
+        const float f = rise ? ex2((m - mx) * c) : 1.f;
+        if (rise) m = mx;
+        l *= f;
+        if (j > 0) {
+          // P V of the tiles before has been added up before O changes (the
+          // scores of tile j were issued after P V of tile j - 2, so at most one
+          // phase is outstanding here)
+          ok = ok && warp_wait(B.pv_done(), (j - 1) & 1, abort_flag, p.err);
+          tc_fence_after();
+#pragma unroll 1
+          for (int f0 = 0; f0 < D / 2; f0 += 32) {
+            uint32_t o[32];
+            const uint32_t to = tmem + lanes + half * (D / 2) + f0;
+            tmem_ld32(to, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float mc = m == kNegInf ? 0.f : m * c;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e0 = ex2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), c, -mc));
+        const float e1 = ex2(fmaf(__uint_as_float(x[i >> 4][(2 * i + 1) & 31]), c, -mc));
+        sum[i & 1] += e0;
+        sum[2 + (i & 1)] += e1;
+        pk[i] = pack2<BF>(e0, e1);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(ts + half * 32, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_release_cluster(p_full0 + 8 * b);
+    }
+    // ---- epilogue
+    // (not pv_done: when the last weights are handed over the products of the
+    // last two tiles may both be outstanding, which its parity cannot tell)
+    ok = ok && warp_wait(B.drain(), 0, abort_flag, p.err);
+    // the row's whole sum (the buffer that the last tile did not use)
+    float* sh_l = sh_max + (nb & 1) * 256;
+    sh_l[half * 128 + trow] = l;
+    quarter_sync(quarter);
+    l += sh_l[(half ^ 1) * 128 + trow];
+    if (ok) {
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float mlog = m * c;  // (-inf: no key seen)
+#pragma unroll 1
+      for (int f0 = 0; f0 < D / 2; f0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lanes + half * (D / 2) + f0, o);
+        tmem_ld_wait();
+        if (!valid) continue;
+        const int f = half * (D / 2) + f0;
+        if (p.chunks > 1) {
+          float4* d4 = reinterpret_cast<float4*>(p.part_o + (rid * p.chunks + ck) * D + f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            d4[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+        } else {
+          uint16_t* dst = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 v;
+            v.x = pack2<BF>(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+            v.y = pack2<BF>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+            v.z = pack2<BF>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+            v.w = pack2<BF>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+            reinterpret_cast<uint4*>(dst)[i] = v;
+          }
+        }
+      }
+      if (valid && half == 0) {
+        if (p.chunks > 1) p.part_ml[rid * p.chunks + ck] = make_float2(mlog, l);
+        else if (p.lse) p.lse[rid] = l == 0.f ? kNegInf : kLn2 * mlog + logf(l);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  pair_sync_all();  // no CTA leaves while the other may still arrive on its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int D, bool BF>
+cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
+  using C = ChunkCfg<D>;
+  static bool attr_set = false;
+  if (!attr_set) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        paged_chunk_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(2ll * p.tiles * p.c.heads * p.chunks));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = C::SMEM;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = 2;
+  a[0].val.clusterDim.y = 1;
+  a[0].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st) {
+  switch (p.c.dim) {
+    case 64: return bf16 ? chunk_launch<64, true>(p, st) : chunk_launch<64, false>(p, st);
+    case 128: return bf16 ? chunk_launch<128, true>(p, st) : chunk_launch<128, false>(p, st);
+    case 256: return bf16 ? chunk_launch<256, true>(p, st) : chunk_launch<256, false>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moe

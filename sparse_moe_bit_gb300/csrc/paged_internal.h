@@ -109,7 +109,8 @@ struct AttnParams {
   // split over the keys: chunk c of a row tile covers keys [c, c+1) * chunk
   // behind its first visible one; the last chunk goes to the end
   int chunks, chunk;
-  int tiles;       // row tiles of a sequence the grid provides for
+  int tiles;       // row tiles the grid provides for: of a sequence (16-row
+                   // tiles), of the batch (256-row tiles)
   float* part_o;   // [T * Hq][chunks][D], unnormalised (chunks > 1)
   float2* part_ml; // [T * Hq][chunks]: running maximum (log2 units) and sum
   int* err;
@@ -126,6 +127,8 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
 }
 constexpr int kRowTile = 16;
 cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
+constexpr int kPairRows = 256;
+cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st);
 
 // ---- pages (pages.cu)
