@@ -23,11 +23,15 @@
 // than 2^8 (weights then stay below 2^8, which fp32 sums and 16-bit weights
 // carry without loss), so that O in TMEM is hardly ever rescaled.
 //
-// Warps: 0 copies keys, 2 copies values (16-byte asynchronous copies into the
-// swizzled operand layout, rows of a page gathered by the page table; rows
-// behind the end or with a bad page number are not read but zero), 1 issues
-// the MMAs (the even CTA's), 4..11 softmax, correction and epilogue.  Every
-// wait is bounded.
+// Warps: 0 copies keys, 2 copies values, 1 issues the MMAs (the even CTA's),
+// 4..11 softmax, correction and epilogue.  Every wait is bounded.  The copies
+// are TMA boxes of up to 64 rows of a page x 64 features, a lane each, into the
+// operands' swizzled layouts (copying the same by 16-byte cp.async took one
+// warp 4500 cycles a tile at D = 256 where the products take 2048).  A box that
+// also holds keys outside the chunk's is loaded whole for K (those scores are
+// masked) but row by row for V: what lies there may be NaN, which a weight of
+// zero does not cancel.  A bad page number becomes the number behind the last
+// page, where TMA fills in zeros, and its scores are masked.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -179,8 +183,30 @@ __device__ __forceinline__ void quarter_sync(int q) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
 }
 
-template <int D, bool BF>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnParams p) {
+// Tensor maps over the cache's keys and values (innermost first): feature, row
+// of a page, head, page; boxes of `box` rows x 64 features (keys) or x 64 (32 at
+// D = 64) features (values), in the operands' swizzles.
+struct ChunkParams {
+  AttnParams a;
+  CUtensorMap k, v;
+  int box_log2;  // rows of a box: a power of two that divides the page and 64, >= 8
+};
+
+__device__ __forceinline__ void tma_box_pair(uint32_t dst, const CUtensorMap* tm, int f, int r,
+                                             int h, int pg, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tm), "r"(f), "r"(r), "r"(h), "r"(pg), "r"(bar_cluster)
+      : "memory");
+}
+
+// TMA: whole boxes of the cache are copied by the tensor memory accelerator;
+// otherwise (pages that no box of 8 rows divides) by 16-byte copies alone.
+template <int D, bool BF, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ ChunkParams cp) {
+  const AttnParams& p = cp.a;
   using C = ChunkCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -236,9 +262,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
   const int2 kr = key_range(p, s, r0, r1);
   const int span = kr.y - kr.x;
   const long long c0 = (long long)ck * p.chunk;
+  // keys of this chunk [lo, hi), in tiles from `first` (a box's boundary) on
   const int lo = kr.x + (int)min(c0, (long long)span);
   const int hi = ck == p.chunks - 1 ? kr.y : kr.x + (int)min(c0 + p.chunk, (long long)span);
-  const int nb = (hi - lo + kTileKeys - 1) / kTileKeys;
+  const int first = TMA ? lo & ~63 : lo;
+  const int nb = hi > lo ? (hi - first + kTileKeys - 1) / kTileKeys : 0;
   const int32_t* table = p.b.table + n * p.b.table_stride;
 
   // this thread's row in the softmax warps (the other warps: unused)
@@ -317,72 +345,122 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
     const uint32_t ring = sm + (is_k ? C::OFF_K : C::OFF_V);
     const uint16_t* base = is_k ? p.c.k + h * p.c.head_stride
                                 : p.c.v + h * p.c.head_stride + rank * (D / 2);
-    long long off[4];
-    auto look = [&](int j) {
-      const int k0 = lo + j * kTileKeys + (is_k ? rank * KEYS_K : 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        off[i] = (j < nb && (!is_k || i < 2)) ? lookup(k0 + 32 * i + lane) : -1;
+    // rows [i0, i0 + 32) of a stage by 16-byte copies, lane l's row at element
+    // offset `off` (-1: zeros)
+    auto copy32_k = [&](uint32_t dst, int i0, long long off) {
+      constexpr int CH = D / 8, RPI = 32 / CH;  // pieces of a key; keys a warp copies at once
+#pragma unroll 8
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int r = i0 + i * RPI + lane / CH, c = lane % CH;
+        const long long o = __shfl_sync(0xffffffffu, off, r & 31);
+        cp_async16(dst + (c >> 3) * (KEYS_K * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
+      }
     };
-    look(0);
-    int told = 0;  // stages announced
-    bool ok = true;
-    for (int j = 0; j < nb; ++j) {
-      const int st = j % C::NST;
-      const uint32_t empty = is_k ? B.k_empty(st) : B.v_empty(st);
-      const uint32_t par = ((j / C::NST) & 1) ^ 1;
-      // a stage that is not free yet: what was copied is announced first
-      if (!__all_sync(0xffffffffu, mbar_try_wait(empty, par)) && told < j) {
+    // rows [i0, i0 + count), offsets held by the lanes of row modulo 32
+    auto copy_v = [&](uint32_t dst, int i0, int count, long long off) {
+      constexpr int CH = D / 16, RPI = 32 / CH;  // pieces of half a value
+      for (int i = 0; i < count / RPI; ++i) {
+        const int r = i0 + i * RPI + lane / CH, c = lane % CH;
+        const long long o = __shfl_sync(0xffffffffu, off, r & 31);
+        const uint32_t at = D == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                    : (c >> 3) * (KEYS_V * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        cp_async16(dst + at, base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
+      }
+    };
+    if constexpr (TMA) {
+      // At most one box a lane: box `y` of the stage's rows, `x` of its features.
+      // A lane's page number is looked up a tile ahead.
+      constexpr int FW = (D == 64) ? 32 : 64;       // features of a box of V
+      const int box = 1 << cp.box_log2;
+      const int fc_log2 = is_k ? (D == 256 ? 2 : (D == 128 ? 1 : 0)) : (D == 256 ? 1 : 0);
+      const int x = lane & ((1 << fc_log2) - 1), y = lane >> fc_log2;
+      const int stage_rows = is_k ? KEYS_K : KEYS_V;
+      const bool mine = (y << cp.box_log2) < stage_rows;
+      const int row0 = (is_k ? rank * KEYS_K : 0) + (y << cp.box_log2);  // first row in the tile
+      const uint32_t at = is_k ? x * (KEYS_K * 128) + (y << cp.box_log2) * 128
+                               : x * (KEYS_V * 128) + (y << cp.box_log2) * FW * 2;
+      const int feature = is_k ? x * 64 : rank * (D / 2) + x * FW;
+      int page_row = 0, page = 0;
+      auto look = [&](int j) {
+        const int key = first + j * kTileKeys + row0;
+        if (mine && j < nb && key < hi) {
+          const int col = fast_div(key, p.c.div);
+          page_row = key - col * p.c.page;
+          page = table[col];
+        }
+      };
+      look(0);
+      int st = 0;
+      uint32_t par = 1;
+      for (int j = 0; j < nb; ++j) {
+        const uint32_t full = full0 + 8 * st;
+        const uint32_t dst = ring + st * C::STAGE;
+        const int t0 = first + j * kTileKeys;
+        // rows of the tile that hold keys of the chunk, [e0, e1), and the boxes
+        // that are loaded: all with such a row (K); those with no other row (V)
+        const int e0 = max(lo - t0, 0), e1 = min(hi - t0, kTileKeys);
+        const int up = is_k ? 0 : box - 1, dn = is_k ? box - 1 : 0;
+        const int w0 = (e0 + up) & ~(box - 1), w1 = (e1 + dn) & ~(box - 1);
+        if (!warp_wait(is_k ? B.k_empty(st) : B.v_empty(st), par, abort_flag, p.err)) break;
+        if (rank == 0 && lane == 0) {
+          const uint32_t bytes = (uint32_t)max(w1 - w0, 0) * D * 2;  // both CTAs'
+          const uint32_t bar = is_k ? B.k_full(st) : B.v_full(st);
+          asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+                       : "memory");
+        }
+        if (mine && row0 >= w0 && row0 < w1)
+          tma_box_pair(dst + at, is_k ? &cp.k : &cp.v, feature, page_row, h,
+                       (page < 0 || page > p.c.pages) ? p.c.pages : page, full);
+        look(j + 1);
+        bool copied = false;
+        if (!is_k && (e0 > 0 || w1 < kTileKeys)) {
+          // the edges of the chunk: what the product's 16-key steps touch besides
+          const int end = (e1 + 15) & ~15;
+          for (int i0 = e0 & ~15; i0 < end; i0 += 8) {
+            if (i0 >= w0 && i0 < w1) continue;
+            const int key = t0 + (i0 & ~31) + lane;
+            copy_v(dst, i0, 8, key >= lo ? lookup(key) : -1);
+            copied = true;
+          }
+          if (copied) {
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (copied) arrive_release_cluster(full);
+          else mbar_arrive_cluster(full);
+        }
+        if (++st == C::NST) {
+          st = 0;
+          par ^= 1;
+        }
+      }
+    } else {
+      for (int j = 0; j < nb; ++j) {
+        const int st = j % C::NST;
+        const uint32_t dst = ring + st * C::STAGE;
+        const int t0 = first + j * kTileKeys;
+        if (!warp_wait(is_k ? B.k_empty(st) : B.v_empty(st), ((j / C::NST) & 1) ^ 1, abort_flag, p.err))
+          break;
+#pragma unroll
+        for (int i0 = 0; i0 < KEYS_V; i0 += 32) {
+          if (is_k && i0 >= KEYS_K) break;
+          const long long off = lookup(t0 + (is_k ? rank * KEYS_K : 0) + i0 + lane);
+          if (is_k) copy32_k(dst, i0, off);
+          else copy_v(dst, i0, 32, off);
+        }
+        cp_async_commit();
         cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-          for (; told < j; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
-        told = j;
-      }
-      if (!warp_wait(empty, par, abort_flag, p.err)) {
-        ok = false;
-        break;
-      }
-      const uint32_t dst = ring + st * C::STAGE;
-      if (is_k) {
-        constexpr int CH = D / 8;        // 16-byte pieces of a key
-        constexpr int RPI = 32 / CH;     // keys a warp copies at once
-#pragma unroll
-        for (int i = 0; i < KEYS_K / RPI; ++i) {
-          const int r = i * RPI + lane / CH, c = lane % CH;
-          const long long o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
-          cp_async16(dst + (c >> 3) * (KEYS_K * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
-        }
-      } else {
-        constexpr int CH = D / 16;       // 16-byte pieces of half a value
-        constexpr int RPI = 32 / CH;
-#pragma unroll
-        for (int i = 0; i < KEYS_V / RPI; ++i) {
-          const int r = i * RPI + lane / CH, c = lane % CH;
-          const long long o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
-          const uint32_t at = D == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
-                                      : (c >> 3) * (KEYS_V * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          cp_async16(dst + at, base + (o >= 0 ? o : 0) + c * 8, o >= 0 ? 16u : 0u);
-        }
-      }
-      cp_async_commit();
-      look(j + 1);
-      if (told < j) {  // the stage before this one (older ones are announced)
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-          for (; told < j; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
-        told = j;
+        if (lane == 0) arrive_release_cluster(full0 + 8 * st);
       }
     }
     cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (ok && lane == 0)
-      for (; told < nb; ++told) arrive_release_cluster(full0 + 8 * (told % C::NST));
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -415,11 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
         tc_fence_after();
         const uint32_t a = tmem + C::S_COL + (j & 1) * 128;
         const uint32_t v = sm + C::OFF_V + st * C::STAGE;
+        // the 16-key steps that hold a key of the chunk (all but at its edges)
+        const int t0 = first + j * kTileKeys;
+        const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+          if (kk < ka || kk >= kz) continue;
           const uint64_t b = D == 64 ? sdesc_mn(v + kk * 16 * 64, 64, 0)
                                      : sdesc_mn(v + kk * 16 * 128, 128, 128 * 128);
-          tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b, id_pv, (j | kk) ? 1u : 0u);
+          tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
         }
         tc_commit_pair_mc_w(B.v_empty(st), 3);
         tc_commit_pair_mc_w(B.pv_done(), 3);
@@ -459,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
     } else {
       vhi = s.kv;
     }
+    vlo = max(vlo, lo);
     int wlo = vlo, whi = vhi;  // the warp's strictest bounds
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
@@ -482,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
       tmem_ld32(ts + half * 64, x[0]);
       tmem_ld32(ts + half * 64 + 32, x[1]);
       tmem_ld_wait();
-      const int k0 = lo + j * kTileKeys + half * 64;
+      const int k0 = first + j * kTileKeys + half * 64;
       if (k0 < wlo || k0 + 64 > min(whi, hi) || any_bad) {
         const int a = vlo - k0, z = min(vhi, hi) - k0;  // visible: a <= i < z
 #pragma unroll
@@ -541,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_release_cluster(p_full0 + 8 * b);
+      // (what this arrival publishes lies in TMEM, ordered by the tcgen05 fences;
+      // a release at cluster scope here costs several hundred cycles a tile)
+      if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * b);
     }
     // ---- epilogue
     // (not pv_done: when the last weights are handed over the products of the
@@ -598,13 +683,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const AttnPara
   }
 }
 
-template <int D, bool BF>
-cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
+template <int D, bool BF, bool TMA>
+cudaError_t chunk_launch_t(const ChunkParams& cp, cudaStream_t st) {
   using C = ChunkCfg<D>;
+  const AttnParams& p = cp.a;
   static bool attr_set = false;
   if (!attr_set) {
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_chunk_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        paged_chunk_kernel<D, BF, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
@@ -620,7 +706,32 @@ cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
   a[0].val.clusterDim.z = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF>, p);
+  return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF, TMA>, cp);
+}
+
+// A map over one of the cache's arrays; false where the array has no such map
+// (a stride that the encoding refuses).
+bool page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box, bool bf16) {
+  const long long dims[4] = {c.dim, c.page, c.heads, c.pages};
+  const long long strides[3] = {c.row_stride * 2, c.head_stride * 2, c.page_stride * 2};
+  const int boxes[4] = {features, box, 1, 1};
+  return make_tmap_paged(m, base, dims, strides, boxes, bf16, features == 64) == cudaSuccess;
+}
+
+template <int D, bool BF>
+cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
+  ChunkParams cp;
+  cp.a = p;
+  int box = 64;
+  cp.box_log2 = 6;
+  while (p.c.page % box) {
+    box >>= 1;
+    --cp.box_log2;
+  }
+  if (box >= 8 && page_map(&cp.k, p.c.k, p.c, 64, box, BF) &&
+      page_map(&cp.v, p.c.v, p.c, D == 64 ? 32 : 64, box, BF))
+    return chunk_launch_t<D, BF, true>(cp, st);
+  return chunk_launch_t<D, BF, false>(cp, st);
 }
 
 }  // namespace
