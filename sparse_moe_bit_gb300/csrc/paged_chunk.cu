@@ -8,7 +8,7 @@
 //   S = Q K^T, m' = max(m, rowmax S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
 //   O = O 2^(m - m') + P V        (S in log2 units; S, m, l, O fp32)
 // Each CTA holds 128 of the rows: its Q in shared memory, its O (D columns)
-// and two S buffers (128 columns each) in TMEM, all 512 columns at D = 256.
+// and two S buffers (128 columns each) in TMEM, all 512 columns at D = 256 (three S buffers below).
 // The pair shares the operands: of a tile each CTA loads 64 keys (half of B's
 // columns in Q K^T) and half of every value's features (half of B's columns in
 // P V), so that a byte of the cache enters one SM for 256 rows.  P goes back to
@@ -17,7 +17,8 @@
 //
 // Bound: the tensor cores (4 D operations per row and key).  Their two products
 // of tile j and the softmax of tile j + 1 overlap: the order of issue is
-// QK(0), QK(1), PV(0), QK(2), PV(1), ...  Eight warps run the softmax, a thread
+// QK(0), QK(1), PV(0), QK(2), PV(1), ... (one tile further ahead with three S
+// buffers)  Eight warps run the softmax, a thread
 // half a row (64 keys) -- a row's two threads exchange their maxima through
 // shared memory -- and the reference maximum only moves when it rises by more
 // than 2^8 (weights then stay below 2^8, which fp32 sums and 16-bit weights
@@ -53,11 +54,13 @@ template <int D>
 struct ChunkCfg {
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int STAGE = 128 * D;  // 64 keys, or half the features of 128 values
-  static constexpr int NST = D == 256 ? 2 : (D == 128 ? 3 : 4);  // stages of K and of V
+  static constexpr int NST = D == 256 ? 2 : 4;  // stages of K and of V
+  // S buffers in TMEM beside O's D columns: the scores run NS - 1 tiles ahead
+  static constexpr int NS = D == 256 ? 2 : 3;
   static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + NST * STAGE;
   static constexpr int OFF_BAR = OFF_V + NST * STAGE;
-  static constexpr int NUM_BARS = 1 + 4 * NST + 2 + 2 + 2;
+  static constexpr int NUM_BARS = 1 + 4 * NST + 2 * NS + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_MAX = (OFF_MISC + 64 + 15) / 16 * 16;  // float [2][128], double-buffered
   // never two CTAs on an SM: each takes all of TMEM, and two pairs that held one
@@ -65,7 +68,8 @@ struct ChunkCfg {
   static constexpr int SMEM =
       OFF_MAX + 2 * 2 * 128 * 4 + 1024 > 120000 ? OFF_MAX + 2 * 2 * 128 * 4 + 1024 : 120000;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static constexpr int S_COL = 256;  // TMEM: O at 0, S buffers at 256 and 384
+  static constexpr int S_COL = 512 - 128 * NS;  // TMEM: O at 0, S buffers at the end
+  static_assert(D <= S_COL, "TMEM budget");
 };
 
 template <int D>
@@ -78,12 +82,17 @@ struct Bars {
   __device__ uint32_t v_full(int s) const { return base + 8 * (1 + 2 * C::NST + s); }
   __device__ uint32_t v_empty(int s) const { return base + 8 * (1 + 3 * C::NST + s); }
   __device__ uint32_t s_full(int b) const { return base + 8 * (1 + 4 * C::NST + b); }
-  __device__ uint32_t p_full(int b) const { return base + 8 * (3 + 4 * C::NST + b); }
-  __device__ uint32_t pv_done() const { return base + 8 * (5 + 4 * C::NST); }
-  __device__ uint32_t drain() const { return base + 8 * (6 + 4 * C::NST); }
+  __device__ uint32_t p_full(int b) const { return base + 8 * (1 + 4 * C::NST + C::NS + b); }
+  __device__ uint32_t pv_done(int b) const { return base + 8 * (1 + 4 * C::NST + 2 * C::NS + b); }
+  __device__ uint32_t drain() const { return base + 8 * (3 + 4 * C::NST + 2 * C::NS); }
 };
 
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+// (CLUSTER: acquires what another CTA's threads wrote to shared memory by plain
+// or asynchronous copies; what TMA wrote or lies in TMEM needs no more than the
+// default, which costs the MMA warp some hundred cycles less a wait)
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  if constexpr (!CLUSTER) return mbar_try_wait_sleep(bar, parity);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -103,13 +112,14 @@ __device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
 
 // The whole warp waits; false when the limit has passed or another wait of the
 // CTA has given up.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           int* err) {
-  bool ok = try_wait_cluster(bar, parity);
+  bool ok = try_wait<CLUSTER>(bar, parity);
   if (__all_sync(0xffffffffu, ok)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    ok = ok || try_wait_cluster(bar, parity);
+    ok = ok || try_wait<CLUSTER>(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     int bail = 0;
     if ((threadIdx.x & 31) == 0) bail = (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs);
@@ -123,15 +133,43 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// D (+)= A[smem] * B[smem]^T over the pair, M = 256 (warp-wide form)
-__device__ __forceinline__ void tc_mma_ss_pair_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
+// Four MMAs (K = 64) of D (+)= A[smem] * B[smem]^T over the pair, M = 256, both
+// operands advancing by 32 bytes.  Warp-wide: every lane makes the call, one
+// elected lane issues; one block for all four, so that the election and the
+// moves of the operands to uniform registers are paid once.
+__device__ __forceinline__ void mma_ss_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Four MMAs (K = 64) of D (+)= A[tmem] * B[smem], A advancing by 8 columns and
+// B's descriptor by STEP.
+template <int STEP>
+__device__ __forceinline__ void mma_ts_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, %5;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, %7;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
       : "memory");
 }
 
@@ -173,6 +211,33 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// pairs of fp32 in one 64-bit register
+__device__ __forceinline__ uint64_t pack_u2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  return pack_u2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ void pair_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -302,11 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(B.v_full(i), 2);
       mbar_init(B.v_empty(i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NS; ++i) {
       mbar_init(B.s_full(i), 1);
       mbar_init(B.p_full(i), 2 * kSoftWarps);
     }
-    mbar_init(B.pv_done(), 1);
+    mbar_init(B.pv_done(0), 1);
+    mbar_init(B.pv_done(1), 1);
     mbar_init(B.drain(), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -467,44 +533,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_qk = idesc_f16(256, kTileKeys, BF ? 1 : 0);
       const uint32_t id_pv = idesc_f16(256, D, BF ? 1 : 0) | (1u << 16);  // B: N contiguous
       auto qk = [&](int j) -> bool {
-        const int st = j % C::NST;
-        if (!warp_wait(B.k_full(st), (j / C::NST) & 1, abort_flag, p.err)) return false;
+        const int st = j % C::NST, sb = j % C::NS;
+        if (!warp_wait<!TMA>(B.k_full(st), (j / C::NST) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + C::S_COL + (j & 1) * 128;
+        const uint32_t d = tmem + C::S_COL + sb * 128;
+        const uint64_t a = sdesc_k_sw128(sm);
+        const uint64_t b = sdesc_k_sw128(sm + C::OFF_K + st * C::STAGE);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t a = sdesc_k_sw128(sm + (kk >> 2) * (128 * 128)) + 2 * (kk & 3);
-          const uint64_t b =
-              sdesc_k_sw128(sm + C::OFF_K + st * C::STAGE + (kk >> 2) * (64 * 128)) + 2 * (kk & 3);
-          tc_mma_ss_pair_w(d, a, b, id_qk, kk ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 64; ++kk)
+          mma_ss_x4(d, a + kk * (128 * 128 / 16), b + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
         tc_commit_pair_mc_w(B.k_empty(st), 3);
-        tc_commit_pair_mc_w(B.s_full(j & 1), 3);
+        tc_commit_pair_mc_w(B.s_full(sb), 3);
         return true;
       };
-      bool ok = warp_wait(B.q_full(), 0, abort_flag, p.err) && qk(0);
+      bool ok = warp_wait<true>(B.q_full(), 0, abort_flag, p.err);
+      for (int j = 0; ok && j < C::NS - 1 && j < nb; ++j) ok = qk(j);
       for (int j = 0; ok && j < nb; ++j) {
-        // S buffer (j + 1) & 1 held P(j - 1), whose product was issued before
-        if (j + 1 < nb && !qk(j + 1)) break;
-        const int st = j % C::NST;
-        if (!warp_wait(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err) ||
-            !warp_wait(B.p_full(j & 1), (j >> 1) & 1, abort_flag, p.err))
-          break;
-        tc_fence_after();
-        const uint32_t a = tmem + C::S_COL + (j & 1) * 128;
-        const uint32_t v = sm + C::OFF_V + st * C::STAGE;
+        // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
+        // before: the tensor core takes a thread's MMAs in the order of issue.
+        if (j + C::NS - 1 < nb && !qk(j + C::NS - 1)) break;
+        const int st = j % C::NST, sb = j % C::NS;
         // the 16-key steps that hold a key of the chunk (all but at its edges)
         const int t0 = first + j * kTileKeys;
         const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-          if (kk < ka || kk >= kz) continue;
-          const uint64_t b = D == 64 ? sdesc_mn(v + kk * 16 * 64, 64, 0)
-                                     : sdesc_mn(v + kk * 16 * 128, 128, 128 * 128);
-          tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
+        const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
+        if (!((TMA && inner) ? warp_wait(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err)
+                             : warp_wait<true>(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err)) ||
+            !warp_wait(B.p_full(sb), (j / C::NS) & 1, abort_flag, p.err))
+          break;
+        tc_fence_after();
+        const uint32_t a = tmem + C::S_COL + sb * 128;
+        const uint32_t v = sm + C::OFF_V + st * C::STAGE;
+        constexpr int STEP = (D == 64 ? 16 * 64 : 16 * 128) / 16;  // 16 keys
+        const uint64_t b = D == 64 ? sdesc_mn(v, 64, 0) : sdesc_mn(v, 128, 128 * 128);
+        if (inner) {
+          mma_ts_x4<STEP>(tmem, a, b, id_pv, j > 0 ? 1u : 0u);
+          mma_ts_x4<STEP>(tmem, a + 32, b + 4 * STEP, id_pv, 1u);
+        } else {
+          for (int kk = ka; kk < kz; ++kk)
+            tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b + STEP * kk, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
         }
         tc_commit_pair_mc_w(B.v_empty(st), 3);
-        tc_commit_pair_mc_w(B.pv_done(), 3);
+        tc_commit_pair_mc_w(B.pv_done(j & 1), 3);
       }
       tc_commit_pair_mc_w(B.drain(), 3);
     }
@@ -556,11 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a wait has given up, the warp runs on without waiting (its partner
     // may stand at their common barrier) and writes no result
     bool ok = true;
+    int sb = 0;
+    uint32_t spar = 0;
     for (int j = 0; j < nb; ++j) {
       const int b = j & 1;
-      ok = ok && warp_wait(B.s_full(b), (j >> 1) & 1, abort_flag, p.err);
+      ok = ok && warp_wait(B.s_full(sb), spar, abort_flag, p.err);
       tc_fence_after();
-      const uint32_t ts = tmem + lanes + C::S_COL + b * 128;
+      const uint32_t ts = tmem + lanes + C::S_COL + sb * 128;
       uint32_t x[2][32];
       tmem_ld32(ts + half * 64, x[0]);
       tmem_ld32(ts + half * 64 + 32, x[1]);
@@ -577,10 +649,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!vis) x[i >> 5][i & 31] = __float_as_uint(kNegInf);
         }
       }
-      float mt[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+      float mt[4];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) mt[i & 3] = fmaxf(mt[i & 3], __uint_as_float(x[i >> 5][i & 31]));
-      float mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+      for (int i = 0; i < 4; ++i) mt[i] = __uint_as_float(x[0][i]);
+#pragma unroll
+      for (int i = 4; i + 8 <= 64; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mt[e] = max3(mt[e], __uint_as_float(x[(i + e) >> 5][(i + e) & 31]),
+                       __uint_as_float(x[(i + 4 + e) >> 5][(i + 4 + e) & 31]));
+      float mx = max3(max3(mt[0], __uint_as_float(x[1][28]), __uint_as_float(x[1][29])),
+                      max3(mt[1], __uint_as_float(x[1][30]), __uint_as_float(x[1][31])),
+                      fmaxf(mt[2], mt[3]));
       sh_max[(b * 2 + half) * 128 + trow] = mx;
       quarter_sync(quarter);  // also: both halves hold their scores in registers
       mx = fmaxf(mx, sh_max[(b * 2 + (half ^ 1)) * 128 + trow]);
@@ -590,10 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rise) m = mx;
         l *= f;
         if (j > 0) {
-          // P V of the tiles before has been added up before O changes (the
-          // scores of tile j were issued after P V of tile j - 2, so at most one
-          // phase is outstanding here)
-          ok = ok && warp_wait(B.pv_done(), (j - 1) & 1, abort_flag, p.err);
+          // P V of the tiles before has been added up before O changes (two
+          // barriers in turn: the scores of tile j were issued after P V of tile
+          // j - 3, so each has at most one phase outstanding)
+          ok = ok && warp_wait(B.pv_done((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag, p.err);
           tc_fence_after();
 #pragma unroll 1
           for (int f0 = 0; f0 < D / 2; f0 += 32) {
@@ -609,24 +689,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float mc = m == kNegInf ? 0.f : m * c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      // two values at a time where the machine can: x c - mc, and the sums
+      const uint64_t c2 = pack_f2(c, c), mc2 = pack_f2(-mc, -mc);
+      uint64_t sum[2] = {0, 0};
       uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float e0 = ex2(fmaf(__uint_as_float(x[i >> 4][(2 * i) & 31]), c, -mc));
-        const float e1 = ex2(fmaf(__uint_as_float(x[i >> 4][(2 * i + 1) & 31]), c, -mc));
-        sum[i & 1] += e0;
-        sum[2 + (i & 1)] += e1;
+        const uint64_t t = fma_f2(pack_u2(x[i >> 4][(2 * i) & 31], x[i >> 4][(2 * i + 1) & 31]), c2, mc2);
+        float e0, e1;
+        unpack_f2(t, e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        sum[i & 1] = add_f2(sum[i & 1], pack_f2(e0, e1));
         pk[i] = pack2<BF>(e0, e1);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      {
+        float a0, a1;
+        unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
+        l += a0 + a1;
+      }
       tmem_st32(ts + half * 32, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       // (what this arrival publishes lies in TMEM, ordered by the tcgen05 fences;
       // a release at cluster scope here costs several hundred cycles a tile)
-      if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * b);
+      if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * sb);
+      if (++sb == C::NS) {
+        sb = 0;
+        spar ^= 1;
+      }
     }
     // ---- epilogue
     // (not pv_done: when the last weights are handed over the products of the
