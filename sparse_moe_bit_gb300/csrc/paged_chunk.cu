@@ -54,13 +54,15 @@ template <int D>
 struct ChunkCfg {
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int STAGE = 128 * D;  // 64 keys, or half the features of 128 values
-  static constexpr int NST = D == 256 ? 2 : 4;  // stages of K and of V
-  // S buffers in TMEM beside O's D columns: the scores run NS - 1 tiles ahead
+  // S buffers in TMEM beside O's D columns (the scores run NS - 1 tiles ahead)
+  // and stages of K: the commit that announces a tile's scores also frees its
+  // K stage
   static constexpr int NS = D == 256 ? 2 : 3;
+  static constexpr int VST = D == 256 ? 2 : 4;  // stages of V
   static constexpr int OFF_K = Q_BYTES;
-  static constexpr int OFF_V = OFF_K + NST * STAGE;
-  static constexpr int OFF_BAR = OFF_V + NST * STAGE;
-  static constexpr int NUM_BARS = 1 + 4 * NST + 2 * NS + 2 + 1;
+  static constexpr int OFF_V = OFF_K + NS * STAGE;
+  static constexpr int OFF_BAR = OFF_V + VST * STAGE;
+  static constexpr int NUM_BARS = 2 + 3 * NS + 2 * VST;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_MAX = (OFF_MISC + 64 + 15) / 16 * 16;  // float [2][128], double-buffered
   // never two CTAs on an SM: each takes all of TMEM, and two pairs that held one
@@ -77,14 +79,12 @@ struct Bars {
   using C = ChunkCfg<D>;
   uint32_t base;
   __device__ uint32_t q_full() const { return base; }
-  __device__ uint32_t k_full(int s) const { return base + 8 * (1 + s); }
-  __device__ uint32_t k_empty(int s) const { return base + 8 * (1 + C::NST + s); }
-  __device__ uint32_t v_full(int s) const { return base + 8 * (1 + 2 * C::NST + s); }
-  __device__ uint32_t v_empty(int s) const { return base + 8 * (1 + 3 * C::NST + s); }
-  __device__ uint32_t s_full(int b) const { return base + 8 * (1 + 4 * C::NST + b); }
-  __device__ uint32_t p_full(int b) const { return base + 8 * (1 + 4 * C::NST + C::NS + b); }
-  __device__ uint32_t pv_done(int b) const { return base + 8 * (1 + 4 * C::NST + 2 * C::NS + b); }
-  __device__ uint32_t drain() const { return base + 8 * (3 + 4 * C::NST + 2 * C::NS); }
+  __device__ uint32_t drain() const { return base + 8; }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (2 + s); }
+  __device__ uint32_t s_full(int s) const { return base + 8 * (2 + C::NS + s); }
+  __device__ uint32_t p_full(int s) const { return base + 8 * (2 + 2 * C::NS + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (2 + 3 * C::NS + s); }
+  __device__ uint32_t v_empty(int s) const { return base + 8 * (2 + 3 * C::NS + C::VST + s); }
 };
 
 // (CLUSTER: acquires what another CTA's threads wrote to shared memory by plain
@@ -361,18 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   if (threadIdx.x == 0) {
     mbar_init(B.q_full(), 2 * kSoftWarps);
-    for (int i = 0; i < C::NST; ++i) {
-      mbar_init(B.k_full(i), 2);
-      mbar_init(B.k_empty(i), 1);
-      mbar_init(B.v_full(i), 2);
-      mbar_init(B.v_empty(i), 1);
-    }
     for (int i = 0; i < C::NS; ++i) {
+      mbar_init(B.k_full(i), 2);
       mbar_init(B.s_full(i), 1);
       mbar_init(B.p_full(i), 2 * kSoftWarps);
     }
-    mbar_init(B.pv_done(0), 1);
-    mbar_init(B.pv_done(1), 1);
+    for (int i = 0; i < C::VST; ++i) {
+      mbar_init(B.v_full(i), 2);
+      mbar_init(B.v_empty(i), 1);
+    }
     mbar_init(B.drain(), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -409,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int KEYS_K = 64, KEYS_V = 128;
     const uint32_t full0 = mapa_shared(is_k ? B.k_full(0) : B.v_full(0), 0);
     const uint32_t ring = sm + (is_k ? C::OFF_K : C::OFF_V);
+    const int stages = is_k ? C::NS : C::VST;
     const uint16_t* base = is_k ? p.c.k + h * p.c.head_stride
                                 : p.c.v + h * p.c.head_stride + rank * (D / 2);
     // rows [i0, i0 + 32) of a stage by 16-byte copies, lane l's row at element
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e0 = max(lo - t0, 0), e1 = min(hi - t0, kTileKeys);
         const int up = is_k ? 0 : box - 1, dn = is_k ? box - 1 : 0;
         const int w0 = (e0 + up) & ~(box - 1), w1 = (e1 + dn) & ~(box - 1);
-        if (!warp_wait(is_k ? B.k_empty(st) : B.v_empty(st), par, abort_flag, p.err)) break;
+        if (!warp_wait(is_k ? B.s_full(st) : B.v_empty(st), par, abort_flag, p.err)) break;
         if (rank == 0 && lane == 0) {
           const uint32_t bytes = (uint32_t)max(w1 - w0, 0) * D * 2;  // both CTAs'
           const uint32_t bar = is_k ? B.k_full(st) : B.v_full(st);
@@ -500,17 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (copied) arrive_release_cluster(full);
           else mbar_arrive_cluster(full);
         }
-        if (++st == C::NST) {
+        if (++st == stages) {
           st = 0;
           par ^= 1;
         }
       }
     } else {
       for (int j = 0; j < nb; ++j) {
-        const int st = j % C::NST;
+        const int st = j % stages;
         const uint32_t dst = ring + st * C::STAGE;
         const int t0 = first + j * kTileKeys;
-        if (!warp_wait(is_k ? B.k_empty(st) : B.v_empty(st), ((j / C::NST) & 1) ^ 1, abort_flag, p.err))
+        if (!warp_wait(is_k ? B.s_full(st) : B.v_empty(st), ((j / stages) & 1) ^ 1, abort_flag,
+                       p.err))
           break;
 #pragma unroll
         for (int i0 = 0; i0 < KEYS_V; i0 += 32) {
@@ -532,38 +531,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       const uint32_t id_qk = idesc_f16(256, kTileKeys, BF ? 1 : 0);
       const uint32_t id_pv = idesc_f16(256, D, BF ? 1 : 0) | (1u << 16);  // B: N contiguous
-      auto qk = [&](int j) -> bool {
-        const int st = j % C::NST, sb = j % C::NS;
-        if (!warp_wait<!TMA>(B.k_full(st), (j / C::NST) & 1, abort_flag, p.err)) return false;
-        tc_fence_after();
+      auto qk = [&](int j) {
+        const int sb = j % C::NS;
         const uint32_t d = tmem + C::S_COL + sb * 128;
         const uint64_t a = sdesc_k_sw128(sm);
-        const uint64_t b = sdesc_k_sw128(sm + C::OFF_K + st * C::STAGE);
+        const uint64_t b = sdesc_k_sw128(sm + C::OFF_K + sb * C::STAGE);
 #pragma unroll
         for (int kk = 0; kk < D / 64; ++kk)
           mma_ss_x4(d, a + kk * (128 * 128 / 16), b + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
-        tc_commit_pair_mc_w(B.k_empty(st), 3);
         tc_commit_pair_mc_w(B.s_full(sb), 3);
-        return true;
       };
       bool ok = warp_wait<true>(B.q_full(), 0, abort_flag, p.err);
-      for (int j = 0; ok && j < C::NS - 1 && j < nb; ++j) ok = qk(j);
+      for (int j = 0; ok && j < C::NS - 1 && j < nb; ++j) {
+        ok = warp_wait<!TMA>(B.k_full(j), 0, abort_flag, p.err);
+        tc_fence_after();
+        if (ok) qk(j);
+      }
       for (int j = 0; ok && j < nb; ++j) {
-        // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
-        // before: the tensor core takes a thread's MMAs in the order of issue.
-        if (j + C::NS - 1 < nb && !qk(j + C::NS - 1)) break;
-        const int st = j % C::NST, sb = j % C::NS;
+        const int ahead = j + C::NS - 1;
+        const int sb = j % C::NS, sv = j % C::VST;
+        const uint32_t kb = B.k_full(ahead % C::NS), kp = (ahead / C::NS) & 1;
+        const uint32_t vb = B.v_full(sv), vp = (j / C::VST) & 1;
+        const uint32_t pb = B.p_full(sb), pp = (j / C::NS) & 1;
+        const bool more = ahead < nb;
         // the 16-key steps that hold a key of the chunk (all but at its edges)
         const int t0 = first + j * kTileKeys;
         const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
         const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
-        if (!((TMA && inner) ? warp_wait(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err)
-                             : warp_wait<true>(B.v_full(st), (j / C::NST) & 1, abort_flag, p.err)) ||
-            !warp_wait(B.p_full(sb), (j / C::NS) & 1, abort_flag, p.err))
+        // The three waits of a tile are tested together: each test takes some 200
+        // cycles even where nothing is waited for, and one warp issues everything.
+        bool rk = !more || (TMA && mbar_try_wait(kb, kp));
+        bool rv = TMA && inner && mbar_try_wait(vb, vp);
+        bool rp = mbar_try_wait(pb, pp);
+        rk = __all_sync(0xffffffffu, rk);
+        rv = __all_sync(0xffffffffu, rv);
+        rp = __all_sync(0xffffffffu, rp);
+        // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
+        // before: the tensor core takes a thread's MMAs in the order of issue.
+        if (more) {
+          if (!rk && !warp_wait<!TMA>(kb, kp, abort_flag, p.err)) break;
+          tc_fence_after();
+          qk(ahead);
+        }
+        if (!rv && !((TMA && inner) ? warp_wait(vb, vp, abort_flag, p.err)
+                                    : warp_wait<true>(vb, vp, abort_flag, p.err)))
           break;
+        if (!rp && !warp_wait(pb, pp, abort_flag, p.err)) break;
         tc_fence_after();
         const uint32_t a = tmem + C::S_COL + sb * 128;
-        const uint32_t v = sm + C::OFF_V + st * C::STAGE;
+        const uint32_t v = sm + C::OFF_V + sv * C::STAGE;
         constexpr int STEP = (D == 64 ? 16 * 64 : 16 * 128) / 16;  // 16 keys
         const uint64_t b = D == 64 ? sdesc_mn(v, 64, 0) : sdesc_mn(v, 128, 128 * 128);
         if (inner) {
@@ -573,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = ka; kk < kz; ++kk)
             tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b + STEP * kk, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
         }
-        tc_commit_pair_mc_w(B.v_empty(st), 3);
-        tc_commit_pair_mc_w(B.pv_done(j & 1), 3);
+        tc_commit_pair_mc_w(B.v_empty(sv), 3);
       }
       tc_commit_pair_mc_w(B.drain(), 3);
     }
@@ -670,10 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rise) m = mx;
         l *= f;
         if (j > 0) {
-          // P V of the tiles before has been added up before O changes (two
-          // barriers in turn: the scores of tile j were issued after P V of tile
-          // j - 3, so each has at most one phase outstanding)
-          ok = ok && warp_wait(B.pv_done((j - 1) & 1), ((j - 1) >> 1) & 1, abort_flag, p.err);
+          // P V of the tiles before has been added up before O changes (the
+          // commit that freed tile j - 1's stage of V)
+          ok = ok && warp_wait(B.v_empty((j - 1) % C::VST), ((j - 1) / C::VST) & 1, abort_flag, p.err);
           tc_fence_after();
 #pragma unroll 1
           for (int f0 = 0; f0 < D / 2; f0 += 32) {
@@ -721,8 +735,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ---- epilogue
-    // (not pv_done: when the last weights are handed over the products of the
-    // last two tiles may both be outstanding, which its parity cannot tell)
     ok = ok && warp_wait(B.drain(), 0, abort_flag, p.err);
     // the row's whole sum (the buffer that the last tile did not use)
     float* sh_l = sh_max + (nb & 1) * 256;
