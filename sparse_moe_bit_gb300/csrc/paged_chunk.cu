@@ -18,11 +18,11 @@
 // Bound: the tensor cores (4 D operations per row and key).  Their two products
 // of tile j and the softmax of tile j + 1 overlap: the order of issue is
 // QK(0), QK(1), PV(0), QK(2), PV(1), ... (one tile further ahead with three S
-// buffers)  Eight warps run the softmax, a thread
-// half a row (64 keys) -- a row's two threads exchange their maxima through
-// shared memory -- and the reference maximum only moves when it rises by more
-// than 2^8 (weights then stay below 2^8, which fp32 sums and 16-bit weights
-// carry without loss), so that O in TMEM is hardly ever rescaled.
+// buffers).  Two groups of four warps take the even and the odd tiles, a thread a
+// row, so that one group's exponentials run while the other waits or reduces;
+// they pass the reference maximum on from tile to tile.  It only moves when it
+// rises by more than 2^8 (weights then stay below 2^8, which fp32 sums and
+// 16-bit weights carry without loss), so that O in TMEM is hardly ever rescaled.
 //
 // Warps: 0 copies keys, 2 copies values, 1 issues the MMAs (the even CTA's),
 // 4..11 softmax, correction and epilogue.  Every wait is bounded.  The copies
@@ -42,8 +42,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftWarp0 = 4, kSoftWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kSoftWarp0 = 4, kSoftWarps = 16;  // two groups of two halves of a row
 constexpr int kTileKeys = 128;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -64,11 +64,13 @@ struct ChunkCfg {
   static constexpr int OFF_BAR = OFF_V + VST * STAGE;
   static constexpr int NUM_BARS = 2 + 3 * NS + 2 * VST;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
-  static constexpr int OFF_MAX = (OFF_MISC + 64 + 15) / 16 * 16;  // float [2][128], double-buffered
+  static constexpr int OFF_REF = (OFF_MISC + 64 + 15) / 16 * 16;  // float [4][128]
+  static constexpr int OFF_MAX = OFF_REF + 4 * 128 * 4;           // float [4][2][128]
+  static constexpr int OFF_ML = OFF_MAX + 8 * 128 * 4;            // float2 [4][128]
+  static constexpr int USED = OFF_ML + 4 * 128 * 8 + 1024;
   // never two CTAs on an SM: each takes all of TMEM, and two pairs that held one
   // SM each would wait for one another
-  static constexpr int SMEM =
-      OFF_MAX + 2 * 2 * 128 * 4 + 1024 > 120000 ? OFF_MAX + 2 * 2 * 128 * 4 + 1024 : 120000;
+  static constexpr int SMEM = USED > 120000 ? USED : 120000;
   static_assert(SMEM <= 232448, "shared memory budget");
   static constexpr int S_COL = 512 - 128 * NS;  // TMEM: O at 0, S buffers at the end
   static_assert(D <= S_COL, "TMEM budget");
@@ -243,9 +245,17 @@ __device__ __forceinline__ void pair_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// the two warps that share the rows of one TMEM lane quarter
+// Barriers of a lane quarter: the one of group g's tile counts its two halves'
+// warps, which wait, and the warp of the other group that hands on the reference.
+__device__ __forceinline__ void tile_arrive(int g, int q) {
+  asm volatile("bar.arrive %0, 96;" ::"r"(5 + g * 4 + q) : "memory");
+}
+__device__ __forceinline__ void tile_wait(int g, int q) {
+  asm volatile("bar.sync %0, 96;" ::"r"(5 + g * 4 + q) : "memory");
+}
+// the four warps that share a lane quarter's rows
 __device__ __forceinline__ void quarter_sync(int q) {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
 }
 
 // Tensor maps over the cache's keys and values (innermost first): feature, row
@@ -335,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t* table = p.b.table + n * p.b.table_stride;
 
   // this thread's row in the softmax warps (the other warps: unused)
-  const int quarter = warp & 3, half = (warp - kSoftWarp0) >> 2;
+  const int quarter = warp & 3, half = ((warp - kSoftWarp0) >> 2) & 1;
+  const int group = (warp - kSoftWarp0) >> 3;
   const int trow = quarter * 32 + lane;
   const int row = r0 + rank * 128 + trow;
   const bool valid = row < r1;
@@ -345,13 +356,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (nb == 0) {  // nothing to see in this chunk (uniform over the pair)
     if (warp >= kSoftWarp0 && valid) {
-      const int f0 = half * (D / 2);
+      const int part = half + 2 * group;  // a quarter of the features
       if (p.chunks > 1) {
-        if (half == 0) p.part_ml[rid * p.chunks + ck] = make_float2(kNegInf, 0.f);
+        if (part == 0) p.part_ml[rid * p.chunks + ck] = make_float2(kNegInf, 0.f);
       } else {
-        uint16_t* o = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f0;
-        for (int f = 0; f < D / 2; f += 8) *reinterpret_cast<uint4*>(o + f) = make_uint4(0, 0, 0, 0);
-        if (half == 0 && p.lse) p.lse[rid] = kNegInf;
+        uint16_t* o = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + part * (D / 4);
+        for (int f = 0; f < D / 4; f += 8) *reinterpret_cast<uint4*>(o + f) = make_uint4(0, 0, 0, 0);
+        if (part == 0 && p.lse) p.lse[rid] = kNegInf;
       }
     }
     return;
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(B.k_full(i), 2);
       mbar_init(B.s_full(i), 1);
-      mbar_init(B.p_full(i), 2 * kSoftWarps);
+      mbar_init(B.p_full(i), kSoftWarps);  // one group's warps of both CTAs
     }
     for (int i = 0; i < C::VST; ++i) {
       mbar_init(B.v_full(i), 2);
@@ -400,6 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return pg * p.c.page_stride + (key - col * p.c.page) * p.c.row_stride;
   };
 
+  // Registers: 96 x 640 at launch = 64 x 128 + 104 x 512 (a thread of the softmax
+  // holds half of a row's scores of a tile).
+  if (warp < kSoftWarp0) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------ keys (0) and values (2)
     const bool is_k = warp == 0;
@@ -558,14 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = first + j * kTileKeys;
         const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
         const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
-        // The three waits of a tile are tested together: each test takes some 200
-        // cycles even where nothing is waited for, and one warp issues everything.
-        bool rk = !more || (TMA && mbar_try_wait(kb, kp));
-        bool rv = TMA && inner && mbar_try_wait(vb, vp);
-        bool rp = mbar_try_wait(pb, pp);
+        // K and V, which have usually arrived, are tested together (a wait costs
+        // some 200 cycles even where nothing is waited for, and one warp issues
+        // everything); the next scores do not wait for this tile's weights
+        bool rk = !more || (TMA && mbar_test(kb, kp));
+        bool rv = TMA && inner && mbar_test(vb, vp);
         rk = __all_sync(0xffffffffu, rk);
         rv = __all_sync(0xffffffffu, rv);
-        rp = __all_sync(0xffffffffu, rp);
         // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
         // before: the tensor core takes a thread's MMAs in the order of issue.
         if (more) {
@@ -576,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!rv && !((TMA && inner) ? warp_wait(vb, vp, abort_flag, p.err)
                                     : warp_wait<true>(vb, vp, abort_flag, p.err)))
           break;
-        if (!rp && !warp_wait(pb, pp, abort_flag, p.err)) break;
+        if (!warp_wait(pb, pp, abort_flag, p.err)) break;
         tc_fence_after();
         const uint32_t a = tmem + C::S_COL + sb * 128;
         const uint32_t v = sm + C::OFF_V + sv * C::STAGE;
@@ -595,14 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every MMA has finished before TMEM is released
     if (lane == 0) mbar_wait_bounded(B.drain(), 0, abort_flag, kWaitLimitNs);
-  } else if (warp >= kSoftWarp0) {
+  }
+  } else {
     // ------------------------------------------- softmax, correction, epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     {
-      // Q: warp w copies rows 16 w .. 16 w + 15 of the CTA's 128
+      // Q: warp w copies rows 8 w .. 8 w + 7 of the CTA's 128
       constexpr int CH = D / 8, RPI = 32 / CH;
 #pragma unroll 4
-      for (int i = 0; i < 16 / RPI; ++i) {
-        const int r = (warp - kSoftWarp0) * 16 + i * RPI + lane / CH, c = lane % CH;
+      for (int i = 0; i < 8 / RPI; ++i) {
+        const int r = (warp - kSoftWarp0) * 8 + i * RPI + lane / CH, c = lane % CH;
         const int gr = r0 + rank * 128 + r;
         const bool in = gr < r1;
         const int tk = in ? fast_div(gr, p.divG) : 0;
@@ -633,19 +649,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       wlo = max(wlo, __shfl_xor_sync(0xffffffffu, wlo, d));
       whi = min(whi, __shfl_xor_sync(0xffffffffu, whi, d));
     }
-    float* sh_max = reinterpret_cast<float*>(smem + C::OFF_MAX);  // [buffer][half][row]
+    // sh_ref [4][128]: a row's reference maximum after tile j, in slot j & 3;
+    // sh_max [slot][half][128]: the halves' maxima of a tile, slot j & 3
+    float* sh_ref = reinterpret_cast<float*>(smem + C::OFF_REF);
+    float* sh_max = reinterpret_cast<float*>(smem + C::OFF_MAX);
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t p_full0 = mapa_shared(B.p_full(0), 0);
     const float c = p.scale_log2;
-    float m = kNegInf, l = 0.f;  // reference maximum (raw score units), this half's sum
-    // after a wait has given up, the warp runs on without waiting (its partner
-    // may stand at their common barrier) and writes no result
+    // the reference that this thread's sum l (over its own scores) is relative to
+    float m = kNegInf, l = 0.f;
+    if (group == 1 && half == 0) {  // "after tile -1"
+      sh_ref[3 * 128 + trow] = kNegInf;
+      tile_arrive(0, quarter);
+    }
+    // after a wait has given up, the warp runs on without waiting (others may
+    // stand at a common barrier) and writes no result
     bool ok = true;
-    int sb = 0;
-    uint32_t spar = 0;
-    for (int j = 0; j < nb; ++j) {
-      const int b = j & 1;
-      ok = ok && warp_wait(B.s_full(sb), spar, abort_flag, p.err);
+    for (int j = group; j < nb; j += 2) {
+      const int sb = j % C::NS;
+      ok = ok && warp_wait(B.s_full(sb), (j / C::NS) & 1, abort_flag, p.err);
       tc_fence_after();
       const uint32_t ts = tmem + lanes + C::S_COL + sb * 128;
       uint32_t x[2][32];
@@ -656,112 +678,139 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (k0 < wlo || k0 + 64 > min(whi, hi) || any_bad) {
         const int a = vlo - k0, z = min(vhi, hi) - k0;  // visible: a <= i < z
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          bool vis = i >= a && i < z;
-          if (any_bad) {  // (rare: the page number is looked up again)
-            if (vis) vis = lookup(k0 + i) >= 0;
+        for (int i = 0; i < 64; ++i)
+          if (i < a || i >= z) x[i >> 5][i & 31] = __float_as_uint(kNegInf);
+        if (any_bad) {  // rare: the page numbers are looked at again
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t out = 0;
+#pragma unroll 1
+            for (int i = max(a - 32 * q, 0); i < min(z - 32 * q, 32); ++i)
+              if (lookup(k0 + 32 * q + i) < 0) out |= 1u << i;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (out >> i & 1) x[q][i] = __float_as_uint(kNegInf);
           }
-          if (!vis) x[i >> 5][i & 31] = __float_as_uint(kNegInf);
         }
       }
       float mt[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) mt[i] = __uint_as_float(x[0][i]);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t* y = x[e >> 1] + (e & 1) * 16;
+        mt[e] = __uint_as_float(y[0]);
 #pragma unroll
-      for (int i = 4; i + 8 <= 64; i += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mt[e] = max3(mt[e], __uint_as_float(x[(i + e) >> 5][(i + e) & 31]),
-                       __uint_as_float(x[(i + 4 + e) >> 5][(i + 4 + e) & 31]));
-      float mx = max3(max3(mt[0], __uint_as_float(x[1][28]), __uint_as_float(x[1][29])),
-                      max3(mt[1], __uint_as_float(x[1][30]), __uint_as_float(x[1][31])),
-                      fmaxf(mt[2], mt[3]));
-      sh_max[(b * 2 + half) * 128 + trow] = mx;
-      quarter_sync(quarter);  // also: both halves hold their scores in registers
-      mx = fmaxf(mx, sh_max[(b * 2 + (half ^ 1)) * 128 + trow]);
-      const bool rise = (mx - m) * c > kRise || (m == kNegInf && mx > m);
-      if (__any_sync(0xffffffffu, rise)) {
-        const float f = rise ? ex2((m - mx) * c) : 1.f;
-        if (rise) m = mx;
-        l *= f;
-        if (j > 0) {
+        for (int i = 1; i < 15; i += 2)
+          mt[e] = max3(mt[e], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+        mt[e] = fmaxf(mt[e], __uint_as_float(y[15]));
+      }
+      float mx = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]);
+      // one barrier for the halves' maxima, for the reference after the tile
+      // before, and for P to replace scores that the other half has read
+      sh_max[((j & 3) * 2 + half) * 128 + trow] = mx;
+      tile_wait(group, quarter);
+      mx = fmaxf(mx, sh_max[((j & 3) * 2 + (half ^ 1)) * 128 + trow]);
+      const float ref = sh_ref[((j - 1) & 3) * 128 + trow];
+      const bool rise = (mx - ref) * c > kRise || (ref == kNegInf && mx > ref);
+      const float now = rise ? mx : ref;
+      if (half == 0) {
+        sh_ref[(j & 3) * 128 + trow] = now;
+        if (j + 1 < nb) tile_arrive(group ^ 1, quarter);
+      }
+      if (__any_sync(0xffffffffu, now != m)) {
+        if (j > 0 && __any_sync(0xffffffffu, rise)) {
           // P V of the tiles before has been added up before O changes (the
           // commit that freed tile j - 1's stage of V)
           ok = ok && warp_wait(B.v_empty((j - 1) % C::VST), ((j - 1) / C::VST) & 1, abort_flag, p.err);
           tc_fence_after();
+          const float f = rise ? ex2((ref - now) * c) : 1.f;
 #pragma unroll 1
-          for (int f0 = 0; f0 < D / 2; f0 += 32) {
-            uint32_t o[32];
+          for (int f0 = 0; f0 < D / 2; f0 += 16) {
+            uint32_t o[16];
             const uint32_t to = tmem + lanes + half * (D / 2) + f0;
-            tmem_ld32(to, o);
+            tmem_ld16(to, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(to, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to, o);
           }
           tmem_st_wait();
         }
+        l = m == kNegInf ? 0.f : l * ex2((m - now) * c);
+        m = now;
       }
       const float mc = m == kNegInf ? 0.f : m * c;
       // two values at a time where the machine can: x c - mc, and the sums
       const uint64_t c2 = pack_f2(c, c), mc2 = pack_f2(-mc, -mc);
       uint64_t sum[2] = {0, 0};
-      uint32_t pk[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const uint64_t t = fma_f2(pack_u2(x[i >> 4][(2 * i) & 31], x[i >> 4][(2 * i + 1) & 31]), c2, mc2);
-        float e0, e1;
-        unpack_f2(t, e0, e1);
-        e0 = ex2(e0);
-        e1 = ex2(e1);
-        sum[i & 1] = add_f2(sum[i & 1], pack_f2(e0, e1));
-        pk[i] = pack2<BF>(e0, e1);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t t = fma_f2(pack_u2(x[q][2 * i], x[q][2 * i + 1]), c2, mc2);
+          float e0, e1;
+          unpack_f2(t, e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          sum[i & 1] = add_f2(sum[i & 1], pack_f2(e0, e1));
+          pk[i] = pack2<BF>(e0, e1);
+        }
+        tmem_st16(ts + half * 32 + 16 * q, pk);
       }
       {
         float a0, a1;
         unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
       }
-      tmem_st32(ts + half * 32, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       // (what this arrival publishes lies in TMEM, ordered by the tcgen05 fences;
       // a release at cluster scope here costs several hundred cycles a tile)
       if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * sb);
-      if (++sb == C::NS) {
-        sb = 0;
-        spar ^= 1;
-      }
     }
-    // ---- epilogue
+    // ---- epilogue: a quarter of the features each
     ok = ok && warp_wait(B.drain(), 0, abort_flag, p.err);
-    // the row's whole sum (the buffer that the last tile did not use)
-    float* sh_l = sh_max + (nb & 1) * 256;
-    sh_l[half * 128 + trow] = l;
+    // the row's whole sum from its four parts
+    const int part = half + 2 * group;
+    float2* sh_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    sh_ml[part * 128 + trow] = make_float2(m, l);
     quarter_sync(quarter);
-    l += sh_l[(half ^ 1) * 128 + trow];
+    {
+      float top = kNegInf;  // the last tile's reference, O's
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, sh_ml[i * 128 + trow].x);
+      l = 0.f;
+      if (top != kNegInf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = sh_ml[i * 128 + trow];
+          l += y.y * ex2((y.x - top) * c);
+        }
+      }
+      m = top;
+    }
     if (ok) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float mlog = m * c;  // (-inf: no key seen)
 #pragma unroll 1
-      for (int f0 = 0; f0 < D / 2; f0 += 32) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lanes + half * (D / 2) + f0, o);
+      for (int f0 = 0; f0 < D / 4; f0 += 16) {
+        const int f = part * (D / 4) + f0;
+        uint32_t o[16];
+        tmem_ld16(tmem + lanes + f, o);
         tmem_ld_wait();
         if (!valid) continue;
-        const int f = half * (D / 2) + f0;
         if (p.chunks > 1) {
           float4* d4 = reinterpret_cast<float4*>(p.part_o + (rid * p.chunks + ck) * D + f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 4; ++i)
             d4[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         } else {
           uint16_t* dst = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             uint4 v;
             v.x = pack2<BF>(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
             v.y = pack2<BF>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
@@ -771,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (valid && half == 0) {
+      if (valid && part == 0) {
         if (p.chunks > 1) p.part_ml[rid * p.chunks + ck] = make_float2(mlog, l);
         else if (p.lse) p.lse[rid] = l == 0.f ? kNegInf : kLn2 * mlog + logf(l);
       }
