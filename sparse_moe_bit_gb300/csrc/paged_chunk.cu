@@ -546,64 +546,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       const uint32_t id_qk = idesc_f16(256, kTileKeys, BF ? 1 : 0);
       const uint32_t id_pv = idesc_f16(256, D, BF ? 1 : 0) | (1u << 16);  // B: N contiguous
-      auto qk = [&](int j) {
-        const int sb = j % C::NS;
-        const uint32_t d = tmem + C::S_COL + sb * 128;
-        const uint64_t a = sdesc_k_sw128(sm);
-        const uint64_t b = sdesc_k_sw128(sm + C::OFF_K + sb * C::STAGE);
+      const uint64_t aq = sdesc_k_sw128(sm);
+      const uint64_t bk0 = sdesc_k_sw128(sm + C::OFF_K);
+      const uint64_t bv0 = D == 64 ? sdesc_mn(sm + C::OFF_V, 64, 0)
+                                   : sdesc_mn(sm + C::OFF_V, 128, 128 * 128);
+      constexpr int STEP = (D == 64 ? 16 * 64 : 16 * 128) / 16;  // descriptor units of 16 keys
+      // ring slots and phase parities of the scores' tile and of the products'
+      int ks = 0, sp = 0, vs = 0;
+      uint32_t kpar = 0, ppar = 0, vpar = 0;
+      auto qk = [&]() {
 #pragma unroll
         for (int kk = 0; kk < D / 64; ++kk)
-          mma_ss_x4(d, a + kk * (128 * 128 / 16), b + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
-        tc_commit_pair_mc_w(B.s_full(sb), 3);
+          mma_ss_x4(tmem + C::S_COL + ks * 128, aq + kk * (128 * 128 / 16),
+                    bk0 + ks * (C::STAGE / 16) + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
+        tc_commit_pair_mc_w(B.s_full(ks), 3);
+        if (++ks == C::NS) {
+          ks = 0;
+          kpar ^= 1;
+        }
       };
       bool ok = warp_wait<true>(B.q_full(), 0, abort_flag, p.err);
       for (int j = 0; ok && j < C::NS - 1 && j < nb; ++j) {
-        ok = warp_wait<!TMA>(B.k_full(j), 0, abort_flag, p.err);
+        ok = warp_wait<!TMA>(B.k_full(ks), kpar, abort_flag, p.err);
         tc_fence_after();
-        if (ok) qk(j);
+        if (ok) qk();
       }
+      bool rk = false;
       for (int j = 0; ok && j < nb; ++j) {
-        const int ahead = j + C::NS - 1;
-        const int sb = j % C::NS, sv = j % C::VST;
-        const uint32_t kb = B.k_full(ahead % C::NS), kp = (ahead / C::NS) & 1;
-        const uint32_t vb = B.v_full(sv), vp = (j / C::VST) & 1;
-        const uint32_t pb = B.p_full(sb), pp = (j / C::NS) & 1;
-        const bool more = ahead < nb;
-        // the 16-key steps that hold a key of the chunk (all but at its edges)
-        const int t0 = first + j * kTileKeys;
-        const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
-        const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
-        // K and V, which have usually arrived, are tested together (a wait costs
-        // some 200 cycles even where nothing is waited for, and one warp issues
-        // everything); the next scores do not wait for this tile's weights
-        bool rk = !more || (TMA && mbar_test(kb, kp));
-        bool rv = TMA && inner && mbar_test(vb, vp);
-        rk = __all_sync(0xffffffffu, rk);
-        rv = __all_sync(0xffffffffu, rv);
         // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
         // before: the tensor core takes a thread's MMAs in the order of issue.
-        if (more) {
-          if (!rk && !warp_wait<!TMA>(kb, kp, abort_flag, p.err)) break;
+        if (j + C::NS - 1 < nb) {
+          if (!rk && !warp_wait<!TMA>(B.k_full(ks), kpar, abort_flag, p.err)) break;
           tc_fence_after();
-          qk(ahead);
+          qk();
         }
-        if (!rv && !((TMA && inner) ? warp_wait(vb, vp, abort_flag, p.err)
-                                    : warp_wait<true>(vb, vp, abort_flag, p.err)))
+        // all but the edges of the chunk
+        const int t0 = first + j * kTileKeys;
+        const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
+        // What has usually arrived is tested together, without waiting: a wait
+        // costs some 200 cycles even where nothing is waited for, and one warp
+        // issues everything.
+        rk = TMA && mbar_test(B.k_full(ks), kpar);
+        bool rv = TMA && inner && mbar_test(B.v_full(vs), vpar);
+        bool rp = mbar_test(B.p_full(sp), ppar);
+        rk = __all_sync(0xffffffffu, rk);
+        rv = __all_sync(0xffffffffu, rv);
+        rp = __all_sync(0xffffffffu, rp);
+        if (!rv && !((TMA && inner) ? warp_wait(B.v_full(vs), vpar, abort_flag, p.err)
+                                    : warp_wait<true>(B.v_full(vs), vpar, abort_flag, p.err)))
           break;
-        if (!warp_wait(pb, pp, abort_flag, p.err)) break;
+        if (!rp && !warp_wait(B.p_full(sp), ppar, abort_flag, p.err)) break;
         tc_fence_after();
-        const uint32_t a = tmem + C::S_COL + sb * 128;
-        const uint32_t v = sm + C::OFF_V + sv * C::STAGE;
-        constexpr int STEP = (D == 64 ? 16 * 64 : 16 * 128) / 16;  // 16 keys
-        const uint64_t b = D == 64 ? sdesc_mn(v, 64, 0) : sdesc_mn(v, 128, 128 * 128);
+        const uint32_t a = tmem + C::S_COL + sp * 128;
+        const uint64_t b = bv0 + vs * (C::STAGE / 16);
         if (inner) {
           mma_ts_x4<STEP>(tmem, a, b, id_pv, j > 0 ? 1u : 0u);
           mma_ts_x4<STEP>(tmem, a + 32, b + 4 * STEP, id_pv, 1u);
         } else {
+          // the 16-key steps that hold a key of the chunk
+          const int ka = max(lo - t0, 0) >> 4, kz = (min(hi - t0, kTileKeys) + 15) >> 4;
           for (int kk = ka; kk < kz; ++kk)
             tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b + STEP * kk, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
         }
-        tc_commit_pair_mc_w(B.v_empty(sv), 3);
+        tc_commit_pair_mc_w(B.v_empty(vs), 3);
+        if (++sp == C::NS) {
+          sp = 0;
+          ppar ^= 1;
+        }
+        if (++vs == C::VST) {
+          vs = 0;
+          vpar ^= 1;
+        }
       }
       tc_commit_pair_mc_w(B.drain(), 3);
     }
