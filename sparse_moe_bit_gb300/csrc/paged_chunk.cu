@@ -17,8 +17,7 @@
 //
 // Bound: the tensor cores (4 D operations per row and key).  Their two products
 // of tile j and the softmax of tile j + 1 overlap: the order of issue is
-// QK(0), QK(1), PV(0), QK(2), PV(1), ... (one tile further ahead with three S
-// buffers).  Two groups of four warps take the even and the odd tiles, a thread a
+// QK(0), QK(1), PV(0), QK(2), PV(1), ... (one more ahead with three S buffers).  Two groups of four warps take the even and the odd tiles, a thread a
 // row, so that one group's exponentials run while the other waits or reduces;
 // they pass the reference maximum on from tile to tile.  It only moves when it
 // rises by more than 2^8 (weights then stay below 2^8, which fp32 sums and
@@ -54,15 +53,13 @@ template <int D>
 struct ChunkCfg {
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int STAGE = 128 * D;  // 64 keys, or half the features of 128 values
-  // S buffers in TMEM beside O's D columns (the scores run NS - 1 tiles ahead)
-  // and stages of K: the commit that announces a tile's scores also frees its
-  // K stage
+  // S buffers in TMEM beside O's D columns, and stages of K and of V: everything
+  // of a tile moves on together (see Bars)
   static constexpr int NS = D == 256 ? 2 : 3;
-  static constexpr int VST = D == 256 ? 2 : 4;  // stages of V
   static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + NS * STAGE;
-  static constexpr int OFF_BAR = OFF_V + VST * STAGE;
-  static constexpr int NUM_BARS = 2 + 3 * NS + 2 * VST;
+  static constexpr int OFF_BAR = OFF_V + NS * STAGE;
+  static constexpr int NUM_BARS = 2 + 3 * NS;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_REF = (OFF_MISC + 64 + 15) / 16 * 16;  // float [4][128]
   static constexpr int OFF_MAX = OFF_REF + 4 * 128 * 4;           // float [4][2][128]
@@ -76,17 +73,23 @@ struct ChunkCfg {
   static_assert(D <= S_COL, "TMEM budget");
 };
 
+// Barriers (the even CTA's unless said otherwise; t % NS in brackets).  The
+// issuing warp waits once and commits once a tile -- every wait, test or commit
+// costs it some 150 cycles, and the tensor core runs dry meanwhile:
+//   ready(j)  P(j) of both CTAs is in TMEM, V(j) and K(j + NS) in shared memory
+//   moved(t)  (both CTAs) QK(t) has completed, and with it P V(t - NS), issued
+//             before it: S(t) can be read; the stages of K(t) and V(t - NS) are
+//             free; O holds the products up to tile t - NS
+//   k_first   K(t), t < NS
 template <int D>
 struct Bars {
   using C = ChunkCfg<D>;
   uint32_t base;
   __device__ uint32_t q_full() const { return base; }
   __device__ uint32_t drain() const { return base + 8; }
-  __device__ uint32_t k_full(int s) const { return base + 8 * (2 + s); }
-  __device__ uint32_t s_full(int s) const { return base + 8 * (2 + C::NS + s); }
-  __device__ uint32_t p_full(int s) const { return base + 8 * (2 + 2 * C::NS + s); }
-  __device__ uint32_t v_full(int s) const { return base + 8 * (2 + 3 * C::NS + s); }
-  __device__ uint32_t v_empty(int s) const { return base + 8 * (2 + 3 * C::NS + C::VST + s); }
+  __device__ uint32_t moved(int s) const { return base + 8 * (2 + s); }
+  __device__ uint32_t ready(int s) const { return base + 8 * (2 + C::NS + s); }
+  __device__ uint32_t k_first(int s) const { return base + 8 * (2 + 2 * C::NS + s); }
 };
 
 // (CLUSTER: acquires what another CTA's threads wrote to shared memory by plain
@@ -110,6 +113,13 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+
+// Waits for the copies counted on `bar`, whatever else has given up.
+__device__ __forceinline__ void copies_done(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_sleep(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
 }
 
 // The whole warp waits; false when the limit has passed or another wait of the
@@ -373,13 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(B.q_full(), 2 * kSoftWarps);
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(B.k_full(i), 2);
-      mbar_init(B.s_full(i), 1);
-      mbar_init(B.p_full(i), kSoftWarps);  // one group's warps of both CTAs
-    }
-    for (int i = 0; i < C::VST; ++i) {
-      mbar_init(B.v_full(i), 2);
-      mbar_init(B.v_empty(i), 1);
+      mbar_init(B.moved(i), 1);
+      // one softmax group's warps of both CTAs, and each CTA's copying warps
+      mbar_init(B.ready(i), kSoftWarps + 4);
+      mbar_init(B.k_first(i), 2);
     }
     mbar_init(B.drain(), 1);
     *abort_flag = 0;
@@ -419,9 +426,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ keys (0) and values (2)
     const bool is_k = warp == 0;
     constexpr int KEYS_K = 64, KEYS_V = 128;
-    const uint32_t full0 = mapa_shared(is_k ? B.k_full(0) : B.v_full(0), 0);
     const uint32_t ring = sm + (is_k ? C::OFF_K : C::OFF_V);
-    const int stages = is_k ? C::NS : C::VST;
+    int sent = 0;  // tiles whose copies have been issued
+    // the barrier that K(j) or V(j) is announced on, and the wait for its stage
+    auto full_bar = [&](int j) {
+      return is_k && j < C::NS ? B.k_first(j) : B.ready(j % C::NS);
+    };
+    // (V(j), j < NS, waits for Q K(j) although its stage is empty: a parity names a
+    // phase only to who has seen the one before)
+    auto stage_free = [&](int j) -> bool {
+      if (is_k && j < C::NS) return true;
+      return warp_wait(B.moved(j % C::NS), (is_k ? (j / C::NS) - 1 : j / C::NS) & 1, abort_flag, p.err);
+    };
     const uint16_t* base = is_k ? p.c.k + h * p.c.head_stride
                                 : p.c.v + h * p.c.head_stride + rank * (D / 2);
     // rows [i0, i0 + 32) of a stage by 16-byte copies, lane l's row at element
@@ -470,27 +486,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       look(0);
-      int st = 0;
-      uint32_t par = 1;
       for (int j = 0; j < nb; ++j) {
-        const uint32_t full = full0 + 8 * st;
-        const uint32_t dst = ring + st * C::STAGE;
+        const uint32_t bar = full_bar(j), full = mapa_shared(bar, 0);
+        const uint32_t dst = ring + (j % C::NS) * C::STAGE;
         const int t0 = first + j * kTileKeys;
         // rows of the tile that hold keys of the chunk, [e0, e1), and the boxes
         // that are loaded: all with such a row (K); those with no other row (V)
         const int e0 = max(lo - t0, 0), e1 = min(hi - t0, kTileKeys);
         const int up = is_k ? 0 : box - 1, dn = is_k ? box - 1 : 0;
         const int w0 = (e0 + up) & ~(box - 1), w1 = (e1 + dn) & ~(box - 1);
-        if (!warp_wait(is_k ? B.s_full(st) : B.v_empty(st), par, abort_flag, p.err)) break;
+        if (!stage_free(j)) break;
         if (rank == 0 && lane == 0) {
           const uint32_t bytes = (uint32_t)max(w1 - w0, 0) * D * 2;  // both CTAs'
-          const uint32_t bar = is_k ? B.k_full(st) : B.v_full(st);
           asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
                        : "memory");
         }
         if (mine && row0 >= w0 && row0 < w1)
           tma_box_pair(dst + at, is_k ? &cp.k : &cp.v, feature, page_row, h,
                        (page < 0 || page > p.c.pages) ? p.c.pages : page, full);
+        sent = j + 1;
         look(j + 1);
         bool copied = false;
         if (!is_k && (e0 > 0 || w1 < kTileKeys)) {
@@ -513,19 +527,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (copied) arrive_release_cluster(full);
           else mbar_arrive_cluster(full);
         }
-        if (++st == stages) {
-          st = 0;
-          par ^= 1;
-        }
       }
     } else {
       for (int j = 0; j < nb; ++j) {
-        const int st = j % stages;
-        const uint32_t dst = ring + st * C::STAGE;
+        const uint32_t dst = ring + (j % C::NS) * C::STAGE;
         const int t0 = first + j * kTileKeys;
-        if (!warp_wait(is_k ? B.s_full(st) : B.v_empty(st), ((j / stages) & 1) ^ 1, abort_flag,
-                       p.err))
-          break;
+        if (!stage_free(j)) break;
+        sent = j + 1;
 #pragma unroll
         for (int i0 = 0; i0 < KEYS_V; i0 += 32) {
           if (is_k && i0 >= KEYS_K) break;
@@ -537,13 +545,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_release_cluster(full0 + 8 * st);
+        if (lane == 0) arrive_release_cluster(mapa_shared(full_bar(j), 0));
       }
     }
     cp_async_wait<0>();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
+    // No CTA leaves while a copy of the pair is in flight (in the usual course
+    // the products have waited for all of them; after a wait has given up
+    // nothing has): the even CTA's barriers count the bytes of both.
     if (rank == 0) {
+      for (int j = max(sent - C::NS, 0); j < sent; ++j)
+        copies_done(full_bar(j), is_k ? (j < C::NS ? 0 : ((j / C::NS) - 1) & 1) : (j / C::NS) & 1);
+    }
+    // The last tiles have no K(j + NS) to wait for.  (After the wait above, which
+    // these arrivals' phases could otherwise overtake.)
+    if (is_k && sent == nb) {
+      for (int j = max(nb, C::NS); j < nb + C::NS; ++j) {
+        if (!stage_free(j)) break;
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(full_bar(j), 0));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- MMA issuer
+    const int nb_all = nb, lo_all = lo, hi_all = hi, first_all = first;
+    const uint32_t tmem_all = tmem, sm_all = sm;
+    // One warp issues everything, in the order P V(j), Q K(j + NS): P(j) gives
+    // way to the scores of tile j + NS without a wait, since the tensor core
+    // takes a thread's MMAs in the order of issue.  (Two warps, one for each
+    // product, had their MMAs interleaved and both finished late.)
+    if (rank == 0 && warp == 1) {
+      // broadcast, so that the compiler knows them to be the same in all lanes and
+      // keeps operands and counters in uniform registers, which the MMAs take
+      const int nb = __shfl_sync(0xffffffffu, nb_all, 0), lo = __shfl_sync(0xffffffffu, lo_all, 0);
+      const int hi = __shfl_sync(0xffffffffu, hi_all, 0), first = __shfl_sync(0xffffffffu, first_all, 0);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_all, 0), sm = __shfl_sync(0xffffffffu, sm_all, 0);
+      const Bars<D> B{sm + C::OFF_BAR};
       const uint32_t id_qk = idesc_f16(256, kTileKeys, BF ? 1 : 0);
       const uint32_t id_pv = idesc_f16(256, D, BF ? 1 : 0) | (1u << 16);  // B: N contiguous
       const uint64_t aq = sdesc_k_sw128(sm);
@@ -551,54 +586,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t bv0 = D == 64 ? sdesc_mn(sm + C::OFF_V, 64, 0)
                                    : sdesc_mn(sm + C::OFF_V, 128, 128 * 128);
       constexpr int STEP = (D == 64 ? 16 * 64 : 16 * 128) / 16;  // descriptor units of 16 keys
-      // ring slots and phase parities of the scores' tile and of the products'
-      int ks = 0, sp = 0, vs = 0;
-      uint32_t kpar = 0, ppar = 0, vpar = 0;
-      auto qk = [&]() {
+      auto qk = [&](int s) {
 #pragma unroll
         for (int kk = 0; kk < D / 64; ++kk)
-          mma_ss_x4(tmem + C::S_COL + ks * 128, aq + kk * (128 * 128 / 16),
-                    bk0 + ks * (C::STAGE / 16) + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
-        tc_commit_pair_mc_w(B.s_full(ks), 3);
-        if (++ks == C::NS) {
-          ks = 0;
-          kpar ^= 1;
-        }
+          mma_ss_x4(tmem + C::S_COL + s * 128, aq + kk * (128 * 128 / 16),
+                    bk0 + s * (C::STAGE / 16) + kk * (64 * 128 / 16), id_qk, kk ? 1u : 0u);
       };
       bool ok = warp_wait<true>(B.q_full(), 0, abort_flag, p.err);
-      for (int j = 0; ok && j < C::NS - 1 && j < nb; ++j) {
-        ok = warp_wait<!TMA>(B.k_full(ks), kpar, abort_flag, p.err);
+      for (int t = 0; ok && t < min(C::NS, nb); ++t) {
+        ok = warp_wait<!TMA>(B.k_first(t), 0, abort_flag, p.err);
         tc_fence_after();
-        if (ok) qk();
-      }
-      bool rk = false;
-      for (int j = 0; ok && j < nb; ++j) {
-        // The S buffer of tile j + NS - 1 held P(j - 1), whose product was issued
-        // before: the tensor core takes a thread's MMAs in the order of issue.
-        if (j + C::NS - 1 < nb) {
-          if (!rk && !warp_wait<!TMA>(B.k_full(ks), kpar, abort_flag, p.err)) break;
-          tc_fence_after();
-          qk();
+        if (ok) {
+          qk(t);
+          tc_commit_pair_mc_w(B.moved(t), 3);
         }
-        // all but the edges of the chunk
+      }
+      int s = 0;
+      uint32_t par = 0;
+      for (int j = 0; ok && j < nb; ++j) {
         const int t0 = first + j * kTileKeys;
-        const bool inner = t0 >= lo && t0 + kTileKeys <= hi;
-        // What has usually arrived is tested together, without waiting: a wait
-        // costs some 200 cycles even where nothing is waited for, and one warp
-        // issues everything.
-        rk = TMA && mbar_test(B.k_full(ks), kpar);
-        bool rv = TMA && inner && mbar_test(B.v_full(vs), vpar);
-        bool rp = mbar_test(B.p_full(sp), ppar);
-        rk = __all_sync(0xffffffffu, rk);
-        rv = __all_sync(0xffffffffu, rv);
-        rp = __all_sync(0xffffffffu, rp);
-        if (!rv && !((TMA && inner) ? warp_wait(B.v_full(vs), vpar, abort_flag, p.err)
-                                    : warp_wait<true>(B.v_full(vs), vpar, abort_flag, p.err)))
+        const bool inner = t0 >= lo && t0 + kTileKeys <= hi;  // not at the chunk's edges
+        if (!((TMA && inner) ? warp_wait(B.ready(s), par, abort_flag, p.err)
+                             : warp_wait<true>(B.ready(s), par, abort_flag, p.err)))
           break;
-        if (!rp && !warp_wait(B.p_full(sp), ppar, abort_flag, p.err)) break;
         tc_fence_after();
-        const uint32_t a = tmem + C::S_COL + sp * 128;
-        const uint64_t b = bv0 + vs * (C::STAGE / 16);
+        const uint32_t a = tmem + C::S_COL + s * 128;
+        const uint64_t b = bv0 + s * (C::STAGE / 16);
         if (inner) {
           mma_ts_x4<STEP>(tmem, a, b, id_pv, j > 0 ? 1u : 0u);
           mma_ts_x4<STEP>(tmem, a + 32, b + 4 * STEP, id_pv, 1u);
@@ -608,20 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = ka; kk < kz; ++kk)
             tc_mma_f16_ts_pair_w(tmem, a + 8 * kk, b + STEP * kk, id_pv, (j > 0 || kk > ka) ? 1u : 0u);
         }
-        tc_commit_pair_mc_w(B.v_empty(vs), 3);
-        if (++sp == C::NS) {
-          sp = 0;
-          ppar ^= 1;
-        }
-        if (++vs == C::VST) {
-          vs = 0;
-          vpar ^= 1;
+        if (j + C::NS < nb) qk(s);
+        tc_commit_pair_mc_w(B.moved(s), 3);
+        if (++s == C::NS) {
+          s = 0;
+          par ^= 1;
         }
       }
       tc_commit_pair_mc_w(B.drain(), 3);
     }
     // every MMA has finished before TMEM is released
-    if (lane == 0) mbar_wait_bounded(B.drain(), 0, abort_flag, kWaitLimitNs);
+    if (warp == 1 && lane == 0) mbar_wait_bounded(B.drain(), 0, abort_flag, kWaitLimitNs);
   }
   } else {
     // ------------------------------------------- softmax, correction, epilogue
@@ -667,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sh_ref = reinterpret_cast<float*>(smem + C::OFF_REF);
     float* sh_max = reinterpret_cast<float*>(smem + C::OFF_MAX);
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t p_full0 = mapa_shared(B.p_full(0), 0);
+    const uint32_t ready0 = mapa_shared(B.ready(0), 0);
     const float c = p.scale_log2;
     // the reference that this thread's sum l (over its own scores) is relative to
     float m = kNegInf, l = 0.f;
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = group; j < nb; j += 2) {
       const int sb = j % C::NS;
-      ok = ok && warp_wait(B.s_full(sb), (j / C::NS) & 1, abort_flag, p.err);
+      ok = ok && warp_wait(B.moved(sb), (j / C::NS) & 1, abort_flag, p.err);
       tc_fence_after();
       const uint32_t ts = tmem + lanes + C::S_COL + sb * 128;
       uint32_t x[2][32];
@@ -731,9 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (__any_sync(0xffffffffu, now != m)) {
         if (j > 0 && __any_sync(0xffffffffu, rise)) {
-          // P V of the tiles before has been added up before O changes (the
-          // commit that freed tile j - 1's stage of V)
-          ok = ok && warp_wait(B.v_empty((j - 1) % C::VST), ((j - 1) / C::VST) & 1, abort_flag, p.err);
+          // P V of the tiles before has been added up before O changes
+          ok = ok && warp_wait(B.moved((j - 1) % C::NS), ((j - 1) / C::NS + 1) & 1, abort_flag, p.err);
           tc_fence_after();
           const float f = rise ? ex2((ref - now) * c) : 1.f;
 #pragma unroll 1
@@ -780,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       // (what this arrival publishes lies in TMEM, ordered by the tcgen05 fences;
       // a release at cluster scope here costs several hundred cycles a tile)
-      if (lane == 0) mbar_arrive_cluster(p_full0 + 8 * sb);
+      if (lane == 0) mbar_arrive_cluster(ready0 + 8 * sb);
     }
     // ---- epilogue: a quarter of the features each
     ok = ok && warp_wait(B.drain(), 0, abort_flag, p.err);
