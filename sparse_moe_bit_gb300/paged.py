@@ -7,6 +7,7 @@ how).  Every call enqueues on ``stream`` (default: torch's current one)."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -24,20 +25,20 @@ _DTYPE = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
-                ("pages", ctypes.c_int), ("page", ctypes.c_int), ("heads", ctypes.c_int),
-                ("dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
-                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
-
-
-class _Batch(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
-                ("kv_len", ctypes.c_void_p), ("N", ctypes.c_int), ("T", ctypes.c_int),
-                ("width", ctypes.c_int), ("table_stride", ctypes.c_int64)]
+# paged_cache and paged_batch of include/paged.h, packed (the calls of a decode
+# step are over in a few microseconds: building ctypes structures would double
+# their host time)
+_CACHE = struct.Struct("@PPiiiiiqqq")
+_BATCH = struct.Struct("@PPPiiiq")
 
 
 _lib = None
+
+
+def _check(status):
+    if status:
+        _moe._check(status)
+
 
 
 def _library():
@@ -47,7 +48,7 @@ def _library():
     lib = _moe.load_library()
     P, I, L, F, D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                      ctypes.c_double)
-    C, B = ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
+    C = B = ctypes.c_char_p
     sig = {
         "rope": [P, P, I, I, I, I, L, L, L, L, P, P, I, F, I, I, P],
         "rope_frequencies": [I, D, I, D, D, D, D, P, P],
@@ -75,27 +76,59 @@ def _need(ok, msg):
 
 
 def _i32(t, ndim, name):
-    _need(t.dtype is torch.int32 and t.dim() == ndim, f"{name} must be int32 with {ndim} axes")
-    _need(t.shape[-1] <= 1 or t.stride(-1) == 1, f"{name} must be contiguous along its last axis")
+    if t.dtype is not torch.int32 or t.dim() != ndim:
+        raise ValueError(f"{name} must be int32 with {ndim} axes")
+    if not t.is_contiguous() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+
+
+def _stream(stream, t) -> int:
+    """The raw stream: the given one, or torch's current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    return _raw_stream(t.get_device())
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _made(stream, *tensors):
+    """Tensors made here lie in the current stream's pool: tell the allocator of the
+    other stream that uses them."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _cache(k, v):
-    _need(k.dim() == 4 and k.dtype is v.dtype and k.shape == v.shape and k.stride() == v.stride(),
-          "k_pages and v_pages must be [pages, page, heads, dim] of one type, shape and strides")
-    _need(k.stride(3) == 1, "a head's features must be contiguous")
-    s = k.stride()
-    return _Cache(k.data_ptr(), v.data_ptr(), _DTYPE.get(k.dtype, 0), k.shape[0], k.shape[1],
-                  k.shape[2], k.shape[3], s[0], s[1], s[2])
+    shape, st = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != st or k.dtype is not v.dtype or st[3] != 1:
+        raise ValueError("k_pages and v_pages must be [pages, page, heads, dim] of one type, shape "
+                         "and strides, a head's features contiguous")
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), _DTYPE.get(k.dtype, 0), *shape, *st[:3])
 
 
 def _batch(table, cu_q, kv_len, T):
     _i32(table, 2, "table")
     _i32(cu_q, 1, "cu_q")
     _i32(kv_len, 1, "kv_len")
-    n = table.shape[0]
-    _need(cu_q.shape[0] == n + 1 and kv_len.shape[0] == n, "cu_q is [N + 1], kv_len [N], table [N, width]")
-    return _Batch(table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, T, table.shape[1],
-                  table.stride(0))
+    n, width = table.shape
+    if cu_q.shape[0] != n + 1 or kv_len.shape[0] != n:
+        raise ValueError("cu_q is [N + 1], kv_len [N], table [N, width]")
+    return _BATCH.pack(table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), n, T, width,
+                       table.stride(0))
+
+
+def _freq(freq):
+    if freq.dtype is not torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise ValueError("freq must be fp64 [r]")
+    return freq.data_ptr(), freq.shape[0]
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -108,7 +141,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     _need(scaling in SCALINGS, f"unknown scaling {scaling!r}")
     f = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
     m = ctypes.c_double(1.0)
-    _moe._check(_library().rope_frequencies(rotary_dim, base, SCALINGS[scaling], factor,
+    _check(_library().rope_frequencies(rotary_dim, base, SCALINGS[scaling], factor,
                                             float(original), low, high, f.data_ptr(),
                                             ctypes.byref(m)))
     return (f if device is None else f.to(device)), m.value
@@ -120,19 +153,25 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, mscale: f
     """Turn the first ``2 * len(freq)`` features of every head of x [T, H, D]
     (bf16, fp16 or fp32) by its token's position.  ``inverse`` turns back: the
     gradient of the call.  ``out`` may be x."""
-    _need(x.dim() == 3 and x.dtype in _DTYPE, "x must be [T, H, D] of bf16, fp16 or fp32")
+    dt = _DTYPE.get(x.dtype)
+    if dt is None or x.dim() != 3:
+        raise ValueError("x must be [T, H, D] of bf16, fp16 or fp32")
     T, H, D = x.shape
     _i32(positions, 1, "positions")
-    _need(positions.shape[0] == T, "one position a token")
-    _need(freq.dtype is torch.float64 and freq.dim() == 1 and freq.is_contiguous(), "freq must be fp64 [r]")
+    if positions.shape[0] != T:
+        raise ValueError("one position a token")
+    f, r = _freq(freq)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    _need(out.shape == x.shape and out.dtype is x.dtype, "out must be like x")
-    _need(D == 1 or (x.stride(2) == 1 and out.stride(2) == 1), "features must be contiguous")
-    _moe._check(_library().rope(x.data_ptr(), out.data_ptr(), _DTYPE[x.dtype], T, H, D,
-                                x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-                                positions.data_ptr(), freq.data_ptr(), freq.shape[0], mscale,
-                                interleaved, inverse, _moe._stream(stream)))
+        out = x.new_empty((T, H, D))
+    elif out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError("out must be like x")
+    xs, os_ = x.stride(), out.stride()
+    if D > 1 and (xs[2] != 1 or os_[2] != 1):
+        raise ValueError("features must be contiguous")
+    _check(_library().rope(x.data_ptr(), out.data_ptr(), dt, T, H, D, xs[0], xs[1], os_[0], os_[1],
+                           positions.data_ptr(), f, r, mscale, interleaved, inverse,
+                           _stream(stream, x)))
+    _made(stream, out)
     return out
 
 
@@ -150,18 +189,24 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torc
     int32 [N + 1], kv_len int32 [N] (new tokens included), freq fp64 [r]."""
     T, Hq, D = q.shape
     c = _cache(k_pages, v_pages)
-    for t, h in ((q, Hq), (k, c.heads), (v, c.heads)):
-        _need(t.dtype is k_pages.dtype and t.shape == (T, h, c.dim), "q, k, v must match the cache's type, heads and dim")
-        _need(t.stride(2) == 1 and (h == 1 or t.stride(1) == D), "heads must be D apart")
-    _need(freq.dtype is torch.float64 and freq.dim() == 1 and freq.is_contiguous(), "freq must be fp64 [r]")
+    dt, hk = k_pages.dtype, k_pages.shape[2]
+    kv = (T, hk, k_pages.shape[3])
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if (D != kv[2] or k.shape != kv or v.shape != kv or q.dtype is not dt or k.dtype is not dt
+            or v.dtype is not dt):
+        raise ValueError("q, k, v must match the cache's type, heads and dim")
+    if (qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or (Hq > 1 and qs[1] != D)
+            or (hk > 1 and (ks[1] != D or vs[1] != D))):
+        raise ValueError("heads must be D apart")
+    f, r = _freq(freq)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _need(q_out.shape == q.shape and q_out.dtype is q.dtype and q_out.is_contiguous(), "q_out must be dense and like q")
-    b = _batch(table, cu_q, kv_len, T)
-    _moe._check(_library().rope_append(
-        q.data_ptr(), q.stride(0), q_out.data_ptr(), Hq, k.data_ptr(), k.stride(0), v.data_ptr(),
-        v.stride(0), ctypes.byref(c), ctypes.byref(b), freq.data_ptr(), freq.shape[0], mscale,
-        interleaved, _moe._stream(stream)))
+        q_out = q.new_empty((T, Hq, D))
+    elif q_out.shape != q.shape or q_out.dtype is not dt or not q_out.is_contiguous():
+        raise ValueError("q_out must be dense and like q")
+    _check(_library().rope_append(q.data_ptr(), qs[0], q_out.data_ptr(), Hq, k.data_ptr(), ks[0],
+                                  v.data_ptr(), vs[0], c, _batch(table, cu_q, kv_len, T), f, r,
+                                  mscale, interleaved, _stream(stream, q)))
+    _made(stream, q_out)
     return q_out
 
 
@@ -181,26 +226,33 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     lib = _library()
     T, Hq, D = q.shape
     c = _cache(k_pages, v_pages)
-    _need(q.dtype is k_pages.dtype and D == c.dim, "q must match the cache's type and dim")
+    if q.dtype is not k_pages.dtype or D != k_pages.shape[3]:
+        raise ValueError("q must match the cache's type and dim")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    _need(out.shape == q.shape and out.dtype is q.dtype, "out must be like q")
-    _need(q.stride(2) == 1 and out.stride(2) == 1, "features must be contiguous")
+        out = q.new_empty((T, Hq, D))
+    elif out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must be like q")
+    qs, os_ = q.stride(), out.stride()
+    if qs[2] != 1 or os_[2] != 1:
+        raise ValueError("features must be contiguous")
     b = _batch(table, cu_q, kv_len, T)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
     if scale is None:
         scale = D ** -0.5
-    need = ctypes.c_size_t(0)
-    _moe._check(lib.paged_attention_workspace(ctypes.byref(c), ctypes.byref(b), Hq, window, max_q,
-                                              max_kv, ctypes.byref(need)))
-    if workspace is None and need.value:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _moe._check(lib.paged_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), Hq, ctypes.byref(c), ctypes.byref(b), scale, causal,
-        window, max_q, max_kv, out.data_ptr(), out.stride(0), out.stride(1),
-        None if lse is None else lse.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), size, _moe._stream(stream)))
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(lib.paged_attention_workspace(c, b, Hq, window, max_q, max_kv, ctypes.byref(need)))
+        size, ws = need.value, None
+        if size:
+            workspace = q.new_empty((size,), dtype=torch.uint8)
+            ws = workspace.data_ptr()
+    else:
+        size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    _check(lib.paged_attention(q.data_ptr(), qs[0], qs[1], Hq, c, b, scale, causal, window, max_q,
+                               max_kv, out.data_ptr(), os_[0], os_[1],
+                               None if lse is None else lse.data_ptr(), ws, size,
+                               _stream(stream, q)))
+    _made(stream, out, lse, workspace)
     return (out, lse) if return_lse else out
 
 
@@ -209,7 +261,8 @@ def _state(refs, table, lens=None):
     _i32(table, 2, "table")
     if lens is not None:
         _i32(lens, 1, "lens")
-        _need(lens.shape[0] == table.shape[0], "one length a slot of the table")
+        if lens.shape[0] != table.shape[0]:
+            raise ValueError("one length a slot of the table")
     return refs.data_ptr(), refs.shape[0], table.data_ptr(), table.stride(0), table.shape[1]
 
 
@@ -221,11 +274,12 @@ def pages_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, src:
     st = _state(refs, table, lens)
     _i32(src, 1, "src")
     _i32(dst, 1, "dst")
-    _need(src.shape == dst.shape, "src and dst must have one length")
-    _moe._check(_library().pages_fork(*st, lens.data_ptr(), lens.shape[0], src.data_ptr(),
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have one length")
+    _check(_library().pages_fork(*st, lens.data_ptr(), lens.shape[0], src.data_ptr(),
                                       dst.data_ptr(), src.shape[0],
                                       None if refused is None else refused.data_ptr(),
-                                      _moe._stream(stream)))
+                                      _stream(stream, refs)))
 
 
 def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, add: torch.Tensor,
@@ -238,12 +292,15 @@ def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, a
     st = _state(refs, table, lens)
     _i32(add, 1, "add")
     S = lens.shape[0]
-    _need(add.shape[0] == S, "one number a slot")
-    buf = torch.empty(3 * S + 3, dtype=torch.int32, device=refs.device)
-    moves, status, scratch = buf[:2 * S].view(S, 2), buf[2 * S:2 * S + 2], buf[2 * S + 2:]
-    _moe._check(_library().pages_reserve(*st, lens.data_ptr(), add.data_ptr(), S, page,
-                                         moves.data_ptr(), status.data_ptr(), scratch.data_ptr(),
-                                         _moe._stream(stream)))
+    if add.shape[0] != S:
+        raise ValueError("one number a slot")
+    buf = refs.new_empty((3 * S + 3,))   # moves, status, scratch
+    moves, status = buf.as_strided((S, 2), (2, 1)), buf.as_strided((2,), (1,), 2 * S)
+    at = buf.data_ptr()
+    _check(_library().pages_reserve(*st, lens.data_ptr(), add.data_ptr(), S, page,
+                                         at, at + 8 * S, at + 8 * S + 8,
+                                         _stream(stream, refs)))
+    _made(stream, buf)
     return moves, status
 
 
@@ -252,8 +309,8 @@ def pages_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slot
     """The slots give up their pages, in place."""
     st = _state(refs, table, lens)
     _i32(slots, 1, "slots")
-    _moe._check(_library().pages_free(*st, lens.data_ptr(), lens.shape[0], slots.data_ptr(),
-                                      slots.shape[0], _moe._stream(stream)))
+    _check(_library().pages_free(*st, lens.data_ptr(), lens.shape[0], slots.data_ptr(),
+                                      slots.shape[0], _stream(stream, refs)))
 
 
 def pages_compact(refs: torch.Tensor, table: torch.Tensor, stream=None):
@@ -261,10 +318,12 @@ def pages_compact(refs: torch.Tensor, table: torch.Tensor, stream=None):
     int32 [P, 2] and their count (int32 scalar), for pages_copy."""
     st = _state(refs, table)
     P = refs.shape[0]
-    buf = torch.empty(3 * P + 2, dtype=torch.int32, device=refs.device)
-    moves, count, scratch = buf[:2 * P].view(P, 2), buf[2 * P], buf[2 * P + 1:]
-    _moe._check(_library().pages_compact(*st, table.shape[0], moves.data_ptr(), count.data_ptr(),
-                                         scratch.data_ptr(), _moe._stream(stream)))
+    buf = refs.new_empty((3 * P + 2,))   # moves, count, scratch
+    moves, count = buf.as_strided((P, 2), (2, 1)), buf.as_strided((), (), 2 * P)
+    at = buf.data_ptr()
+    _check(_library().pages_compact(*st, table.shape[0], at, at + 8 * P,
+                                         at + 8 * P + 4, _stream(stream, refs)))
+    _made(stream, buf)
     return moves, count
 
 
@@ -273,20 +332,23 @@ def pages_copy(pools: torch.Tensor, moves: torch.Tensor, count: torch.Tensor | N
     """Copy the rows of page moves[i, 0] to page moves[i, 1] in every array of
     pools [B, P, ...] (keys and values of all layers; what a page holds is
     contiguous).  ``count``: only the first so many moves (int32, on the GPU)."""
-    _need(pools.dim() >= 3, "pools must be [B, P, ...]")
+    shape, st, es = pools.shape, pools.stride(), pools.element_size()
+    if len(shape) < 3:
+        raise ValueError("pools must be [B, P, ...]")
     _i32(moves, 2, "moves")
-    _need(moves.shape[1] == 2 and (moves.shape[0] <= 1 or moves.stride(0) == 2), "moves must be dense [M, 2]")
-    es = pools.element_size()
+    if moves.shape[1] != 2 or (moves.shape[0] > 1 and moves.stride(0) != 2):
+        raise ValueError("moves must be dense [M, 2]")
     n = 1
-    for size, stride in zip(reversed(pools.shape[2:]), reversed(pools.stride()[2:])):
-        _need(size == 1 or stride == n, "a page's rows must be contiguous")
-        n *= size
-    _need(count is None or count.dtype is torch.int32, "count must be int32")
-    _moe._check(_library().pages_copy(pools.data_ptr(), pools.shape[0], pools.stride(0) * es,
-                                      pools.shape[1], pools.stride(1) * es, n * es,
-                                      moves.data_ptr(), moves.shape[0],
-                                      None if count is None else count.data_ptr(),
-                                      _moe._stream(stream)))
+    for i in range(len(shape) - 1, 1, -1):
+        if shape[i] != 1 and st[i] != n:
+            raise ValueError("a page's rows must be contiguous")
+        n *= shape[i]
+    if count is not None and count.dtype is not torch.int32:
+        raise ValueError("count must be int32")
+    _check(_library().pages_copy(pools.data_ptr(), shape[0], st[0] * es, shape[1], st[1] * es,
+                                 n * es, moves.data_ptr(), moves.shape[0],
+                                 None if count is None else count.data_ptr(),
+                                 _stream(stream, pools)))
 
 
 def paged_device_error(stream=None) -> int:
@@ -295,5 +357,5 @@ def paged_device_error(stream=None) -> int:
     code = ctypes.c_int(0)
     st = _library().paged_get_device_error(_moe._stream(stream), ctypes.byref(code))
     if st not in (0, 5):
-        _moe._check(st)
+        _check(st)
     return code.value

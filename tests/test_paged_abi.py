@@ -31,19 +31,39 @@ def test_header_and_binding_agree(lib):
         assert hasattr(lib, n)
 
 
-def _cache(**kw):
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page", ctypes.c_int), ("heads", ctypes.c_int),
+                ("dim", ctypes.c_int), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("N", ctypes.c_int), ("T", ctypes.c_int),
+                ("width", ctypes.c_int), ("table_stride", ctypes.c_int64)]
+
+
+def test_binding_packs_the_structures(lib):
     from sparse_moe_bit_gb300 import paged
+    assert paged._CACHE.size == ctypes.sizeof(_Cache) and paged._BATCH.size == ctypes.sizeof(_Batch)
+    c = _Cache.from_buffer_copy(paged._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10))
+    assert [getattr(c, n) for n, _ in _Cache._fields_] == list(range(1, 11))
+    b = _Batch.from_buffer_copy(paged._BATCH.pack(1, 2, 3, 4, 5, 6, 7))
+    assert [getattr(b, n) for n, _ in _Batch._fields_] == list(range(1, 8))
+
+
+def _cache(**kw):
     a = dict(k=_A, v=_A, dtype=1, pages=8, page=16, heads=2, dim=128, page_stride=16 * 256,
              row_stride=256, head_stride=128)
     a.update(kw)
-    return paged._Cache(**a)
+    return bytes(_Cache(**a))
 
 
 def _batch(**kw):
-    from sparse_moe_bit_gb300 import paged
     a = dict(table=_A, cu_q=_A, kv_len=_A, N=2, T=4, width=4, table_stride=4)
     a.update(kw)
-    return paged._Batch(**a)
+    return bytes(_Batch(**a))
 
 
 CACHE_BAD = [(dict(k=None), 1), (dict(v=_A + 8), 1), (dict(dtype=3), 1), (dict(dtype=0), 1),
@@ -58,8 +78,8 @@ def _attend(lib, c=None, b=None, **kw):
              o=_A, o_ts=1024, o_hs=128, lse=None, ws=None, ws_bytes=0)
     a.update(kw)
     c, b = c or _cache(), b or _batch()
-    return lib.paged_attention(a["q"], a["q_ts"], a["q_hs"], a["Hq"], ctypes.byref(c),
-                               ctypes.byref(b), a["scale"], a["causal"], a["window"], a["max_q"],
+    return lib.paged_attention(a["q"], a["q_ts"], a["q_hs"], a["Hq"], c,
+                               b, a["scale"], a["causal"], a["window"], a["max_q"],
                                a["max_kv"], a["o"], a["o_ts"], a["o_hs"], a["lse"], a["ws"],
                                a["ws_bytes"], None)
 
@@ -80,9 +100,9 @@ def test_bad_cache_is_rejected(lib, kw, status):
     assert _attend(lib, c=_cache(**kw)) == status
     n = ctypes.c_size_t()
     c, b = _cache(**kw), _batch()
-    assert lib.paged_attention_workspace(ctypes.byref(c), ctypes.byref(b), 8, 0, 1, 64,
+    assert lib.paged_attention_workspace(c, b, 8, 0, 1, 64,
                                          ctypes.byref(n)) == status
-    assert lib.rope_append(_A, 1024, _A, 8, _A, 256, _A, 256, ctypes.byref(c), ctypes.byref(b), _A,
+    assert lib.rope_append(_A, 1024, _A, 8, _A, 256, _A, 256, c, b, _A,
                            16, 1.0, 0, None) == status
 
 
@@ -96,7 +116,7 @@ def test_attention_needs_its_workspace(lib):
     workspace that the split needs is refused."""
     c, b = _cache(pages=4096), _batch(N=1, T=1, width=4096, table_stride=4096)
     n = ctypes.c_size_t()
-    assert lib.paged_attention_workspace(ctypes.byref(c), ctypes.byref(b), 8, 0, 1, 65536,
+    assert lib.paged_attention_workspace(c, b, 8, 0, 1, 65536,
                                          ctypes.byref(n)) == 0
     assert n.value > 0
     assert _attend(lib, c=c, b=b, max_kv=65536, ws=_A, ws_bytes=n.value - 1) == 1
@@ -109,7 +129,7 @@ def test_empty_batches_are_no_ops(lib):
     assert _attend(lib, b=_batch(N=0, table=None, cu_q=None, kv_len=None)) == 0
     assert _attend(lib, b=_batch(T=0), q=None, o=None) == 0
     c, b = _cache(), _batch(T=0)
-    assert lib.rope_append(None, 0, None, 8, None, 0, None, 0, ctypes.byref(c), ctypes.byref(b),
+    assert lib.rope_append(None, 0, None, 8, None, 0, None, 0, c, b,
                            _A, 16, 1.0, 0, None) == 0
     assert lib.rope(None, None, 1, 0, 4, 64, 256, 64, 256, 64, None, _A, 8, 1.0, 0, 0, None) == 0
     assert lib.pages_copy(None, 0, 0, 4, 64, 64, None, 0, None, None) == 0
@@ -140,7 +160,7 @@ def test_append_rejects_bad_arguments(lib, kw):
     a.update(kw)
     c, b = _cache(), _batch()
     assert lib.rope_append(a["q"], a["q_ts"], a["q_out"], a["Hq"], a["k"], 256, a["v"], 256,
-                           ctypes.byref(c), ctypes.byref(b), a["freq"], a["r"], a["mscale"], 0,
+                           c, b, a["freq"], a["r"], a["mscale"], 0,
                            None) == 1
 
 
