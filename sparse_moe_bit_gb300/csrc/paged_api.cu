@@ -107,24 +107,23 @@ moe_status check_rope(int D, const double* freq, int r, float mscale) {
   return MOE_OK;
 }
 
-// Choice of kernel and split for one call; see plan().
+// Choice of kernel and split for one call.
 struct Plan {
   bool wide;  // 256-row tiles on the tensor cores, else 16-row tiles
-  int tiles, chunks, chunk;
-  size_t ws;
+  int tiles, chunks, chunk;  // 256-row tiles
+  int warps;                 // 16-row tiles
+  size_t ml, before, ws;     // offsets of the partial maxima and sums, of the counts; total bytes
 };
 
 // 16-row tiles while one holds the longest chunk's rows (each tile reads the
 // keys again), 256-row tiles above.
 //
-// 16-row tiles: enough chunks that the work items make three waves of the CTAs
-// an SM holds (one of head dim 256, two of 128, three of 64), which evens out
-// ragged contexts; no chunk below 256 keys, where a CTA's start and the join
-// cost more than they spread.
-// 256-row tiles: chunks only while the pairs of CTAs leave SMs without work;
-// none below 512 keys.
+// 16-row tiles: as many warps as the SMs hold (four a CTA; one CTA of head dim
+// 256, two of 128, three of 64), but at least two groups of 16 keys for each.
+// 256-row tiles: split over the keys only while the pairs of CTAs leave SMs
+// without work; no chunk below 512 keys.
 Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv) {
-  Plan r;
+  Plan r{};
   const int G = Hq / c.heads;
   long long mq = max_q > 0 ? max_q : b.T;
   if (mq > b.T) mq = b.T;
@@ -134,33 +133,36 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
   const long long rows = r.wide ? kPairRows : kRowTile;
   long long span = kv;
   if (window > 0 && window + rows < span) span = window + rows;
-  long long tiles, items, target, least, step;
+  r.tiles = r.chunks = r.chunk = 1;
+  size_t parts;
   if (r.wide) {
-    tiles = ((long long)b.T * G + rows - 1) / rows + (b.N < b.T ? b.N : b.T);
+    long long tiles = ((long long)b.T * G + rows - 1) / rows + (b.N < b.T ? b.N : b.T);
     if (b.N == 1) --tiles;
-    items = tiles * c.heads;
-    target = device_sms() / 2;
-    least = 512;
-    step = 128;
+    if (tiles < 1) tiles = 1;
+    const long long items = tiles * c.heads;
+    long long chunks = device_sms() / 2 / items;
+    if (chunks < 1) chunks = 1;
+    long long chunk = (span + chunks - 1) / chunks;
+    chunk = (chunk + 127) / 128 * 128;
+    if (chunk < 512) chunk = 512;
+    chunks = (span + chunk - 1) / chunk;
+    if (chunks < 1) chunks = 1;
+    r.tiles = (int)tiles;
+    r.chunk = (int)chunk;
+    r.chunks = (int)chunks;
+    parts = r.chunks > 1 ? (size_t)b.T * Hq * r.chunks : 0;
   } else {
-    tiles = (mq * G + rows - 1) / rows;
-    items = (long long)b.N * tiles * c.heads;
-    target = 3ll * (c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3)) * device_sms();
-    least = 256;
-    step = 64;
+    const long long tiles = (mq * G + rows - 1) / rows;
+    const long long groups = (long long)b.N * tiles * c.heads * ((span + 15) / 16);
+    const long long most = (long long)kRowWarps * (c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3)) * device_sms();
+    long long warps = groups / 2 / kRowWarps * kRowWarps;
+    if (warps < kRowWarps) warps = kRowWarps;
+    r.warps = (int)(warps < most ? warps : most);
+    parts = (size_t)2 * r.warps * kRowTile;
   }
-  long long chunks = items > 0 ? target / items : 1;
-  if (chunks < 1) chunks = 1;
-  long long chunk = (span + chunks - 1) / chunks;
-  chunk = (chunk + step - 1) / step * step;
-  if (chunk < least) chunk = least;
-  chunks = (span + chunk - 1) / chunk;
-  if (chunks < 1) chunks = 1;
-  r.tiles = (int)(tiles < 1 ? 1 : tiles);
-  r.chunk = (int)chunk;
-  r.chunks = (int)chunks;
-  const size_t parts = (size_t)b.T * Hq * r.chunks;
-  r.ws = r.chunks > 1 ? (parts * 8 + 255) / 256 * 256 + parts * c.dim * 4 : 0;
+  r.ml = parts * c.dim * 4;
+  r.before = (r.ml + parts * 8 + 255) / 256 * 256;
+  r.ws = r.before + (r.wide ? 0 : ((size_t)b.N + 1) * 8);
   return r;
 }
 
@@ -346,7 +348,7 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
   const Plan r = plan(p.c, p.b, Hq, window, max_q, max_kv);
   if (r.ws > 0 && (!workspace || workspace_bytes < r.ws))
     return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, r.ws);
-  if ((r.wide ? 2ll : (long long)p.b.N) * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
+  if (2ll * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
     return fail(MOE_ERR_UNSUPPORTED, "too many row tiles");
   p.q = static_cast<const uint16_t*>(q);
   p.o = static_cast<uint16_t*>(o);
@@ -364,18 +366,17 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
   p.tiles = r.tiles;
   p.chunks = r.chunks;
   p.chunk = r.chunk;
-  if (r.chunks > 1) {
-    p.part_ml = static_cast<float2*>(workspace);
-    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                        ((size_t)p.b.T * Hq * r.chunks * 8 + 255) / 256 * 256);
-  }
+  p.warps = r.warps;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + r.ml);
+  p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + r.before);
   p.err = paged_error_word();
   if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == PAGED_BF16;
   PAGED_CK(r.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
            "paged_attention launch");
-  if (r.chunks > 1) PAGED_CK(launch_paged_join(p, bf, st), "paged_attention join launch");
+  if (!r.wide || r.chunks > 1) PAGED_CK(launch_paged_join(p, bf, st), "paged_attention join launch");
   return MOE_OK;
 }
 

@@ -884,15 +884,6 @@ cudaError_t chunk_launch_t(const ChunkParams& cp, cudaStream_t st) {
   return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF, TMA>, cp);
 }
 
-// A map over one of the cache's arrays; false where the array has no such map
-// (a stride that the encoding refuses).
-bool page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box, bool bf16) {
-  const long long dims[4] = {c.dim, c.page, c.heads, c.pages};
-  const long long strides[3] = {c.row_stride * 2, c.head_stride * 2, c.page_stride * 2};
-  const int boxes[4] = {features, box, 1, 1};
-  return make_tmap_paged(m, base, dims, strides, boxes, bf16, features == 64) == cudaSuccess;
-}
-
 template <int D, bool BF>
 cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
   ChunkParams cp;
@@ -903,8 +894,8 @@ cudaError_t chunk_launch(const AttnParams& p, cudaStream_t st) {
     box >>= 1;
     --cp.box_log2;
   }
-  if (box >= 8 && page_map(&cp.k, p.c.k, p.c, 64, box, BF) &&
-      page_map(&cp.v, p.c.v, p.c, D == 64 ? 32 : 64, box, BF))
+  if (box >= 8 && make_page_map(&cp.k, p.c.k, p.c, 64, box, BF) &&
+      make_page_map(&cp.v, p.c.v, p.c, D == 64 ? 32 : 64, box, BF))
     return chunk_launch_t<D, BF, true>(cp, st);
   return chunk_launch_t<D, BF, false>(cp, st);
 }

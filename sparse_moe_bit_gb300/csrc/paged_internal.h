@@ -106,13 +106,16 @@ struct AttnParams {
   BatchView b;
   float scale_log2;  // scale * log2(e)
   int causal, window;
-  // split over the keys: chunk c of a row tile covers keys [c, c+1) * chunk
-  // behind its first visible one; the last chunk goes to the end
-  int chunks, chunk;
-  int tiles;       // row tiles the grid provides for: of a sequence (16-row
-                   // tiles), of the batch (256-row tiles)
-  float* part_o;   // [T * Hq][chunks][D], unnormalised (chunks > 1)
-  float2* part_ml; // [T * Hq][chunks]: running maximum (log2 units) and sum
+  // 256-row tiles: `tiles` of the batch; chunk c of a tile covers the keys
+  // [c, c+1) * chunk behind its first visible one, the last goes to the end.
+  // Partial results [T * Hq][chunks] where chunks > 1.
+  int tiles, chunks, chunk;
+  // 16-row tiles: `warps` (a multiple of kRowWarps) share the work; partial
+  // results [2 * warps][16], groups of keys before each sequence [N + 1].
+  int warps;
+  long long* before;
+  float* part_o;    // [..][D], unnormalised
+  float2* part_ml;  // [..]: running maximum (log2 units) and sum
   int* err;
 };
 // the first and one past the last key that rows [r0, r1) of a sequence see
@@ -125,7 +128,17 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
   if (p.window > 0) lo = max(0, p0 - p.window + 1);
   return make_int2(lo, max(hi, lo));
 }
-constexpr int kRowTile = 16;
+// A tensor map over one of the cache's arrays: boxes of `box` rows of a page x
+// `features` (64: 128-byte swizzle, 32: 64-byte); false where the array has none
+// (a stride that the encoding refuses).
+inline bool make_page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box,
+                          bool bf16) {
+  const long long dims[4] = {c.dim, c.page, c.heads, c.pages};
+  const long long strides[3] = {c.row_stride * 2, c.head_stride * 2, c.page_stride * 2};
+  const int boxes[4] = {features, box, 1, 1};
+  return make_tmap_paged(m, base, dims, strides, boxes, bf16, features == 64) == cudaSuccess;
+}
+constexpr int kRowTile = 16, kRowWarps = 4;
 cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
 constexpr int kPairRows = 256;
 cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st);
