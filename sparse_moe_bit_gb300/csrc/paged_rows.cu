@@ -213,19 +213,22 @@ __global__ void __launch_bounds__(32 * kWarps)
     int n;
     Seq s;
     Extent e;
-    int item, g;
+    const int32_t* table;
+    int item, h, g;  // item = row tile * heads + h
   };
   auto enter = [&](Cursor& c) {  // the next sequence with rows, from c.n on
     for (; c.n < p.b.N; ++c.n) {
       c.s = load_seq(p.b, c.n);
       c.e = extent_of(p, c.s);
-      if (c.e.items > 0) return;
+      if (c.e.items > 0) break;
     }
-    c.n = p.b.N - 1;  // (behind the last group: nothing reads it)
+    // (behind the last group there may be none: nothing reads it)
+    c.table = p.b.table + min(c.n, p.b.N - 1) * p.b.table_stride;
   };
   auto advance = [&](Cursor& c) {
     if (++c.g < c.e.groups) return;
     c.g = 0;
+    if (++c.h == p.c.heads) c.h = 0;
     if (++c.item < c.e.items) return;
     c.item = 0;
     ++c.n;
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
     use.item = (int)(left / use.e.groups);
     use.g = (int)(left - (long long)use.item * use.e.groups);
+    use.h = use.item % p.c.heads;
   }
   Cursor get = use;  // the copies' cursor, ahead
 
@@ -272,20 +276,20 @@ __global__ void __launch_bounds__(32 * kWarps)
   const bool copies = TMA ? lane < 2 * per_kv : true;
   const int my_row = TMA ? by * box : (lane & 15);
   struct Source {
-    int page, row, head;  // page -1: nothing to copy (or a bad page)
+    int page, row, head;
+    bool any;  // something to copy
   };
+  // (the page number is not looked at before the copies are issued, a step later:
+  // its load is then never waited for)
   auto lookup = [&](int st) -> Source {
-    Source r{-1, 0, 0};
+    Source r{-1, 0, 0, false};
     const int key = get.e.lo + get.g * kGroup + my_row;
     if (!copies || st >= steps || key >= get.s.kv || key + box <= get.e.first) return r;
     const int col = fast_div(key, p.c.div);
-    r.page = p.b.table[get.n * p.b.table_stride + col];
+    r.page = get.table[col];
     r.row = key - col * p.c.page;
-    r.head = get.item % p.c.heads;
-    if (r.page < 0 || r.page >= p.c.pages) {
-      atomicOr(p.err, PAGED_DEVERR_PAGE);
-      r.page = -1;
-    }
+    r.head = get.h;
+    r.any = true;
     return r;
   };
   // issues the copies; returns the group's keys that may be scored
@@ -294,12 +298,14 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (!TMA) cp_async_commit();
       return 0;
     }
+    const bool good_page = src.any && src.page >= 0 && src.page < p.c.pages;
+    if (src.any && !good_page) atomicOr(p.err, PAGED_DEVERR_PAGE);
     const uint32_t kd = ring + stage * C::STAGE, vd = kd + kGroup * C::ROW;
     if constexpr (TMA) {
-      const uint32_t got = __ballot_sync(0xffffffffu, src.page >= 0);
+      const uint32_t got = __ballot_sync(0xffffffffu, good_page);
       if (lane == 0) mbar_arrive_expect_tx(bars + stage * 8, __popc(got) * box * 128);
       __syncwarp();
-      if (src.page >= 0)
+      if (good_page)
         tma_box((is_v ? vd : kd) + bx * (kGroup * 128) + my_row * 128, is_v ? &rp.v : &rp.k, bx * 64,
                 src.row, src.head, src.page, bars + stage * 8);
       // keys of the boxes that hold some, up to the sequence's end
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (left < kGroup) seen &= left > 0 ? (1u << left) - 1 : 0;
       return seen;
     } else {
-      const long long at = src.page < 0 ? -1
+      const long long at = !good_page ? -1
                                         : src.page * p.c.page_stride + src.row * p.c.row_stride +
                                               src.head * p.c.head_stride;
       constexpr int CH = C::ROW / 16;                 // 16-byte pieces of a key
@@ -341,6 +347,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane
   int hiA = 0, hiB = 0, loA = 0, loB = 0;   // visible keys of the two rows: [lo, hi)
+  int strict_lo = 0, strict_hi = 0;         // visible to all rows of the tile
   int r0 = 0, rows = 0, h = 0;
   float mA = kNegInf, mB = kNegInf, lA = 0.f, lB = 0.f;
   float o[D / 8][4];
@@ -362,9 +369,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (fresh) {
       fresh = false;
       begun = use.g > 0;
-      const int tile = use.item / p.c.heads;
-      h = use.item - tile * p.c.heads;
-      r0 = tile * kRowTile;
+      h = use.h;
+      r0 = use.item / p.c.heads * kRowTile;
       rows = use.s.nq * p.G;
       // Q rows into shared memory, 16-byte chunks swizzled by the row
       constexpr int CH = C::ROW / 16;
@@ -386,6 +392,9 @@ __global__ void __launch_bounds__(32 * kWarps)
       };
       range(g, loA, hiA);
       range(g + 8, loB, hiB);
+      int last;  // the first row's last key, the last row's first key
+      range(0, last, strict_hi);
+      range(kRowTile - 1, strict_lo, last);
       mA = mB = kNegInf;
       lA = lB = 0.f;
 #pragma unroll
@@ -419,12 +428,12 @@ __global__ void __launch_bounds__(32 * kWarps)
       cp_async_wait<AHEAD>();
     }
     __syncwarp();
-    // S: two blocks of 8 keys, two accumulators each to halve the chains
-    float sc[2][2][4];
+    // S: two blocks of 8 keys, four accumulators each to shorten the chains
+    float sc[2][4][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[i][j][e] = 0.f;
 #pragma unroll
@@ -439,20 +448,26 @@ __global__ void __launch_bounds__(32 * kWarps)
         const int r = (mi >> 1) * 8 + mr, c = 2 * kk + (mi & 1);
         ldsm4(b, ks + piece_at(r, c));
       }
-      mma16816<BF>(sc[0][kk & 1], a, b[0], b[1]);
-      mma16816<BF>(sc[1][kk & 1], a, b[2], b[3]);
+      mma16816<BF>(sc[0][kk & 3], a, b[0], b[1]);
+      mma16816<BF>(sc[1][kk & 3], a, b[2], b[3]);
     }
     const int key0 = use.e.lo + use.g * kGroup;
     float x[2][4];
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb) {
+    for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int kx = nb * 8 + t2 + (e & 1);
-        const int key = key0 + kx;
-        const bool vis = (ok >> kx & 1) && (e < 2 ? (key >= loA && key < hiA)
-                                                  : (key >= loB && key < hiB));
-        x[nb][e] = vis ? (sc[nb][0][e] + sc[nb][1][e]) * p.scale_log2 : kNegInf;
+      for (int e = 0; e < 4; ++e)
+        x[nb][e] = ((sc[nb][0][e] + sc[nb][1][e]) + (sc[nb][2][e] + sc[nb][3][e])) * p.scale_log2;
+    if (ok != 0xffffu || key0 < strict_lo || key0 + kGroup > strict_hi) {
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int kx = nb * 8 + t2 + (e & 1), key = key0 + kx;
+          const bool vis = (ok >> kx & 1) && (e < 2 ? (key >= loA && key < hiA)
+                                                    : (key >= loB && key < hiB));
+          if (!vis) x[nb][e] = kNegInf;
+        }
       }
     }
     float nA = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
