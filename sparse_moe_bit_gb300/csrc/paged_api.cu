@@ -109,17 +109,19 @@ moe_status check_rope(int D, const double* freq, int r, float mscale) {
 
 // Choice of kernel and split for one call.
 struct Plan {
-  bool wide;  // 256-row tiles on the tensor cores, else 16-row tiles
+  bool wide;  // 256-row tiles on the tensor cores, else 8- or 16-row tiles
   int tiles, chunks, chunk;  // 256-row tiles
-  int warps;                 // 16-row tiles
+  int warps, row_tile;       // small tiles
+  int parts;                 // of a row, about
   size_t ml, before, ws;     // offsets of the partial maxima and sums, of the counts; total bytes
 };
 
-// 16-row tiles while one holds the longest chunk's rows (each tile reads the
-// keys again), 256-row tiles above.
+// Tiles of 8 or 16 rows while one holds the longest chunk's rows (each tile reads
+// the keys again), 256-row tiles above.
 //
-// 16-row tiles: as many warps as the SMs hold (four a CTA; one CTA of head dim
-// 256, two of 128, three of 64), but at least two groups of 16 keys for each.
+// Small tiles: as many warps as the SMs hold, four each (a warp's ring takes a
+// quarter of the shared memory), but at least two groups of keys (16 KB each) for
+// a warp.
 // 256-row tiles: split over the keys only while the pairs of CTAs leave SMs
 // without work; no chunk below 512 keys.
 Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv) {
@@ -130,7 +132,8 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
   long long kv = max_kv > 0 ? max_kv : b.capacity;
   if (kv > b.capacity) kv = b.capacity;
   r.wide = mq * G > kRowTile;
-  const long long rows = r.wide ? kPairRows : kRowTile;
+  r.row_tile = mq * G <= 8 ? 8 : kRowTile;
+  const long long rows = r.wide ? kPairRows : r.row_tile;
   long long span = kv;
   if (window > 0 && window + rows < span) span = window + rows;
   r.tiles = r.chunks = r.chunk = 1;
@@ -151,13 +154,17 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
     r.chunk = (int)chunk;
     r.chunks = (int)chunks;
     parts = r.chunks > 1 ? (size_t)b.T * Hq * r.chunks : 0;
+    r.parts = r.chunks;
   } else {
     const long long tiles = (mq * G + rows - 1) / rows;
-    const long long groups = (long long)b.N * tiles * c.heads * ((span + 15) / 16);
-    const long long most = (long long)kRowWarps * (c.dim == 256 ? 1 : (c.dim == 128 ? 2 : 3)) * device_sms();
+    const int kg = 4096 / c.dim;  // keys of a group
+    const long long items = (long long)b.N * tiles * c.heads;
+    const long long groups = items * ((span + kg - 1) / kg);
+    const long long most = (long long)kRowWarps * device_sms();
     long long warps = groups / 2 / kRowWarps * kRowWarps;
     if (warps < kRowWarps) warps = kRowWarps;
     r.warps = (int)(warps < most ? warps : most);
+    r.parts = (int)(r.warps / (items > 0 ? items : 1)) + 1;
     parts = (size_t)2 * r.warps * kRowTile;
   }
   r.ml = parts * c.dim * 4;
@@ -367,6 +374,8 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
   p.chunks = r.chunks;
   p.chunk = r.chunk;
   p.warps = r.warps;
+  p.row_tile = r.row_tile;
+  p.parts = r.parts;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + r.ml);
   p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + r.before);

@@ -110,9 +110,11 @@ struct AttnParams {
   // [c, c+1) * chunk behind its first visible one, the last goes to the end.
   // Partial results [T * Hq][chunks] where chunks > 1.
   int tiles, chunks, chunk;
-  // 16-row tiles: `warps` (a multiple of kRowWarps) share the work; partial
-  // results [2 * warps][16], groups of keys before each sequence [N + 1].
-  int warps;
+  // tiles of `row_tile` = 8 or 16 rows: `warps` (a multiple of kRowWarps) share the
+  // work; partial results [2 * warps][16], groups of keys before each sequence
+  // [N + 1].
+  int warps, row_tile;
+  int parts;  // about so many partial results of a row
   long long* before;
   float* part_o;    // [..][D], unnormalised
   float2* part_ml;  // [..]: running maximum (log2 units) and sum

@@ -3,27 +3,31 @@
 //
 // The G query heads that share a key/value head and the sequence's new tokens
 // form the rows of one small matrix: row r is token r / G, head r % G of the
-// group.  An item is 16 rows (one mma tile) of a sequence over all of their
-// keys, so that every key and value is read from HBM once for the whole group.
+// group.  An item is a tile of 8 or 16 rows of a sequence over all of their keys,
+// so that every key and value is read from HBM once for the whole group.
 //   S = Q K^T, m' = max(m, rowmax S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
 //   O = O 2^(m - m') + P V                         (S in log2 units, all fp32)
 //
 // Bound: HBM (2 bytes x 2 D per key against 2 x 4 D x rows operations).  What
-// counts is bytes in flight and an even share for every SM, so the work is cut
-// into groups of 16 keys, the groups of all items stand in one row, and each of
-// the launch's warps takes the same number of them in sequence, across items:
-// no warp ever waits for another.  It streams its groups through a ring of its
-// own, filled by 16-byte asynchronous copies two or more groups ahead (page
-// numbers one further), and keeps m, l and O of its 16 rows in registers.  An
-// item that one warp covers is written at once; of the others every warp leaves
-// O, m and l in a slot -- a warp has at most two such items, its first and its
-// last -- and a second kernel joins them in order, which makes the result
-// independent of timing.  (Chunks of keys fixed on the host, a CTA each, gave
-// 72 % of the copy bandwidth on 64 ragged contexts up to 8192: the last wave
-// ran half empty.)  The product of 16 rows by mma.sync (m16n8k16) needs a tenth
-// of the rate at which keys arrive; wider row tiles go to the tcgen05 kernel.
-// Rows of a page that lie behind the sequence's end, or whose page number is
-// bad, are never read: the copy fills them with zeros and the score is masked.
+// counts is bytes in flight and an even share for every SM, so the keys are cut
+// into groups, the groups of all items stand in one row, and each of the launch's
+// warps takes the same number of them in sequence, across items: no warp ever
+// waits for another.  It streams its groups through a ring of its own, 16 KB a
+// stage, filled by TMA two groups ahead (page numbers one further), and keeps m, l
+// and O of its rows in registers.  An item that one warp covers is written at
+// once; of the others every warp leaves O, m and l in a slot -- a warp has at most
+// two such items, its first and its last -- and a second kernel joins them in
+// order, which makes the result independent of timing.  (Chunks of keys fixed on
+// the host, a CTA each, gave 72 % of the copy bandwidth on 64 ragged contexts up
+// to 8192: the last wave ran half empty.)
+//
+// With four warps an SM the time of a group is the latency of its instructions.
+// So the products are transposed, S^T = K Q^T and O^T = V^T P^T by mma.sync
+// (m16n8k16) with the keys and the features as the 16 rows and the tile's rows as
+// the 8 columns: half of the products, of the softmax's values and of the
+// accumulators of the other way round, and Q stays in registers.
+// Rows of a page that lie behind the sequence's end, or whose page number is bad,
+// can hold anything: their scores are masked and their values zeroed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,32 +38,32 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = kRowWarps;  // of a CTA
-constexpr int kGroup = 16;  // keys of a warp's step
 
+// KG: keys of a group
 template <int D>
 struct RowsCfg {
+  static constexpr int KG = D == 256 ? 16 : (D == 128 ? 32 : 64);
   static constexpr int ROW = 2 * D;  // bytes of a key
-  static constexpr int STAGES = D == 64 ? 4 : 3;
-  static constexpr int STAGE = 2 * kGroup * ROW;  // keys and values of a group
+  static constexpr int STAGES = 3;
+  static constexpr int STAGE = 2 * KG * ROW;  // keys and values of a group
   static constexpr int RING = kWarps * STAGES * STAGE;
-  static constexpr int OFF_Q = RING;
-  static constexpr int OFF_BAR = OFF_Q + kWarps * kRowTile * ROW;  // per warp and stage
+  static constexpr int OFF_BAR = RING;  // per warp and stage
   static constexpr int SMEM = OFF_BAR + kWarps * STAGES * 8 + 1024;
   static_assert(SMEM + 1100 <= 232448, "shared memory budget");  // (the rest: static)
+  // KG rows of D features in shared memory: blocks of 64 features, rows of 128
+  // bytes, the 16-byte pieces of a row swizzled by the row -- the 128-byte swizzle
+  // of TMA, and free of bank conflicts for ldmatrix.  Offset of piece c of row r:
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return (c >> 3) * (KG * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
 };
-// 16 rows of D features in shared memory: blocks of 64 features, rows of 128
-// bytes, the 16-byte pieces of a row swizzled by the row -- the 128-byte swizzle
-// of TMA, and free of bank conflicts for ldmatrix.  Offset of piece c of row r:
-__device__ __forceinline__ uint32_t piece_at(int r, int c) {
-  return (c >> 3) * (kGroup * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
 
 // Tensor maps over the cache's keys and values (innermost first): feature, row
-// of a page, head, page; boxes of 64 features x `box` (16 or 8) rows.
+// of a page, head, page; boxes of 64 features x 2^box_log2 rows (8 to KG).
 struct RowsParams {
   AttnParams a;
   CUtensorMap k, v;
-  int box;
+  int box_log2;
 };
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* tm, int f, int r, int h,
                                         int pg, uint32_t bar) {
@@ -127,22 +131,28 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// the 8x8 matrix of 16-bit values whose row i the lanes 4i .. 4i+3 hold, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // The items of one sequence: `items` (row tile, key/value head) pairs of
-// `groups` groups each, over the keys [lo, kv).  A sequence with rows has at
-// least one group an item, so that rows without keys are written too.
+// `groups` groups of KG keys each, over the keys [lo, kv).  A sequence with rows
+// has at least one group an item, so that rows without keys are written too.
 struct Extent {
   int lo, first, groups, items;  // first: the first key that a row may see
 };
-__device__ __forceinline__ Extent extent_of(const AttnParams& p, const Seq& s) {
+__device__ __forceinline__ Extent extent_of(const AttnParams& p, const Seq& s, int kg, int tile) {
   Extent e;
-  const int rows = s.nq * p.G;
   e.first = p.window > 0 ? max(0, s.kv - s.nq - p.window + 1) : 0;
-  e.lo = e.first & ~(kGroup - 1);  // groups do not straddle pages that hold whole ones
-  e.groups = max((s.kv - e.lo + kGroup - 1) / kGroup, 1);
-  e.items = (rows + kRowTile - 1) / kRowTile * p.c.heads;
+  e.lo = e.first & ~(kg - 1);  // groups do not straddle pages that hold whole ones
+  e.groups = max((s.kv - e.lo + kg - 1) / kg, 1);
+  e.items = (s.nq * p.G + tile - 1) / tile * p.c.heads;
   return e;
 }
 // warp w of W takes the groups [share(w), share(w + 1)) of U
@@ -152,13 +162,15 @@ __device__ __forceinline__ int owner_of(long long U, int W, long long u) {
   return (int)(((u + 1) * W - 1) / U);
 }
 
-// TMA: a group is copied as boxes of the pages' rows, a lane each; otherwise
-// (pages that no box of 8 rows divides) by 16-byte copies.
-template <int D, bool BF, bool TMA>
+// NB: blocks of 8 rows of a tile.  TMA: a group is copied as boxes of the pages'
+// rows, a lane each; otherwise (pages that no box of 8 rows divides) by 16-byte
+// copies.
+template <int D, int NB, bool BF, bool TMA>
 __global__ void __launch_bounds__(32 * kWarps)
     paged_rows_kernel(const __grid_constant__ RowsParams rp) {
   const AttnParams& p = rp.a;
   using C = RowsCfg<D>;
+  constexpr int KG = C::KG, MB = KG / 16, TILE = 8 * NB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -174,7 +186,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int n0 = threadIdx.x * per, n1 = min(n0 + per, p.b.N);
   long long mine = 0;
   for (int n = n0; n < n1; ++n) {
-    const Extent e = extent_of(p, load_seq(p.b, n));
+    const Extent e = extent_of(p, load_seq(p.b, n), KG, TILE);
     mine += (long long)e.items * e.groups;
   }
   long long inc = mine;
@@ -196,7 +208,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     long long at = inc - mine;
     for (int n = n0; n < n1; ++n) {
       p.before[n] = at;
-      const Extent e = extent_of(p, load_seq(p.b, n));
+      const Extent e = extent_of(p, load_seq(p.b, n), KG, TILE);
       at += (long long)e.items * e.groups;
     }
     if (threadIdx.x == 0) p.before[p.b.N] = U;
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   auto enter = [&](Cursor& c) {  // the next sequence with rows, from c.n on
     for (; c.n < p.b.N; ++c.n) {
       c.s = load_seq(p.b, c.n);
-      c.e = extent_of(p, c.s);
+      c.e = extent_of(p, c.s, KG, TILE);
       if (c.e.items > 0) break;
     }
     // (behind the last group there may be none: nothing reads it)
@@ -257,7 +269,6 @@ __global__ void __launch_bounds__(32 * kWarps)
   Cursor get = use;  // the copies' cursor, ahead
 
   const uint32_t sm = smem_u32(smem);
-  const uint32_t qs = sm + C::OFF_Q + warp * kRowTile * C::ROW;
   const uint32_t ring = sm + warp * C::STAGES * C::STAGE;
   const uint32_t bars = sm + C::OFF_BAR + warp * C::STAGES * 8;
   if (TMA) {
@@ -267,24 +278,23 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 
   // ---- the ring.  TMA: lane l copies box l of a group (blocks of 64 features
-  // side by side, keys then values; at most 16 boxes).  Else: lane l (and l + 16)
-  // addresses key l.  Where a lane's copy of group `st` comes from:
+  // side by side, then rows; keys, then values: at most 32).  Where a lane's copy
+  // comes from; the page number is not looked at before the copies are issued, a
+  // step after its load.
   constexpr int FC = D / 64;
-  const int box = TMA ? rp.box : 1, per_kv = FC * (kGroup / box);  // boxes of the keys
-  const bool is_v = TMA && lane >= per_kv;
+  const int box_log2 = TMA ? rp.box_log2 : 0, per_kv = FC * (KG >> box_log2);  // boxes of the keys
+  const bool is_v = lane >= per_kv;
   const int bx = (lane - (is_v ? per_kv : 0)) % FC, by = (lane - (is_v ? per_kv : 0)) / FC;
-  const bool copies = TMA ? lane < 2 * per_kv : true;
-  const int my_row = TMA ? by * box : (lane & 15);
+  const int my_row = by << box_log2;
   struct Source {
     int page, row, head;
     bool any;  // something to copy
   };
-  // (the page number is not looked at before the copies are issued, a step later:
-  // its load is then never waited for)
   auto lookup = [&](int st) -> Source {
     Source r{-1, 0, 0, false};
-    const int key = get.e.lo + get.g * kGroup + my_row;
-    if (!copies || st >= steps || key >= get.s.kv || key + box <= get.e.first) return r;
+    if (!TMA || lane >= 2 * per_kv || st >= steps) return r;
+    const int key = get.e.lo + get.g * KG + my_row;
+    if (key >= get.s.kv || key + (1 << box_log2) <= get.e.first) return r;
     const int col = fast_div(key, p.c.div);
     r.page = get.table[col];
     r.row = key - col * p.c.page;
@@ -292,49 +302,65 @@ __global__ void __launch_bounds__(32 * kWarps)
     r.any = true;
     return r;
   };
+  constexpr uint64_t kAll = KG == 64 ? ~0ull : (1ull << (KG & 63)) - 1;
   // issues the copies; returns the group's keys that may be scored
-  auto issue = [&](int st, int stage, const Source& src) -> uint32_t {
+  auto issue = [&](int st, int stage, const Source& src) -> uint64_t {
     if (st >= steps) {
       if (!TMA) cp_async_commit();
       return 0;
     }
-    const bool good_page = src.any && src.page >= 0 && src.page < p.c.pages;
-    if (src.any && !good_page) atomicOr(p.err, PAGED_DEVERR_PAGE);
-    const uint32_t kd = ring + stage * C::STAGE, vd = kd + kGroup * C::ROW;
+    const uint32_t kd = ring + stage * C::STAGE, vd = kd + KG * C::ROW;
+    const int key0 = get.e.lo + get.g * KG, left = get.s.kv - key0;
+    uint64_t seen = 0;
     if constexpr (TMA) {
+      const bool good_page = src.any && src.page >= 0 && src.page < p.c.pages;
+      if (src.any && !good_page) atomicOr(p.err, PAGED_DEVERR_PAGE);
       const uint32_t got = __ballot_sync(0xffffffffu, good_page);
-      if (lane == 0) mbar_arrive_expect_tx(bars + stage * 8, __popc(got) * box * 128);
+      if (lane == 0) mbar_arrive_expect_tx(bars + stage * 8, (__popc(got) << box_log2) * 128);
       __syncwarp();
       if (good_page)
-        tma_box((is_v ? vd : kd) + bx * (kGroup * 128) + my_row * 128, is_v ? &rp.v : &rp.k, bx * 64,
+        tma_box((is_v ? vd : kd) + bx * (KG * 128) + my_row * 128, is_v ? &rp.v : &rp.k, bx * 64,
                 src.row, src.head, src.page, bars + stage * 8);
-      // keys of the boxes that hold some, up to the sequence's end
-      uint32_t seen = box == 16 ? (got & 1 ? 0xffffu : 0)
-                                : ((got & 1 ? 0x00ffu : 0) | (got >> FC & 1 ? 0xff00u : 0));
-      const int left = get.s.kv - (get.e.lo + get.g * kGroup);
-      if (left < kGroup) seen &= left > 0 ? (1u << left) - 1 : 0;
-      return seen;
+      seen = kAll;
+      if (__popc(got) != 2 * per_kv || left < KG) {  // the keys of the boxes that are there
+        seen = 0;
+        for (int y = 0; y < KG >> box_log2; ++y)
+          if (got >> (y * FC) & 1) seen |= ((1ull << ((1 << box_log2) & 63)) - 1) << (y << box_log2);
+        if (box_log2 == 6 && (got & 1)) seen = kAll;
+        if (left < KG) seen &= left > 0 ? (1ull << left) - 1 : 0;
+      }
     } else {
-      const long long at = !good_page ? -1
-                                        : src.page * p.c.page_stride + src.row * p.c.row_stride +
-                                              src.head * p.c.head_stride;
       constexpr int CH = C::ROW / 16;                 // 16-byte pieces of a key
       constexpr int RPI = 32 / CH > 0 ? 32 / CH : 1;  // keys a warp copies at once
+#pragma unroll 1
+      for (int k0 = 0; k0 < KG; k0 += 16) {
+        const int key = key0 + k0 + (lane & 15);
+        long long at = -1;
+        if (key >= get.e.first && key < get.s.kv) {
+          const int col = fast_div(key, p.c.div), page = get.table[col];
+          if (page >= 0 && page < p.c.pages)
+            at = page * p.c.page_stride + (key - col * p.c.page) * p.c.row_stride +
+                 get.h * p.c.head_stride;
+          else
+            atomicOr(p.err, PAGED_DEVERR_PAGE);
+        }
+        seen |= (uint64_t)(__ballot_sync(0xffffffffu, at >= 0) & 0xffffu) << k0;
 #pragma unroll 4
-      for (int i = 0; i < kGroup / RPI; ++i) {
-        const int r = i * RPI + lane / CH, c = lane % CH;
-        const long long o = __shfl_sync(0xffffffffu, at, r);
-        const uint32_t nb = o >= 0 ? 16u : 0u;
-        const long long e = (o >= 0 ? o : 0) + c * 8;
-        cp_async16(kd + piece_at(r, c), p.c.k + e, nb);
-        cp_async16(vd + piece_at(r, c), p.c.v + e, nb);
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = i * RPI + lane / CH, c = lane % CH;
+          const long long o = __shfl_sync(0xffffffffu, at, r);
+          const uint32_t nb = o >= 0 ? 16u : 0u;
+          const long long e = (o >= 0 ? o : 0) + c * 8;
+          cp_async16(kd + C::at(k0 + r, c), p.c.k + e, nb);
+          cp_async16(vd + C::at(k0 + r, c), p.c.v + e, nb);
+        }
       }
       cp_async_commit();
-      return __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
     }
+    return seen;
   };
   constexpr int AHEAD = C::STAGES - 1;
-  uint32_t seen[C::STAGES];  // of the next groups: keys that may be scored
+  uint64_t seen[C::STAGES];  // of the next groups: keys that may be scored
   Source src = lookup(0);
 #pragma unroll
   for (int st = 0; st < AHEAD; ++st) {
@@ -343,17 +369,22 @@ __global__ void __launch_bounds__(32 * kWarps)
     src = lookup(st + 1);
   }
 
-  // per-thread rows: g and g + 8 of the tile
+  // In the products' layouts a lane holds keys (and features) g and g + 8 of 16,
+  // and rows t2 and t2 + 1 of 8; as an operand's, row g.
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   const int mi = lane >> 3, mr = lane & 7;  // ldmatrix: matrix and row of this lane
-  int hiA = 0, hiB = 0, loA = 0, loB = 0;   // visible keys of the two rows: [lo, hi)
+  int vis_lo[NB][2], vis_hi[NB][2];         // visible keys of the rows: [lo, hi)
   int strict_lo = 0, strict_hi = 0;         // visible to all rows of the tile
-  int r0 = 0, rows = 0, h = 0;
-  float mA = kNegInf, mB = kNegInf, lA = 0.f, lB = 0.f;
-  float o[D / 8][4];
+  int r0 = 0, rows = 0;
+  float m[NB][2], l[NB][2];
+  uint32_t q[NB][D / 16][2];
+  float o[NB][D / 16][4];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) vis_lo[nb][i] = vis_hi[nb][i] = 0;
   bool fresh = true;   // the next group is the first of this warp's part of its item
   bool begun = false;  // ... which began before this warp
-
   int stage = 0;        // of this group
   uint32_t parity = 0;  // of its barrier
   bool good = true;
@@ -369,191 +400,226 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (fresh) {
       fresh = false;
       begun = use.g > 0;
-      h = use.h;
-      r0 = use.item / p.c.heads * kRowTile;
+      r0 = use.item / p.c.heads * TILE;
       rows = use.s.nq * p.G;
-      // Q rows into shared memory, 16-byte chunks swizzled by the row
-      constexpr int CH = C::ROW / 16;
-#pragma unroll 4
-      for (int i = lane; i < kRowTile * CH; i += 32) {
-        const int r = i / CH, c = i % CH;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r0 + r < rows) {
-          const int tok = fast_div(r0 + r, p.divG);
-          v = *reinterpret_cast<const uint4*>(p.q + (use.s.t0 + tok) * p.q_ts +
-                                              (h * p.G + r0 + r - tok * p.G) * p.q_hs + c * 8);
-        }
-        *reinterpret_cast<uint4*>(smem + C::OFF_Q + warp * kRowTile * C::ROW + piece_at(r, c)) = v;
-      }
-      auto range = [&](int r, int& a, int& b) {
-        const int pos = use.s.kv - use.s.nq + fast_div(min(r0 + r, rows - 1), p.divG);
+      const int pos0 = use.s.kv - use.s.nq;
+      auto vis = [&](int r, int& a, int& b) {
+        const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
         b = p.causal ? min(use.s.kv, pos + 1) : use.s.kv;
         a = p.window > 0 ? pos - p.window + 1 : 0;
       };
-      range(g, loA, hiA);
-      range(g + 8, loB, hiB);
-      int last;  // the first row's last key, the last row's first key
-      range(0, last, strict_hi);
-      range(kRowTile - 1, strict_lo, last);
-      mA = mB = kNegInf;
-      lA = lB = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int nb = 0; nb < NB; ++nb) {
+        // operand Q^T: row 8 nb + g, features 16 kk + t2, + 1 and + 8, + 9
+        const int r = r0 + 8 * nb + g;
+        const int tok = r < rows ? fast_div(r, p.divG) : 0;
+        const uint16_t* src_q =
+            p.q + (r < rows ? (use.s.t0 + tok) * p.q_ts + (use.h * p.G + r - tok * p.G) * p.q_hs : 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            q[nb][kk][i] = 0;
+            if (r < rows) q[nb][kk][i] = *reinterpret_cast<const uint32_t*>(src_q + kk * 16 + t2 + 8 * i);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vis(8 * nb + t2 + i, vis_lo[nb][i], vis_hi[nb][i]);
+          m[nb][i] = kNegInf;
+          l[nb][i] = 0.f;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nb][d][e] = 0.f;
+      }
+      int other;  // the first row's last key, the last row's first key
+      vis(0, other, strict_hi);
+      vis(TILE - 1, strict_lo, other);
     }
-    const uint32_t ks = ring + stage * C::STAGE, vs = ks + kGroup * C::ROW;
-    const uint32_t ok = seen[0];
+    const uint32_t ks = ring + stage * C::STAGE, vs = ks + KG * C::ROW;
+    const uint64_t ok = seen[0];
+    const int key0 = use.e.lo + use.g * KG;
+    const bool edge = ok != kAll || key0 < use.e.first || key0 < strict_lo || key0 + KG > strict_hi;
     if constexpr (TMA) {
       good = copies_wait(bars + stage * 8, parity);
       if (!__all_sync(0xffffffffu, good)) {
         good = false;
         break;
       }
-      // Rows behind the sequence's end (or before its window, or of a bad page)
-      // can hold anything, NaN included, which a weight of zero does not cancel:
-      // values of keys that no row may see are zeroed.
-      const int early = max(use.e.first - (use.e.lo + use.g * kGroup), 0);
-      uint32_t clear = ~ok & 0xffffu;
-      if (early > 0) clear |= (1u << min(early, 16)) - 1;
-      if (clear) {
-        for (int i = lane; i < kGroup * (C::ROW / 16); i += 32) {
-          const int r = i / (C::ROW / 16), c = i % (C::ROW / 16);
-          if (clear >> r & 1)
-            *reinterpret_cast<uint4*>(smem + (vs - sm) + piece_at(r, c)) = make_uint4(0, 0, 0, 0);
+      if (edge) {
+        // what lies in rows that no query may see can be NaN, which a weight of
+        // zero does not cancel
+        const int early = use.e.first - key0;
+        uint64_t clear = ~ok & kAll;
+        if (early > 0) clear |= early >= KG ? kAll : (1ull << early) - 1;
+        if (clear) {
+          for (int i = lane; i < KG * (C::ROW / 16); i += 32) {
+            const int r = i / (C::ROW / 16), c = i % (C::ROW / 16);
+            if (clear >> r & 1)
+              *reinterpret_cast<uint4*>(smem + (vs - sm) + C::at(r, c)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();  // before the stage's next copy
         }
-        fence_proxy_async_smem();  // before the stage's next copy
       }
     } else {
       cp_async_wait<AHEAD>();
     }
     __syncwarp();
-    // S: two blocks of 8 keys, four accumulators each to shorten the chains
-    float sc[2][4][4];
+    // ---- S^T: two chains a block where there is only one block
+    constexpr int CHAINS = MB * NB >= 4 ? 1 : 2;
+    float x[MB][NB][4];
+    {
+      float sc[CHAINS][MB][NB][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int ch = 0; ch < CHAINS; ++ch)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[i][j][e] = 0.f;
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t a[4], b[4];
-      // A: matrices (rows 0-7, k 0-7), (rows 8-15, k 0-7), (0-7, 8-15), (8-15, 8-15)
-      {
-        const int r = (mi & 1) * 8 + mr, c = 2 * kk + (mi >> 1);
-        ldsm4(a, qs + piece_at(r, c));
-      }
-      {
-        const int r = (mi >> 1) * 8 + mr, c = 2 * kk + (mi & 1);
-        ldsm4(b, ks + piece_at(r, c));
-      }
-      mma16816<BF>(sc[0][kk & 3], a, b[0], b[1]);
-      mma16816<BF>(sc[1][kk & 3], a, b[2], b[3]);
-    }
-    const int key0 = use.e.lo + use.g * kGroup;
-    float x[2][4];
+            for (int e = 0; e < 4; ++e) sc[ch][mb][nb][e] = 0.f;
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb)
+      for (int kk = 0; kk < D / 16; ++kk) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[nb][e] = ((sc[nb][0][e] + sc[nb][1][e]) + (sc[nb][2][e] + sc[nb][3][e])) * p.scale_log2;
-    if (ok != 0xffffu || key0 < strict_lo || key0 + kGroup > strict_hi) {
+        for (int mb = 0; mb < MB; ++mb) {
+          // matrices (keys 0-7, k 0-7), (keys 8-15, k 0-7), (0-7, 8-15), (8-15, 8-15)
+          uint32_t a[4];
+          ldsm4(a, ks + C::at(mb * 16 + (mi & 1) * 8 + mr, 2 * kk + (mi >> 1)));
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int kx = nb * 8 + t2 + (e & 1), key = key0 + kx;
-          const bool vis = (ok >> kx & 1) && (e < 2 ? (key >= loA && key < hiA)
-                                                    : (key >= loB && key < hiB));
-          if (!vis) x[nb][e] = kNegInf;
+          for (int nb = 0; nb < NB; ++nb)
+            mma16816<BF>(sc[kk % CHAINS][mb][nb], a, q[nb][kk][0], q[nb][kk][1]);
         }
       }
-    }
-    float nA = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-    float nB = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-      nA = fmaxf(nA, __shfl_xor_sync(0xffffffffu, nA, d));
-      nB = fmaxf(nB, __shfl_xor_sync(0xffffffffu, nB, d));
-    }
-    nA = fmaxf(mA, nA);
-    nB = fmaxf(mB, nB);
-    if (__any_sync(0xffffffffu, nA > mA || nB > mB)) {
-      // (-inf) - (-inf): a row that has seen nothing has nothing to scale
-      const float fA = mA == nA ? 1.f : exp2_approx(mA - nA);
-      const float fB = mB == nB ? 1.f : exp2_approx(mB - nB);
-      lA *= fA;
-      lB *= fB;
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= fA;
-        o[i][1] *= fA;
-        o[i][2] *= fB;
-        o[i][3] *= fB;
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = sc[0][mb][nb][e];
+            if (CHAINS == 2) v += sc[CHAINS - 1][mb][nb][e];
+            x[mb][nb][e] = v * p.scale_log2;
+          }
+    }
+    if (edge) {
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int kx = mb * 16 + g + 8 * (e >> 1), key = key0 + kx;
+            if (!(ok >> kx & 1) || key < vis_lo[nb][e & 1] || key >= vis_hi[nb][e & 1])
+              x[mb][nb][e] = kNegInf;
+          }
+    }
+    // ---- running maxima (over the keys: over the lanes of equal t2)
+    float now[NB][2];
+    bool rise = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = kNegInf;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) v = fmaxf(v, fmaxf(x[mb][nb][i], x[mb][nb][2 + i]));
+        now[nb][i] = v;
       }
-      mA = nA;
-      mB = nB;
-    }
-    const float uA = mA == kNegInf ? 0.f : mA, uB = mB == kNegInf ? 0.f : mB;
-    uint32_t pa[4];
-    {
-      float e0[4], e1[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        e0[e] = exp2_approx(x[0][e] - (e < 2 ? uA : uB));
-        e1[e] = exp2_approx(x[1][e] - (e < 2 ? uA : uB));
+    for (int d = 4; d <= 16; d <<= 1)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          now[nb][i] = fmaxf(now[nb][i], __shfl_xor_sync(0xffffffffu, now[nb][i], d));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        now[nb][i] = fmaxf(now[nb][i], m[nb][i]);
+        rise = rise || now[nb][i] > m[nb][i];
       }
-      lA += (e0[0] + e0[1]) + (e1[0] + e1[1]);
-      lB += (e0[2] + e0[3]) + (e1[2] + e1[3]);
-      pa[0] = pack2<BF>(e0[0], e0[1]);
-      pa[1] = pack2<BF>(e0[2], e0[3]);
-      pa[2] = pack2<BF>(e1[0], e1[1]);
-      pa[3] = pack2<BF>(e1[2], e1[3]);
-    }
+    if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-    for (int nn = 0; nn < D / 16; ++nn) {
-      uint32_t b[4];
-      const int r = (mi & 1) * 8 + mr, c = 2 * nn + (mi >> 1);
-      ldsm4t(b, vs + piece_at(r, c));
-      mma16816<BF>(o[2 * nn], pa, b[0], b[1]);
-      mma16816<BF>(o[2 * nn + 1], pa, b[2], b[3]);
+      for (int nb = 0; nb < NB; ++nb) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // (-inf) - (-inf): a row that has seen nothing has nothing to scale
+          f[i] = m[nb][i] == now[nb][i] ? 1.f : exp2_approx(m[nb][i] - now[nb][i]);
+          l[nb][i] *= f[i];
+          m[nb][i] = now[nb][i];
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nb][d][e] *= f[e & 1];
+      }
     }
-    __syncwarp();  // the stage and Q are read before they are overwritten
+    // ---- P^T as the operand: keys in pairs along a lane, row g
+    uint32_t pb[MB][NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const float u0m = m[nb][0] == kNegInf ? 0.f : m[nb][0], u1m = m[nb][1] == kNegInf ? 0.f : m[nb][1];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const float e0 = exp2_approx(x[mb][nb][0] - u0m), e1 = exp2_approx(x[mb][nb][1] - u1m);
+        const float e2 = exp2_approx(x[mb][nb][2] - u0m), e3 = exp2_approx(x[mb][nb][3] - u1m);
+        l[nb][0] += e0 + e2;
+        l[nb][1] += e1 + e3;
+        pb[mb][nb][0] = transpose8(pack2<BF>(e0, e1));
+        pb[mb][nb][1] = transpose8(pack2<BF>(e2, e3));
+      }
+    }
+    // ---- O^T
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        // matrices (features 0-7, keys 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+        uint32_t a[4];
+        ldsm4t(a, vs + C::at(mb * 16 + (mi >> 1) * 8 + mr, 2 * d + (mi & 1)));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma16816<BF>(o[nb][d], a, pb[mb][nb][0], pb[mb][nb][1]);
+      }
+    __syncwarp();  // the stage is read before it is overwritten
     const bool ends = use.g + 1 == use.e.groups;
     if (ends || st + 1 == steps) {
-#pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {
-        lA += __shfl_xor_sync(0xffffffffu, lA, d);
-        lB += __shfl_xor_sync(0xffffffffu, lB, d);
-      }
       const bool whole = ends && !begun;
       const long long slot = 2ll * w + (begun ? 0 : 1);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
-        const float m = half ? mB : mA, l = half ? lB : lA;
-        if (r0 + r >= rows) continue;
-        if (!whole) {
-          float* d = p.part_o + (slot * kRowTile + r) * D + t2;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(d + i * 8) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
-          if ((lane & 3) == 0) p.part_ml[slot * kRowTile + r] = make_float2(m, l);
-        } else {
-          const int tok = fast_div(r0 + r, p.divG);
-          const int head = h * p.G + (r0 + r - tok * p.G);
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* d = p.o + (use.s.t0 + tok) * p.o_ts + head * p.o_hs + t2;
+        for (int i = 0; i < 2; ++i) {
+          float sum = l[nb][i];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint32_t*>(d + i * 8) =
-                pack2<BF>(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
-          if ((lane & 3) == 0 && p.lse)
-            p.lse[(long long)(use.s.t0 + tok) * p.Hq + head] =
-                l == 0.f ? kNegInf : kLn2 * m + logf(l);
+          for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const int r = 8 * nb + t2 + i;
+          if (r0 + r >= rows) continue;
+          if (!whole) {
+            float* dst = p.part_o + (slot * kRowTile + r) * D + g;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              dst[d * 16] = o[nb][d][i];
+              dst[d * 16 + 8] = o[nb][d][2 + i];
+            }
+            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(m[nb][i], sum);
+          } else {
+            const int tok = fast_div(r0 + r, p.divG);
+            const int head = use.h * p.G + (r0 + r - tok * p.G);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint16_t* dst = p.o + (use.s.t0 + tok) * p.o_ts + head * p.o_hs + g;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              dst[d * 16] = pack1<BF>(o[nb][d][i] * inv);
+              dst[d * 16 + 8] = pack1<BF>(o[nb][d][2 + i] * inv);
+            }
+            if (g == 0 && p.lse)
+              p.lse[(long long)(use.s.t0 + tok) * p.Hq + head] =
+                  sum == 0.f ? kNegInf : kLn2 * m[nb][i] + logf(sum);
+          }
         }
-      }
       fresh = true;
     }
     if (st + 1 < steps) advance(use);
@@ -605,15 +671,15 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
     step = 1;
     parts = p.chunks;
   } else {
-    const int r = (t - s.t0) * p.G + head % p.G, tile = r / kRowTile;
-    const Extent e = extent_of(p, s);
+    const int r = (t - s.t0) * p.G + head % p.G, tile = r / p.row_tile;
+    const Extent e = extent_of(p, s, RowsCfg<D>::KG, p.row_tile);
     const long long U = p.before[p.b.N];
     const long long u = p.before[n] + (long long)(tile * p.c.heads + head / p.G) * e.groups;
     const int warps = (int)min((long long)p.warps, U);
     const int w0 = owner_of(U, warps, u), w1 = owner_of(U, warps, u + e.groups - 1);
     if (w0 == w1) return;  // written by its warp
-    at = (2ll * w0 + 1) * kRowTile + r % kRowTile;
-    rest = 2ll * w0 * kRowTile + r % kRowTile;
+    at = (2ll * w0 + 1) * kRowTile + r % p.row_tile;
+    rest = 2ll * w0 * kRowTile + r % p.row_tile;
     step = 2 * kRowTile;
     parts = w1 - w0 + 1;
   }
@@ -626,7 +692,7 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   float l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = warp; c < parts; c += W) {
     const float2 x = p.part_ml[slot(c)];
     const float* po = p.part_o + slot(c) * D;
@@ -654,17 +720,17 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   if (threadIdx.x == 0 && p.lse) p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
 }
 
-template <int D, bool BF, bool TMA>
+template <int D, int NB, bool BF, bool TMA>
 cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
   using C = RowsCfg<D>;
   static bool attr_set = false;
   if (!attr_set) {
     const cudaError_t e = cudaFuncSetAttribute(
-        paged_rows_kernel<D, BF, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        paged_rows_kernel<D, NB, BF, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  return launch_kernel(paged_rows_kernel<D, BF, TMA>, dim3(rp.a.warps / kWarps), dim3(32 * kWarps),
+  return launch_kernel(paged_rows_kernel<D, NB, BF, TMA>, dim3(rp.a.warps / kWarps), dim3(32 * kWarps),
                        C::SMEM, st, rp);
 }
 
@@ -672,11 +738,15 @@ template <int D, bool BF>
 cudaError_t rows_launch(const AttnParams& p, cudaStream_t st) {
   RowsParams rp;
   rp.a = p;
-  rp.box = p.c.page % 16 == 0 ? 16 : 8;
-  if (p.c.page % 8 == 0 && make_page_map(&rp.k, p.c.k, p.c, 64, rp.box, BF) &&
-      make_page_map(&rp.v, p.c.v, p.c, 64, rp.box, BF))
-    return rows_launch_t<D, BF, true>(rp, st);
-  return rows_launch_t<D, BF, false>(rp, st);
+  int box = RowsCfg<D>::KG;
+  while (p.c.page % box) box >>= 1;
+  rp.box_log2 = 0;
+  while (1 << rp.box_log2 < box) ++rp.box_log2;
+  const bool tma = box >= 8 && make_page_map(&rp.k, p.c.k, p.c, 64, box, BF) &&
+                   make_page_map(&rp.v, p.c.v, p.c, 64, box, BF);
+  if (p.row_tile == 8)
+    return tma ? rows_launch_t<D, 1, BF, true>(rp, st) : rows_launch_t<D, 1, BF, false>(rp, st);
+  return tma ? rows_launch_t<D, 2, BF, true>(rp, st) : rows_launch_t<D, 2, BF, false>(rp, st);
 }
 
 template <int D, bool BF, int W>
@@ -696,7 +766,10 @@ cudaError_t join_w(const AttnParams& p, cudaStream_t st) {
 
 template <int D, bool BF>
 cudaError_t join_launch(const AttnParams& p, cudaStream_t st) {
-  return join_w<D, BF, 4>(p, st);
+  // a warp for four parts or so: a row's parts, a kilobyte each at D = 256, are
+  // read in as many rounds of latency as a warp has parts
+  if (p.parts <= 16) return join_w<D, BF, 4>(p, st);
+  return join_w<D, BF, 32>(p, st);
 }
 
 }  // namespace
