@@ -655,7 +655,6 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   __shared__ float sh_o[W][D];
   __shared__ float sh_l[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long rid = blockIdx.x;
   const int t = (int)(rid / p.Hq), head = (int)(rid - (long long)t * p.Hq);
   // new tokens outside every sequence have no partial results
@@ -663,6 +662,8 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   if (n < 0) return;
   const Seq s = load_seq(p.b, n);
   if (t < s.t0 || t >= s.t0 + s.nq) return;
+  // the batch's arrays were there before the partial results; those are now
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // part c of this row: slot (c ? rest + c * step : at), in rows
   long long at, rest, step;
   int parts;
