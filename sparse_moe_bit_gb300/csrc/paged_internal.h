@@ -90,7 +90,9 @@ struct RopeParams {
   CacheView c;
   BatchView b;
   int* err;
-  int tokens;  // tokens of a CTA
+  // set by the launch: tokens of a CTA, divisions
+  int tokens;
+  FastDiv div_r, div_tok, div_q, div_k, div_v;
 };
 cudaError_t launch_rope(const RopeParams& p, int dtype, bool append, cudaStream_t st);
 

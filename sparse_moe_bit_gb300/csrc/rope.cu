@@ -1,19 +1,22 @@
 // Rotary positions, alone and with the write of new keys and values into the
 // paged cache (include/paged.h).
 //
-// Pair i of a head at position pos turns by theta = pos f_i.  Only theta
-// modulo one turn matters, and that is exact in integers: with F = the 64-bit
-// fraction of f_i / (2 pi) turns, the low 64 bits of pos * F are the fraction
-// of a turn reached, off by at most pos 2^-53 of the fp64 frequency's own
-// rounding -- where pos * f in fp32 is off by 0.03 rad at 2^20 positions.  Its
-// top 32 bits, as a signed number of half turns, go to sincospif.
+// Pair i of a head at position pos turns by theta = pos f_i.  Only theta modulo
+// one turn matters, and that is exact in integers: with F = the 64-bit fraction of
+// f_i / (2 pi) turns, the low 64 bits of pos * F are the fraction of a turn
+// reached, off by at most pos 2^-64 -- where pos * f in fp32 is off by 0.03 rad at
+// 2^20 positions.  Its top 32 bits, as a signed number of half turns, go to
+// sincospif.  F comes from the bits of the fp64 frequency by integer products (the
+// few fp64 units would serialise the CTAs).
 //
-// Bound: HBM, one read and one write of every value.  A CTA takes a few
-// tokens, computes the r angles of each once into shared memory (they serve
-// every head) and then moves 16 bytes of each side of a pair a thread and
-// step.  Vectors need r (half layout) or 2r (interleaved) a multiple of the
-// 16 bytes and aligned rows; everything else takes the same loop one pair at a
-// time.
+// Bound: HBM, one read and one write of every value.  A CTA takes a few tokens,
+// computes the r angles of each once into shared memory (they serve every head)
+// and then moves 16 bytes of each side of a pair (eight pairs) a thread and step.
+// (A thread that keeps its piece of the head, with its angles in registers, and
+// walks the heads needs four times the registers and was slower by a factor of 1.1
+// to 4: what counts is the loads that many threads have in flight.)
+// Vectors need r (half layout) or 2r (interleaved) a multiple of the 16 bytes and
+// aligned rows; everything else takes the same loop one pair at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,6 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 6;  // about so many CTAs an SM
 
 template <typename T>
 __device__ __forceinline__ float to_f(T v);
@@ -69,7 +73,7 @@ __device__ __forceinline__ void rope_item(const T* src, T* dst, int u, int r, co
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float a = to_f(t[2 * j]), b = to_f(t[2 * j + 1]);
-        turn(a, b, cs[u * V + j]);
+        turn(a, b, cs[j * turns + u]);
         t[2 * j] = from_f<T>(a);
         t[2 * j + 1] = from_f<T>(b);
       }
@@ -82,7 +86,7 @@ __device__ __forceinline__ void rope_item(const T* src, T* dst, int u, int r, co
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float fa = to_f(a.e[j]), fb = to_f(b.e[j]);
-        turn(fa, fb, cs[u * V + j]);
+        turn(fa, fb, cs[j * turns + u]);
         a.e[j] = from_f<T>(fa);
         b.e[j] = from_f<T>(fb);
       }
@@ -93,6 +97,25 @@ __device__ __forceinline__ void rope_item(const T* src, T* dst, int u, int r, co
     const int i = (2 * r) / V + (u - turns);
     reinterpret_cast<W*>(dst)[i] = reinterpret_cast<const W*>(src)[i];
   }
+}
+
+// The 64-bit fraction of freq / (2 pi) turns, freq's bits given.
+__device__ __forceinline__ uint64_t turns_of(uint64_t bits) {
+  const int ex = (int)(bits >> 52 & 2047);
+  uint64_t man = bits & 0xfffffffffffffull;
+  if (ex) man |= 1ull << 52;
+  // freq = man 2^(e - 52); 1 / (2 pi) = kInv 2^-66; so turns 2^64 = man kInv 2^(e - 54)
+  constexpr uint64_t kInv = 0xa2f9836e4e44152aull;
+  const uint64_t hi = __umul64hi(man, kInv), lo = man * kInv;
+  const int sh = 54 - ((ex ? ex : 1) - 1023);  // to the right
+  uint64_t f = 0;
+  if (sh >= 64)
+    f = sh < 128 ? hi >> (sh - 64) : 0;
+  else if (sh > 0)
+    f = hi << (64 - sh) | lo >> sh;
+  else
+    f = sh > -64 ? lo << -sh : 0;
+  return bits >> 63 ? 0 - f : f;
 }
 
 struct Slot {
@@ -138,17 +161,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     slots[threadIdx.x] = s;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.r; i += kRopeThreads) {
-    const double turns = p.freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-    const double frac = turns - floor(turns);
-    const uint64_t F = __double2ull_rz(frac * 18446744073709551616.0);
-    for (int j = 0; j < nt; ++j) {
-      const uint64_t at = (uint64_t)(int64_t)slots[j].pos * F;  // modulo one turn
-      const float half = (float)(int32_t)(at >> 32) * 4.656612873077393e-10f;  // 2^-31
-      float s, c;
-      sincospif(half, &s, &c);
-      cs_all[j * p.r + i] = make_float2(c * p.mscale, s * p.mscale * p.sign);
-    }
+  for (int i = threadIdx.x; i < nt * p.r; i += kRopeThreads) {
+    const int j = fast_div(i, p.div_r);
+    const uint64_t bits = reinterpret_cast<const uint64_t*>(p.freq)[i - j * p.r];
+    const uint64_t at = (uint64_t)(int64_t)slots[j].pos * turns_of(bits);  // modulo one turn
+    const float half = (float)(int32_t)(at >> 32) * 4.656612873077393e-10f;  // 2^-31
+    // (no angle where the frequency is not a number)
+    const float scale = (bits >> 52 & 2047) == 2047 ? __int_as_float(0x7fffffff) : p.mscale;
+    float s, c;
+    sincospif(half, &s, &c);
+    // (the V angles of a piece apart: pieces of neighbouring threads side by side)
+    const int k = i - j * p.r;
+    cs_all[j * p.r + k % V * (p.r / V) + k / V] = make_float2(c * scale, s * scale * p.sign);
   }
   __syncthreads();
   const T* x = static_cast<const T*>(p.x);
@@ -161,27 +185,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int per_q = p.H * q_items, per_k = heads * all_items, per_v = heads * v_items;
   const int per_tok = per_q + per_k + per_v;
   for (int w = threadIdx.x; w < nt * per_tok; w += kRopeThreads) {
-    const int j = w / per_tok;
+    const int j = fast_div(w, p.div_tok);
     int u = w - j * per_tok;
     const Slot s = slots[j];
     const long long t = t0 + j;
     const float2* cs = cs_all + j * p.r;
     if (APPEND && s.seq < 0) continue;
     if (u < per_q) {
-      const int h = u / q_items;
+      const int h = fast_div(u, p.div_q);
       rope_item<T, V, INTER>(x + t * p.x_ts + h * p.x_hs, out + t * p.o_ts + h * p.o_hs,
                              u - h * q_items, p.r, cs);
     } else if constexpr (APPEND) {
       if (s.off < 0) continue;
       u -= per_q;
       if (u < per_k) {
-        const int h = u / all_items;
+        const int h = fast_div(u, p.div_k);
         rope_item<T, V, INTER>(static_cast<const T*>(p.k) + t * p.k_ts + (long long)h * p.D,
                                reinterpret_cast<T*>(p.c.k) + s.off + h * p.c.head_stride,
                                u - h * all_items, p.r, cs);
       } else {
         u -= per_k;
-        const int h = u / v_items, i = u - h * v_items;
+        const int h = fast_div(u, p.div_v), i = u - h * v_items;
         using W = Vec<T, V>;
         const T* src = static_cast<const T*>(p.v) + t * p.v_ts + (long long)h * p.D;
         T* dst = reinterpret_cast<T*>(p.c.v) + s.off + h * p.c.head_stride;
@@ -192,7 +216,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 }
 
 template <typename T, int V>
-cudaError_t launch_t(const RopeParams& p, bool append, cudaStream_t st) {
+cudaError_t launch_t(const RopeParams& p0, bool append, cudaStream_t st) {
+  RopeParams p = p0;
+  const int rot = p.r / V, all = rot + (p.D - 2 * p.r) / V, per_q = p.in_place ? rot : all;
+  p.div_r = make_fastdiv(p.r);
+  p.div_q = make_fastdiv(per_q);
+  p.div_k = make_fastdiv(all);
+  p.div_v = make_fastdiv(p.D / V > 0 ? p.D / V : 1);
+  p.div_tok = make_fastdiv(p.H * per_q + (append ? p.c.heads * (all + p.D / V) : 0));
+  // tokens of a CTA: one while the CTAs do not fill the machine three times over
+  // (a small call is over in one token's time, and the last wave of a large one is
+  // a small part), then up to eight, so that the lookups and angles of several
+  // tokens take one round of latency
+  const int full = device_sms() * kRopeCtas * 3;
+  p.tokens = p.T / full;
+  p.tokens = p.tokens < 1 ? 1 : (p.tokens > 8 ? 8 : p.tokens);
   const int grid = (p.T + p.tokens - 1) / p.tokens;
   const size_t smem = (size_t)p.tokens * p.r * sizeof(float2);
   void (*k)(RopeParams);
@@ -206,8 +244,7 @@ cudaError_t launch_t(const RopeParams& p, bool append, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeParams& p0, int dtype, bool append, cudaStream_t st) {
-  RopeParams p = p0;
+cudaError_t launch_rope(const RopeParams& p, int dtype, bool append, cudaStream_t st) {
   const int es = dtype == PAGED_F32 ? 4 : 2;
   const int V = 16 / es;
   // 16-byte vectors: whole vectors in each of the row's parts, aligned rows
@@ -215,12 +252,6 @@ cudaError_t launch_rope(const RopeParams& p0, int dtype, bool append, cudaStream
   bool vec = p.r % V == 0 && (p.D - 2 * p.r) % V == 0 && al(p.x) && al(p.out) && p.x_ts % V == 0 &&
              p.x_hs % V == 0 && p.o_ts % V == 0 && p.o_hs % V == 0;
   if (append) vec = vec && al(p.k) && al(p.v) && p.k_ts % V == 0 && p.v_ts % V == 0;
-  // tokens of a CTA: one while the CTAs do not fill the machine eight deep
-  // (a small call is over in one token's time), then up to eight, so that the
-  // angles' fp64 conversion and the slot lookup are paid once for several
-  const int sms = device_sms();
-  p.tokens = p.T / (sms * 8);
-  p.tokens = p.tokens < 1 ? 1 : (p.tokens > 8 ? 8 : p.tokens);
   if (dtype == PAGED_F32)
     return vec ? launch_t<float, 4>(p, false, st) : launch_t<float, 1>(p, false, st);
   if (dtype == PAGED_BF16)
