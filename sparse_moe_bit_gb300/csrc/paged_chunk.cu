@@ -63,8 +63,8 @@ struct ChunkCfg {
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_REF = (OFF_MISC + 64 + 15) / 16 * 16;  // float [4][128]
   static constexpr int OFF_MAX = OFF_REF + 4 * 128 * 4;           // float [4][2][128]
-  static constexpr int OFF_ML = OFF_MAX + 8 * 128 * 4;            // float2 [4][128]
-  static constexpr int USED = OFF_ML + 4 * 128 * 8 + 1024;
+  static constexpr int OFF_ML = 0;  // float4 [4][128], over Q, which is done with then
+  static constexpr int USED = OFF_MAX + 8 * 128 * 4 + 1024;
   // never two CTAs on an SM: each takes all of TMEM, and two pairs that held one
   // SM each would wait for one another
   static constexpr int SMEM = USED > 120000 ? USED : 120000;
@@ -219,6 +219,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
   }
 }
+// x rounded to the 16-bit type
+template <bool BF>
+__device__ __forceinline__ float round16(float x) {
+  if constexpr (BF) return __bfloat162float(__float2bfloat16_rn(x));
+  else return __half2float(__float2half_rn(x));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -263,6 +269,17 @@ __device__ __forceinline__ void tile_arrive(int g, int q) {
 __device__ __forceinline__ void tile_wait(int g, int q) {
   asm volatile("bar.sync %0, 96;" ::"r"(5 + g * 4 + q) : "memory");
 }
+// whether any thread of the softmax warps says so
+__device__ __forceinline__ bool softmax_any(int v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 13, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v), "n"(32 * kSoftWarps)
+      : "memory");
+  return r != 0;
+}
 // the four warps that share a lane quarter's rows
 __device__ __forceinline__ void quarter_sync(int q) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
@@ -303,6 +320,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = blockIdx.x & 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  // barriers and TMEM, while the other warps look for the tile
+  if (warp == 2 && lane == 0) {
+    mbar_init(B.q_full(), 2 * kSoftWarps);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(B.moved(i), 1);
+      // one softmax group's warps of both CTAs, and each CTA's copying warps
+      mbar_init(B.ready(i), kSoftWarps + 4);
+      mbar_init(B.k_first(i), 2);
+    }
+    mbar_init(B.drain(), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  auto leave = [&]() {  // every warp of both CTAs
+    tc_fence_before();
+    __syncthreads();
+    pair_sync_all();  // no CTA leaves while the other may still arrive on its barriers
+    if (warp == 1) {
+      tc_fence_after();
+      tmem_dealloc_pair(*tmem_slot, 512);
+    }
+  };
+
   int bid = blockIdx.x >> 1;
   const int ck = bid % p.chunks;
   bid /= p.chunks;
@@ -337,9 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     before += total;
     if (want < before) break;  // uniform
   }
+  tc_fence_before();
   __syncthreads();
   const int n = sh_find[0];
-  if (n < 0) return;  // uniform over the pair: both CTAs look for the same tile
+  if (n < 0) {  // uniform over the pair: both CTAs look for the same tile
+    leave();
+    return;
+  }
   const int tile = sh_find[1];
   const Seq s = load_seq(p.b, n);
   const int rows = s.nq * p.G;
@@ -375,36 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part == 0 && p.lse) p.lse[rid] = kNegInf;
       }
     }
+    leave();
     return;
   }
 
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  if (threadIdx.x == 0) {
-    mbar_init(B.q_full(), 2 * kSoftWarps);
-    for (int i = 0; i < C::NS; ++i) {
-      mbar_init(B.moved(i), 1);
-      // one softmax group's warps of both CTAs, and each CTA's copying warps
-      mbar_init(B.ready(i), kSoftWarps + 4);
-      mbar_init(B.k_first(i), 2);
-    }
-    mbar_init(B.drain(), 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), 512);
-    tmem_relinquish_pair();
-  }
-  // page numbers of this chunk that are bad (then every score is looked at)
-  int bad = 0;
-  for (int c = fast_div(lo, p.c.div) + threadIdx.x; c <= fast_div(hi - 1, p.c.div); c += kThreads) {
-    const int pg = table[c];
-    if (pg < 0 || pg >= p.c.pages) bad = 1;
-  }
-  tc_fence_before();
-  const bool any_bad = __syncthreads_or(bad);
-  if (any_bad && threadIdx.x == 0) atomicOr(p.err, PAGED_DEVERR_PAGE);
   pair_sync_all();  // the other CTA's barriers are there before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -636,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------- softmax, correction, epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    bool any_bad;
     {
       // Q: warp w copies rows 8 w .. 8 w + 7 of the CTA's 128
       constexpr int CH = D / 8, RPI = 32 / CH;
@@ -655,6 +680,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_release_cluster(mapa_shared(B.q_full(), 0));
+      // page numbers of this chunk that are bad (then every score is looked at)
+      int bad = 0;
+      for (int i = fast_div(lo, p.c.div) + threadIdx.x - 32 * kSoftWarp0;
+           i <= fast_div(hi - 1, p.c.div); i += 32 * kSoftWarps) {
+        const int pg = table[i];
+        if (pg < 0 || pg >= p.c.pages) bad = 1;
+      }
+      any_bad = softmax_any(bad);
+      if (any_bad && threadIdx.x == 32 * kSoftWarp0) atomicOr(p.err, PAGED_DEVERR_PAGE);
     }
     // visible keys of the row: [vlo, vhi); rows that do not exist see all (of zeros)
     int vlo = 0, vhi = 0x7fffffff;
@@ -681,6 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = p.scale_log2;
     // the reference that this thread's sum l (over its own scores) is relative to
     float m = kNegInf, l = 0.f;
+    // The weights are rounded to 16 bits for the product, l sums them unrounded
+    // (the lse is its logarithm).  With a lagging reference the largest weight,
+    // which the result follows most, is rounded like any other; so the result is
+    // divided by l with the rounding of each tile's largest weight put back:
+    // `extra` is what that adds up to (of the row: in one half's threads).
+    float extra = 0.f;
     if (group == 1 && half == 0) {  // "after tile -1"
       sh_ref[3 * 128 + trow] = kNegInf;
       tile_arrive(0, quarter);
@@ -757,10 +797,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st_wait();
         }
-        l = m == kNegInf ? 0.f : l * ex2((m - now) * c);
+        const float f = m == kNegInf ? 0.f : ex2((m - now) * c);
+        l *= f;
+        extra *= f;
         m = now;
       }
       const float mc = m == kNegInf ? 0.f : m * c;
+      {
+        const float top = ex2(fmaf(mx, c, -mc));
+        extra += round16<BF>(top) - top;
+      }
       // two values at a time where the machine can: x c - mc, and the sums
       const uint64_t c2 = pack_f2(c, c), mc2 = pack_f2(-mc, -mc);
       uint64_t sum[2] = {0, 0};
@@ -795,26 +841,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = ok && warp_wait(B.drain(), 0, abort_flag, p.err);
     // the row's whole sum from its four parts
     const int part = half + 2 * group;
-    float2* sh_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-    sh_ml[part * 128 + trow] = make_float2(m, l);
+    float4* sh_ml = reinterpret_cast<float4*>(smem + C::OFF_ML);
+    sh_ml[part * 128 + trow] = make_float4(m, l, half == 0 ? extra : 0.f, 0.f);
     quarter_sync(quarter);
     {
       float top = kNegInf;  // the last tile's reference, O's
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, sh_ml[i * 128 + trow].x);
-      l = 0.f;
+      l = extra = 0.f;
       if (top != kNegInf) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 y = sh_ml[i * 128 + trow];
-          l += y.y * ex2((y.x - top) * c);
+          const float4 y = sh_ml[i * 128 + trow];
+          const float f = ex2((y.x - top) * c);
+          l += y.y * f;
+          extra += y.z * f;
         }
       }
       m = top;
     }
     if (ok) {
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // (a part of a row: for a join that divides by the sum of the l)
+      const float inv = l == 0.f ? 0.f : (p.chunks > 1 ? l : 1.f) / (l + extra);
       const float mlog = m * c;  // (-inf: no key seen)
 #pragma unroll 1
       for (int f0 = 0; f0 < D / 4; f0 += 16) {
@@ -827,8 +876,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4* d4 = reinterpret_cast<float4*>(p.part_o + (rid * p.chunks + ck) * D + f);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            d4[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            d4[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
         } else {
           uint16_t* dst = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f;
 #pragma unroll
@@ -849,13 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  tc_fence_before();
-  __syncthreads();
-  pair_sync_all();  // no CTA leaves while the other may still arrive on its barriers
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
-  }
+  leave();
 }
 
 template <int D, bool BF, bool TMA>

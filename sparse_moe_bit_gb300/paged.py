@@ -33,6 +33,7 @@ _BATCH = struct.Struct("@PPPiiiq")
 
 
 _lib = None
+_sizes: dict = {}  # workspace bytes of paged_attention by the call's sizes
 
 
 def _check(status):
@@ -162,7 +163,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, mscale: f
         raise ValueError("one position a token")
     f, r = _freq(freq)
     if out is None:
-        out = x.new_empty((T, H, D))
+        out = torch.empty_strided((T, H, D), (H * D, D, 1), dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must be like x")
     xs, os_ = x.stride(), out.stride()
@@ -200,7 +201,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torc
         raise ValueError("heads must be D apart")
     f, r = _freq(freq)
     if q_out is None:
-        q_out = q.new_empty((T, Hq, D))
+        q_out = torch.empty_strided((T, Hq, D), (Hq * D, D, 1), dtype=dt, device=q.device)
     elif q_out.shape != q.shape or q_out.dtype is not dt or not q_out.is_contiguous():
         raise ValueError("q_out must be dense and like q")
     _check(_library().rope_append(q.data_ptr(), qs[0], q_out.data_ptr(), Hq, k.data_ptr(), ks[0],
@@ -229,22 +230,28 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     if q.dtype is not k_pages.dtype or D != k_pages.shape[3]:
         raise ValueError("q must match the cache's type and dim")
     if out is None:
-        out = q.new_empty((T, Hq, D))
+        out = torch.empty_strided((T, Hq, D), (Hq * D, D, 1), dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must be like q")
     qs, os_ = q.stride(), out.stride()
     if qs[2] != 1 or os_[2] != 1:
         raise ValueError("features must be contiguous")
     b = _batch(table, cu_q, kv_len, T)
-    lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check(lib.paged_attention_workspace(c, b, Hq, window, max_q, max_kv, ctypes.byref(need)))
-        size, ws = need.value, None
+        # (a function of these sizes alone, on one kind of GPU)
+        key = (T, Hq, k_pages.dtype, *k_pages.shape[1:], *table.shape, window, max_q, max_kv)
+        size, ws = _sizes.get(key), None
+        if size is None:
+            need = ctypes.c_size_t(0)
+            _check(lib.paged_attention_workspace(c, b, Hq, window, max_q, max_kv, ctypes.byref(need)))
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            size = _sizes[key] = need.value
         if size:
-            workspace = q.new_empty((size,), dtype=torch.uint8)
+            workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
         size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
@@ -294,7 +301,7 @@ def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, a
     S = lens.shape[0]
     if add.shape[0] != S:
         raise ValueError("one number a slot")
-    buf = refs.new_empty((3 * S + 3,))   # moves, status, scratch
+    buf = torch.empty((3 * S + 3,), dtype=torch.int32, device=refs.device)  # moves, status, scratch
     moves, status = buf.as_strided((S, 2), (2, 1)), buf.as_strided((2,), (1,), 2 * S)
     at = buf.data_ptr()
     _check(_library().pages_reserve(*st, lens.data_ptr(), add.data_ptr(), S, page,
@@ -318,7 +325,7 @@ def pages_compact(refs: torch.Tensor, table: torch.Tensor, stream=None):
     int32 [P, 2] and their count (int32 scalar), for pages_copy."""
     st = _state(refs, table)
     P = refs.shape[0]
-    buf = refs.new_empty((3 * P + 2,))   # moves, count, scratch
+    buf = torch.empty((3 * P + 2,), dtype=torch.int32, device=refs.device)  # moves, count, scratch
     moves, count = buf.as_strided((P, 2), (2, 1)), buf.as_strided((), (), 2 * P)
     at = buf.data_ptr()
     _check(_library().pages_compact(*st, table.shape[0], at, at + 8 * P,
