@@ -1023,28 +1023,6 @@ cudaError_t make_tmap_16bit(CUtensorMap* map, const void* base, long long rows, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_paged(CUtensorMap* map, const void* base, const long long (&dims)[4],
-                            const long long (&strides)[3], const int (&box)[4], bool bf16,
-                            bool swizzle128) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  cuuint64_t d[4], s[3];
-  cuuint32_t b[4];
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  for (int i = 0; i < 4; ++i) {
-    d[i] = (cuuint64_t)dims[i];
-    b[i] = (cuuint32_t)box[i];
-  }
-  // (a dimension of one element is never stepped along: any stride will do)
-  for (int i = 0; i < 3; ++i) s[i] = dims[i + 1] == 1 ? 16 : (cuuint64_t)strides[i];
-  const CUresult r =
-      fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-         const_cast<void*>(base), d, s, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 cudaError_t launch_grouped_mma(int mode, const MmaParams& p, int grid, cudaStream_t st) {
   if (grid <= 0) return cudaSuccess;
   if (mode == MMA_ROUTER) return launch_mode<MMA_ROUTER, 1, false>(p, grid, st);

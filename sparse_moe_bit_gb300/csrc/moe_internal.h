@@ -158,11 +158,6 @@ cudaError_t launch_grouped_mma(int mode, const MmaParams& p, int grid, cudaStrea
 // 128-byte swizzle (the tensor-core operand layout), zero fill out of bounds
 cudaError_t make_tmap_16bit(CUtensorMap* map, const void* base, long long rows, long long cols,
                             int box_rows, bool bf16);
-// 4-D tensor map over 16-bit values (innermost dimension first; strides of the
-// outer three in bytes), 128-byte swizzle or 64-byte, zero fill out of bounds
-cudaError_t make_tmap_paged(CUtensorMap* map, const void* base, const long long (&dims)[4],
-                            const long long (&strides)[3], const int (&box)[4], bool bf16,
-                            bool swizzle128);
 
 // ---- routing (routing.cu)
 // top-k, histogram, scan + tile map, scatter and (x non-null) the fp16 copy of

@@ -39,6 +39,37 @@ int device_sms() {
   return sms[dev];
 }
 
+bool make_page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box,
+                   bool bf16) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+  static Encode encode = nullptr;
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    encode = reinterpret_cast<Encode>(f);
+  }
+  const cuuint64_t dims[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.page, (cuuint64_t)c.heads,
+                              (cuuint64_t)c.pages};
+  // (a dimension of one element is never stepped along: any stride will do)
+  const cuuint64_t strides[3] = {c.page == 1 ? 16 : (cuuint64_t)c.row_stride * 2,
+                                 c.heads == 1 ? 16 : (cuuint64_t)c.head_stride * 2,
+                                 c.pages == 1 ? 16 : (cuuint64_t)c.page_stride * 2};
+  const cuuint32_t boxes[4] = {(cuuint32_t)features, (cuuint32_t)box, 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<void*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                features == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
 
 namespace {

@@ -132,16 +132,12 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
   if (p.window > 0) lo = max(0, p0 - p.window + 1);
   return make_int2(lo, max(hi, lo));
 }
-// A tensor map over one of the cache's arrays: boxes of `box` rows of a page x
-// `features` (64: 128-byte swizzle, 32: 64-byte); false where the array has none
-// (a stride that the encoding refuses).
-inline bool make_page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box,
-                          bool bf16) {
-  const long long dims[4] = {c.dim, c.page, c.heads, c.pages};
-  const long long strides[3] = {c.row_stride * 2, c.head_stride * 2, c.page_stride * 2};
-  const int boxes[4] = {features, box, 1, 1};
-  return make_tmap_paged(m, base, dims, strides, boxes, bf16, features == 64) == cudaSuccess;
-}
+// A tensor map over one of the cache's arrays (innermost first: feature, row of a
+// page, head, page): boxes of `box` rows of a page x `features` (64: 128-byte
+// swizzle, 32: 64-byte), zero fill out of bounds; false where the array has none
+// (a stride that the encoding refuses).  (paged_api.cu)
+bool make_page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box,
+                   bool bf16);
 constexpr int kRowTile = 16, kRowWarps = 4;
 cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
 constexpr int kPairRows = 256;
