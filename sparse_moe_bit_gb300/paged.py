@@ -1,9 +1,10 @@
 """Binding of include/paged.h: rotary positions, the paged key/value cache and
 attention over it (argument marshalling only; no fallback path).
 
-Tensors are CUDA tensors; shapes, types and strides are checked here, values
-that only the GPU can see are handled by the kernels (include/paged.h says
-how).  Every call enqueues on ``stream`` (default: torch's current one)."""
+Tensors are CUDA tensors of the current device; that, shapes, types and strides
+are checked here, values that only the GPU can see are handled by the kernels
+(include/paged.h says how).  Every call enqueues on ``stream`` (default: torch's
+current one)."""
 from __future__ import annotations
 
 import ctypes
@@ -83,6 +84,18 @@ def _i32(t, ndim, name):
         raise ValueError(f"{name} must be contiguous along its last axis")
 
 
+def _placed(t, *others):
+    """Every tensor has to lie on the current device: the kernels run there, and an
+    address of the host or of another device would be a memory fault in them.
+    (Where there is no device at all the library says so.)"""
+    d = t.get_device()
+    if d != _current_device() if d >= 0 else _have_gpu():
+        raise ValueError(f"tensors must be on the current GPU, not on {t.device}")
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError(f"tensors must be on one GPU, not on {t.device} and {o.device}")
+
+
 def _stream(stream, t) -> int:
     """The raw stream: the given one, or torch's current one of t's device."""
     if stream is not None:
@@ -94,6 +107,9 @@ def _stream(stream, t) -> int:
 
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
     else (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+_have_gpu = torch.cuda.is_available
 
 
 def _made(stream, *tensors):
@@ -135,10 +151,11 @@ def _freq(freq):
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
                      factor: float = 1.0, original: int = 0, low: float = 1.0,
                      high: float = 32.0, device=None):
-    """Radians a position of every pair (fp64 [rotary_dim / 2] on ``device``) and
-    the factor on cos and sin: plain, or scaled ("linear", "ntk", "yarn",
-    "banded"; include/paged.h has the formulas) for contexts ``factor`` times
-    the ``original`` length."""
+    """Radians a position of every pair (fp64 [rotary_dim / 2] on ``device``, by
+    default the host; rope and rope_append take them on the GPU) and the factor
+    on cos and sin: plain, or scaled ("linear", "ntk", "yarn", "banded";
+    include/paged.h has the formulas) for contexts ``factor`` times the
+    ``original`` length."""
     _need(scaling in SCALINGS, f"unknown scaling {scaling!r}")
     f = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
     m = ctypes.c_double(1.0)
@@ -158,6 +175,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, mscale: f
     if dt is None or x.dim() != 3:
         raise ValueError("x must be [T, H, D] of bf16, fp16 or fp32")
     T, H, D = x.shape
+    _placed(x, positions, freq, out)
     _i32(positions, 1, "positions")
     if positions.shape[0] != T:
         raise ValueError("one position a token")
@@ -189,6 +207,7 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torc
     the first three axes, the same for both), table int32 [N, width], cu_q
     int32 [N + 1], kv_len int32 [N] (new tokens included), freq fp64 [r]."""
     T, Hq, D = q.shape
+    _placed(q, k, v, k_pages, v_pages, table, cu_q, kv_len, freq, q_out)
     c = _cache(k_pages, v_pages)
     dt, hk = k_pages.dtype, k_pages.shape[2]
     kv = (T, hk, k_pages.shape[3])
@@ -226,6 +245,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     made here (paged_attention_workspace() in include/paged.h)."""
     lib = _library()
     T, Hq, D = q.shape
+    _placed(q, k_pages, v_pages, table, cu_q, kv_len, out, workspace)
     c = _cache(k_pages, v_pages)
     if q.dtype is not k_pages.dtype or D != k_pages.shape[3]:
         raise ValueError("q must match the cache's type and dim")
@@ -278,6 +298,7 @@ def pages_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, src:
     """Slot dst[i] of the table becomes a copy of slot src[i] that shares its
     pages (refs int32 [P], table int32 [S, width], lens int32 [S], in place).
     ``refused``: int32 [1], the number of pairs left out."""
+    _placed(refs, table, lens, src, dst, refused)
     st = _state(refs, table, lens)
     _i32(src, 1, "src")
     _i32(dst, 1, "dst")
@@ -296,6 +317,7 @@ def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, a
     (the page to copy from and to, or -1, -1: hand them to pages_copy) and
     status int32 [2] (pages missing, slots whose row is too short; nothing was
     changed unless both are 0)."""
+    _placed(refs, table, lens, add)
     st = _state(refs, table, lens)
     _i32(add, 1, "add")
     S = lens.shape[0]
@@ -314,6 +336,7 @@ def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, a
 def pages_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slots: torch.Tensor,
                stream=None) -> None:
     """The slots give up their pages, in place."""
+    _placed(refs, table, lens, slots)
     st = _state(refs, table, lens)
     _i32(slots, 1, "slots")
     _check(_library().pages_free(*st, lens.data_ptr(), lens.shape[0], slots.data_ptr(),
@@ -323,6 +346,7 @@ def pages_free(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, slot
 def pages_compact(refs: torch.Tensor, table: torch.Tensor, stream=None):
     """Renumber the pages in use to the lowest numbers, in place.  Returns moves
     int32 [P, 2] and their count (int32 scalar), for pages_copy."""
+    _placed(refs, table)
     st = _state(refs, table)
     P = refs.shape[0]
     buf = torch.empty((3 * P + 2,), dtype=torch.int32, device=refs.device)  # moves, count, scratch
@@ -342,6 +366,7 @@ def pages_copy(pools: torch.Tensor, moves: torch.Tensor, count: torch.Tensor | N
     shape, st, es = pools.shape, pools.stride(), pools.element_size()
     if len(shape) < 3:
         raise ValueError("pools must be [B, P, ...]")
+    _placed(pools, moves, count)
     _i32(moves, 2, "moves")
     if moves.shape[1] != 2 or (moves.shape[0] > 1 and moves.stride(0) != 2):
         raise ValueError("moves must be dense [M, 2]")
