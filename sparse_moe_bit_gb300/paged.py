@@ -96,6 +96,11 @@ def _placed(t, *others):
             raise ValueError(f"tensors must be on one GPU, not on {t.device} and {o.device}")
 
 
+def _one(t, name):
+    if t is not None and (t.dtype is not torch.int32 or t.numel() != 1):
+        raise ValueError(f"{name} must be one int32")
+
+
 def _stream(stream, t) -> int:
     """The raw stream: the given one, or torch's current one of t's device."""
     if stream is not None:
@@ -274,6 +279,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
             workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     _check(lib.paged_attention(q.data_ptr(), qs[0], qs[1], Hq, c, b, scale, causal, window, max_q,
                                max_kv, out.data_ptr(), os_[0], os_[1],
@@ -304,6 +311,7 @@ def pages_fork(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, src:
     _i32(dst, 1, "dst")
     if src.shape != dst.shape:
         raise ValueError("src and dst must have one length")
+    _one(refused, "refused")
     _check(_library().pages_fork(*st, lens.data_ptr(), lens.shape[0], src.data_ptr(),
                                       dst.data_ptr(), src.shape[0],
                                       None if refused is None else refused.data_ptr(),
@@ -375,8 +383,7 @@ def pages_copy(pools: torch.Tensor, moves: torch.Tensor, count: torch.Tensor | N
         if shape[i] != 1 and st[i] != n:
             raise ValueError("a page's rows must be contiguous")
         n *= shape[i]
-    if count is not None and count.dtype is not torch.int32:
-        raise ValueError("count must be int32")
+    _one(count, "count")
     _check(_library().pages_copy(pools.data_ptr(), shape[0], st[0] * es, shape[1], st[1] * es,
                                  n * es, moves.data_ptr(), moves.shape[0],
                                  None if count is None else count.data_ptr(),

@@ -85,3 +85,25 @@ def test_tensors_elsewhere_are_refused(lib, i, stream, monkeypatch):
         assert lib.calls == []
         fn(**tensors, **more, stream=stream)
         assert lib.calls
+
+
+def test_buffers_smaller_than_what_is_written_are_refused(lib):
+    """A workspace whose elements share memory, and counts that are not one int32:
+    the library would read and write past them."""
+    with FakeTensorMode():
+        calls = _calls("cuda")
+        one = torch.empty(1, dtype=torch.uint8, device="cuda")
+        wide = torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")
+        i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")
+        for i, name, bad in [(2, "workspace", one.expand(1 << 20)), (2, "workspace", wide[:, 0]),
+                             (3, "refused", i32(1).to(torch.uint8)), (3, "refused", i32(0)),
+                             (3, "refused", i32(2)), (7, "count", i32(0)), (7, "count", i32(3)),
+                             (7, "count", i32(1).long())]:
+            fn, tensors, more = calls[i]
+            with pytest.raises(ValueError):
+                fn(**dict(tensors, **{name: bad}), **more)
+        assert lib.calls == []
+        for i, name, good in [(3, "refused", i32()), (7, "count", i32(1)), (7, "count", None),
+                              (2, "workspace", torch.empty(64, 64, device="cuda"))]:
+            fn, tensors, more = calls[i]
+            fn(**dict(tensors, **{name: good}), **more)
