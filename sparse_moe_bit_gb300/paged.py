@@ -117,15 +117,32 @@ _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice
 _have_gpu = torch.cuda.is_available
 
 
-def _made(stream, *tensors):
-    """Tensors made here lie in the current stream's pool: tell the allocator of the
-    other stream that uses them."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _new(stream, shape, strides, dtype, device):
+    """A tensor for the kernels on ``stream`` (None: the current one) to write.
+    It comes from that stream's pool: a block of another stream's may still be in
+    use there by work that was queued before its last holder let go of it."""
+    if stream is None or device.type != "cuda":
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+
+
+def _torch_stream(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _used(stream, made, given):
+    """After a call on a given stream: what was made here goes back to the caller,
+    whose current stream may read it last; what was given belongs to another stream
+    and is used on this one.  The allocator is told of both."""
+    if stream is None:
+        return
+    for t in made:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream(t.device))
+    for t in given:
+        if t is not None:
+            t.record_stream(_torch_stream(stream))
 
 
 def _cache(k, v):
@@ -185,8 +202,9 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, mscale: f
     if positions.shape[0] != T:
         raise ValueError("one position a token")
     f, r = _freq(freq)
-    if out is None:
-        out = torch.empty_strided((T, H, D), (H * D, D, 1), dtype=x.dtype, device=x.device)
+    made = out is None
+    if made:
+        out = _new(stream, (T, H, D), (H * D, D, 1), x.dtype, x.device)
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must be like x")
     xs, os_ = x.stride(), out.stride()
@@ -195,7 +213,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, mscale: f
     _check(_library().rope(x.data_ptr(), out.data_ptr(), dt, T, H, D, xs[0], xs[1], os_[0], os_[1],
                            positions.data_ptr(), f, r, mscale, interleaved, inverse,
                            _stream(stream, x)))
-    _made(stream, out)
+    if stream is not None:
+        _used(stream, [out] if made else (), () if made else [out])
     return out
 
 
@@ -224,14 +243,16 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_pages: torc
             or (hk > 1 and (ks[1] != D or vs[1] != D))):
         raise ValueError("heads must be D apart")
     f, r = _freq(freq)
-    if q_out is None:
-        q_out = torch.empty_strided((T, Hq, D), (Hq * D, D, 1), dtype=dt, device=q.device)
+    made = q_out is None
+    if made:
+        q_out = _new(stream, (T, Hq, D), (Hq * D, D, 1), dt, q.device)
     elif q_out.shape != q.shape or q_out.dtype is not dt or not q_out.is_contiguous():
         raise ValueError("q_out must be dense and like q")
     _check(_library().rope_append(q.data_ptr(), qs[0], q_out.data_ptr(), Hq, k.data_ptr(), ks[0],
                                   v.data_ptr(), vs[0], c, _batch(table, cu_q, kv_len, T), f, r,
                                   mscale, interleaved, _stream(stream, q)))
-    _made(stream, q_out)
+    if stream is not None:
+        _used(stream, [q_out] if made else (), () if made else [q_out])
     return q_out
 
 
@@ -254,15 +275,16 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     c = _cache(k_pages, v_pages)
     if q.dtype is not k_pages.dtype or D != k_pages.shape[3]:
         raise ValueError("q must match the cache's type and dim")
+    given = (out, workspace)
     if out is None:
-        out = torch.empty_strided((T, Hq, D), (Hq * D, D, 1), dtype=q.dtype, device=q.device)
+        out = _new(stream, (T, Hq, D), (Hq * D, D, 1), q.dtype, q.device)
     elif out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("out must be like q")
     qs, os_ = q.stride(), out.stride()
     if qs[2] != 1 or os_[2] != 1:
         raise ValueError("features must be contiguous")
     b = _batch(table, cu_q, kv_len, T)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = _new(stream, (T, Hq), (Hq, 1), torch.float32, q.device) if return_lse else None
     if scale is None:
         scale = D ** -0.5
     if workspace is None:
@@ -276,7 +298,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                 _sizes.clear()
             size = _sizes[key] = need.value
         if size:
-            workspace = torch.empty((size,), dtype=torch.uint8, device=q.device)
+            workspace = _new(stream, (size,), (1,), torch.uint8, q.device)
             ws = workspace.data_ptr()
     else:
         if not workspace.is_contiguous():
@@ -286,7 +308,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                                max_kv, out.data_ptr(), os_[0], os_[1],
                                None if lse is None else lse.data_ptr(), ws, size,
                                _stream(stream, q)))
-    _made(stream, out, lse, workspace)
+    if stream is not None:  # (a workspace made here is let go of on the stream that uses it)
+        _used(stream, (lse,) if given[0] is out else (out, lse), given)
     return (out, lse) if return_lse else out
 
 
@@ -331,13 +354,13 @@ def pages_reserve(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, a
     S = lens.shape[0]
     if add.shape[0] != S:
         raise ValueError("one number a slot")
-    buf = torch.empty((3 * S + 3,), dtype=torch.int32, device=refs.device)  # moves, status, scratch
+    buf = _new(stream, (3 * S + 3,), (1,), torch.int32, refs.device)  # moves, status, scratch
     moves, status = buf.as_strided((S, 2), (2, 1)), buf.as_strided((2,), (1,), 2 * S)
     at = buf.data_ptr()
     _check(_library().pages_reserve(*st, lens.data_ptr(), add.data_ptr(), S, page,
                                          at, at + 8 * S, at + 8 * S + 8,
                                          _stream(stream, refs)))
-    _made(stream, buf)
+    _used(stream, (buf,), ())
     return moves, status
 
 
@@ -357,12 +380,12 @@ def pages_compact(refs: torch.Tensor, table: torch.Tensor, stream=None):
     _placed(refs, table)
     st = _state(refs, table)
     P = refs.shape[0]
-    buf = torch.empty((3 * P + 2,), dtype=torch.int32, device=refs.device)  # moves, count, scratch
+    buf = _new(stream, (3 * P + 2,), (1,), torch.int32, refs.device)  # moves, count, scratch
     moves, count = buf.as_strided((P, 2), (2, 1)), buf.as_strided((), (), 2 * P)
     at = buf.data_ptr()
     _check(_library().pages_compact(*st, table.shape[0], at, at + 8 * P,
                                          at + 8 * P + 4, _stream(stream, refs)))
-    _made(stream, buf)
+    _used(stream, (buf,), ())
     return moves, count
 
 

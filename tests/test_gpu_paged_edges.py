@@ -29,3 +29,32 @@ def test_host_tensors_are_refused():
                             stream=stream)
     torch.cuda.synchronize()
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("new,kv", [([1], [5000]), ([40], [300]), ([30], [9000])])
+def test_given_stream_does_not_write_where_the_current_one_still_works(new, kv):
+    """A block let go of on the current stream while its work is still queued there:
+    outputs and workspaces of a call on another stream must not be made of it."""
+    b = make_batch(2, new, kv, 16, 1, 128, BF, 4, device="cuda")
+    names = ("q", "k", "v", "table", "cu", "kv_len")
+    f = torch.ones(8, dtype=torch.float64, device="cuda")
+    pos = torch.arange(new[0], dtype=torch.int32, device="cuda")
+    want = M.paged_attention(*(b[x] for x in names), return_lse=True)
+    turned = M.rope(b["q"], pos, f)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty_like(want[0]) for _ in range(3)] + [torch.empty_like(want[1])]
+    blocks += [torch.empty(40 << 20, dtype=torch.uint8, device="cuda")]
+    at = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in blocks]
+    torch.cuda._sleep(20_000_000)            # some 10 ms
+    for t in blocks:
+        t.fill_(7)
+    del blocks, t
+    o, lse = M.paged_attention(*(b[x] for x in names), return_lse=True, stream=st)
+    y = M.rope(b["q"], pos, f, stream=st)
+    for t in (o, lse, y):
+        assert not any(a <= t.data_ptr() < z for a, z in at)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, turned)
+    assert M.paged_device_error() == 0

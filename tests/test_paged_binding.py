@@ -1,6 +1,7 @@
 """The binding of include/paged.h where a call must not reach the library: no
 GPU.  Tensors on a GPU are stood in for by torch's fake ones."""
 import contextlib
+import sys
 
 import pytest
 import torch
@@ -107,3 +108,67 @@ def test_buffers_smaller_than_what_is_written_are_refused(lib):
                               (2, "workspace", torch.empty(64, 64, device="cuda"))]:
             fn, tensors, more = calls[i]
             fn(**dict(tensors, **{name: good}), **more)
+
+
+class _Pool:
+    """Stands in for the streams of torch: which one is current, and which one each
+    tensor was made on and is said to be used on."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.made, self.told = "mine", {}, {}
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw: raw)
+        monkeypatch.setattr(torch.cuda, "stream", self._enter)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(torch.Tensor, "record_stream",
+                            lambda t, s: self.told.setdefault(id(t), []).append(s))
+        for name in ("empty", "empty_strided"):
+            monkeypatch.setattr(torch, name, self._maker(getattr(torch, name)))
+        self.kept = []
+
+    @contextlib.contextmanager
+    def _enter(self, stream):
+        old, self.current = self.current, stream
+        yield
+        self.current = old
+
+    def _maker(self, make):
+        def f(*args, **kw):
+            t = make(*args, **kw)
+            if sys._getframe(1).f_globals["__name__"] == paged.__name__:
+                self.made[id(t)] = self.current
+                self.kept.append(t)
+            return t
+        return f
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["made", "given"])
+@pytest.mark.parametrize("i", range(8))
+def test_tensors_come_from_the_pool_of_the_stream_that_writes_them(lib, monkeypatch, i, given):
+    """What a call makes for a given stream to write must not be a block that the
+    current stream may still be using; what it returns is used on the current
+    stream, and what it was given to write on the given one."""
+    with FakeTensorMode():
+        fn, tensors, more = _calls("cuda")[i]
+        if not given:
+            tensors = {n: t for n, t in tensors.items()
+                       if n not in ("out", "q_out", "workspace", "refused", "count")}
+        if fn is M.paged_attention:
+            more = dict(return_lse=True)
+            monkeypatch.setattr(paged, "_sizes", _Sizes())
+        pool = _Pool(monkeypatch)
+        r = fn(**tensors, **more, stream=_Stream())
+        assert [s for s in pool.made.values() if s != 0x77] == []
+        mine = [t for t in (r if isinstance(r, tuple) else (r,)) if t is not None]
+        for t in mine:
+            if id(t) in pool.made:
+                assert pool.told.get(id(t)) == ["mine"]
+        for n in ("out", "q_out", "workspace"):
+            if n in tensors:
+                assert pool.told.get(id(tensors[n])) == [0x77]
+
+
+class _Sizes(dict):
+    """Every call needs a workspace."""
+
+    def get(self, key):
+        return 4096
