@@ -662,13 +662,15 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long rid = blockIdx.x;
   const int t = (int)(rid / p.Hq), head = (int)(rid - (long long)t * p.Hq);
-  // new tokens outside every sequence have no partial results
+  // (the batch's arrays were there before the partial results)
   const int n = find_seq(p.b, t);
-  if (n < 0) return;
-  const Seq s = load_seq(p.b, n);
-  if (t < s.t0 || t >= s.t0 + s.nq) return;
-  // the batch's arrays were there before the partial results; those are now
+  const Seq s = load_seq(p.b, max(n, 0));
+  // The partial results are there behind this wait.  No CTA leaves before it: this
+  // grid must not be over before the first one, whose workspace may be another's
+  // from then on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // new tokens outside every sequence have no partial results
+  if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
   // part c of this row: slot (c ? rest + c * step : at), in rows
   long long at, rest, step;
   int parts;

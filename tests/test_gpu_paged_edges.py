@@ -58,3 +58,20 @@ def test_given_stream_does_not_write_where_the_current_one_still_works(new, kv):
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(y, turned)
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("nq", [1, 30])
+def test_tokens_outside_every_sequence_leave_no_trace(nq):
+    """No token belongs to a sequence: nothing is written but the workspace, and
+    that not after the call."""
+    b = make_batch(3, [nq], [9000], 16, 1, 128, BF, 4, device="cuda")
+    b["cu"].fill_(nq)
+    out = torch.full_like(b["q"], 5.0)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], max_q=nq,
+                          max_kv=9000, out=out, workspace=ws)
+        ws.fill_(i)
+    torch.cuda.synchronize()
+    assert torch.all(ws == 19) and torch.all(out == 5)
+    assert M.paged_device_error() == 0
