@@ -39,9 +39,12 @@ enum { PAGED_BF16 = 1, PAGED_F16 = 2, PAGED_F32 = 3 };
 enum {
   PAGED_DEVERR_WAIT_TIMEOUT = 1, /* an internal wait passed its limit (the
                                     outputs of that call are not valid)     */
-  PAGED_DEVERR_PAGE = 2          /* a token's page number was outside
+  PAGED_DEVERR_PAGE = 2,         /* a token's page number was outside
                                     [0, pages): rope_append did not write
                                     it, attention left its key out          */
+  PAGED_DEVERR_LENGTH = 4        /* a token of rope_append stood past the
+                                    width * page tokens that a row of the
+                                    table holds: it was not written         */
 };
 
 /* One layer's cache.  k and v 16-byte aligned; strides in elements, multiples
@@ -61,9 +64,11 @@ typedef struct paged_cache {
  * another.  Sequence n's new tokens are cu_q[n] .. cu_q[n+1]-1; kv_len[n]
  * counts its tokens, the new ones included, so that its i-th new token stands
  * at position kv_len[n] - (cu_q[n+1] - cu_q[n]) + i.  All arrays int32, on
- * the device.  cu_q is read clamped into [0, T] and non-decreasing, kv_len
- * into [0, width * page]; new tokens at negative positions (a kv_len below
- * the number of new tokens) see no key and are not written to the cache. */
+ * the device.  cu_q is read clamped into [0, T] and non-decreasing, a negative
+ * kv_len as 0.  New tokens at negative positions (a kv_len below the number
+ * of new tokens) see no key and are not written to the cache.  A row of the
+ * table holds width * page tokens: rope_append writes none past them (a device
+ * error bit), paged_attention reads a larger kv_len as that many. */
 typedef struct paged_batch {
   const int32_t* table; /* [N][width], rows table_stride apart */
   const int32_t* cu_q;  /* [N + 1] */

@@ -143,8 +143,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       if (s.seq >= 0) {
         const Seq q = load_seq(p.b, s.seq);
         if (t >= q.t0 && t < q.t0 + q.nq) {
-          s.pos = q.kv - q.nq + (t - q.t0);
-          if (s.pos >= 0) {
+          // (kv_len as it is: clamped to the row's capacity it would put tokens that
+          // have no place over the last ones that have)
+          s.pos = max(p.b.kv_len[s.seq], 0) - q.nq + (t - q.t0);
+          if (s.pos >= p.b.capacity) {
+            atomicOr(p.err, PAGED_DEVERR_LENGTH);
+          } else if (s.pos >= 0) {
             const int col = fast_div(s.pos, p.c.div);
             const int pg = p.b.table[s.seq * p.b.table_stride + col];
             if (pg >= 0 && pg < p.c.pages)

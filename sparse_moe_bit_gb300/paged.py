@@ -16,6 +16,7 @@ from . import moe as _moe
 
 PAGED_DEVERR_WAIT_TIMEOUT = 1
 PAGED_DEVERR_PAGE = 2
+PAGED_DEVERR_LENGTH = 4
 
 # names of the functions include/paged.h declares (checked by its ABI test)
 EXPORTS = ["rope", "rope_frequencies", "rope_append", "paged_attention_workspace",

@@ -75,3 +75,27 @@ def test_tokens_outside_every_sequence_leave_no_trace(nq):
     torch.cuda.synchronize()
     assert torch.all(ws == 19) and torch.all(out == 5)
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("page,width", [(16, 3), (1, 7)])
+def test_append_past_the_table_row_leaves_the_cache_alone(page, width):
+    """More tokens than a row of the table has pages for: those that fit go where
+    they belong, the rest nowhere, and an error bit says so."""
+    cap = page * width
+    b = make_batch(4, [5, 2], [cap, 2], page, 2, 64, BF, 4, device="cuda", width=width)
+    b["kv_len"] = torch.tensor([cap + 3, cap + 1000], dtype=torch.int32, device="cuda")
+    q, k, v = (torch.randn(7, h, 64, device="cuda").to(BF) for h in (4, 2, 2))
+    f = torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64, device="cuda")
+    kp, vp = b["k"].clone(), b["v"].clone()
+    y = M.rope_append(q, k, v, kp, vp, b["table"], b["cu"], b["kv_len"], f)
+    assert M.paged_device_error() == M.PAGED_DEVERR_LENGTH
+    pos = torch.tensor([cap - 2, cap - 1, cap, cap + 1, cap + 2, cap + 998, cap + 999],
+                       dtype=torch.int32, device="cuda")
+    assert torch.equal(y, M.rope(q, pos, f))
+    turned = M.rope(k, pos, f)
+    for i, p in ((0, cap - 2), (1, cap - 1)):
+        pg = b["table"][0, p // page].long()
+        assert torch.equal(kp[pg, p % page], turned[i]) and torch.equal(vp[pg, p % page], v[i])
+        kp[pg, p % page], vp[pg, p % page] = b["k"][pg, p % page], b["v"][pg, p % page]
+    assert torch.equal(kp, b["k"]) and torch.equal(vp, b["v"])
+    assert M.paged_device_error() == 0
