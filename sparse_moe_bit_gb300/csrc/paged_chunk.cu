@@ -861,14 +861,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, sh_ml[i * 128 + trow].x);
       l = extra = 0.f;
-      if (top != kNegInf) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 y = sh_ml[i * 128 + trow];
-          const float f = ex2((y.x - top) * c);
-          l += y.y * f;
-          extra += y.z * f;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float4 y = sh_ml[i * 128 + trow];
+        // (no key seen: (-inf) - (-inf); there l is 0, or NaN where the scores were,
+        // which raise no maximum)
+        const float f = y.x == top ? 1.f : ex2((y.x - top) * c);
+        l += y.y * f;
+        extra += y.z * f;
       }
       m = top;
     }

@@ -99,3 +99,20 @@ def test_append_past_the_table_row_leaves_the_cache_alone(page, width):
         kp[pg, p % page], vp[pg, p % page] = b["k"][pg, p % page], b["v"][pg, p % page]
     assert torch.equal(kp, b["k"]) and torch.equal(vp, b["v"])
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,kv", [(1, 50), (1, 5000), (40, 90), (40, 128), (30, 9000)])
+def test_nan_queries_show_in_output_and_lse(nq, kv, d):
+    """A query that is not a number gives an output and an lse that are not, in one
+    piece or split over the keys, and no other row does."""
+    b = make_batch(5, [nq], [kv], 16, 1, d, BF, 2, device="cpu")
+    b["q"][nq - 1, 1, 7] = float("nan")
+    b = {n: t.cuda() for n, t in b.items()}
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], max_q=nq,
+                               max_kv=kv, return_lse=True)
+    want = torch.zeros(nq, 2, dtype=torch.bool, device="cuda")
+    want[nq - 1, 1] = True
+    assert torch.equal(torch.isnan(lse), want)
+    assert torch.equal(torch.isnan(o).all(-1), want) and torch.equal(torch.isnan(o).any(-1), want)
+    assert M.paged_device_error() == 0
