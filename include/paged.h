@@ -137,7 +137,7 @@ moe_status rope_append(const void* q, int64_t q_token_stride, void* q_out, int H
  *   o = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j)
  * A query that sees no key gets o = 0 and lse = -inf.  Scores, softmax
  * statistics and sums are fp32; the weights are rounded to the cache's type
- * for the product with v.  Rows of the cache at or past kv_len, or whose page
+ * (in fp16 at the upper end of its range) for the product with v.  Rows of the cache at or past kv_len, or whose page
  * number is bad, may hold anything, NaN included; values of visible rows are
  * expected to be finite (a non-finite value may reach queries of its chunk
  * that do not see it).

@@ -138,6 +138,12 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
 // (a stride that the encoding refuses).  (paged_api.cu)
 bool make_page_map(CUtensorMap* m, const void* base, const CacheView& c, int features, int box,
                    bool bf16);
+// Log2 of the largest softmax weight that is rounded to the 16-bit type.  fp16 holds
+// 2^15 and rounds off by up to 2^-25 whatever is small: with weights up to 1 a key 17.4
+// nats behind the largest would vanish, and a long tail of such keys with it
+// (one-sidedly, while the sums count them).  bf16 has fp32's exponents.
+template <bool BF>
+constexpr float kTopWeight = BF ? 0.f : 15.f;
 constexpr int kRowTile = 16, kRowWarps = 4;
 cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
 constexpr int kPairRows = 256;

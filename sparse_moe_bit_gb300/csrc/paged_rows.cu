@@ -7,6 +7,9 @@
 // so that every key and value is read from HBM once for the whole group.
 //   S = Q K^T, m' = max(m, rowmax S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
 //   O = O 2^(m - m') + P V                         (S in log2 units, all fp32)
+// (fp16: P = 2^(S - m' + 15), so that small weights stay in the type's range, off by
+// half a step or 2^-40 of the largest; l and O likewise, with m' - 15 as their
+// reference.)
 //
 // Bound: HBM (2 bytes x 2 D per key against 2 x 4 D x rows operations).  What
 // counts is bytes in flight and an even share for every SM, so the keys are cut
@@ -566,7 +569,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     uint32_t pb[MB][NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float u0m = m[nb][0] == kNegInf ? 0.f : m[nb][0], u1m = m[nb][1] == kNegInf ? 0.f : m[nb][1];
+      const float u0m = m[nb][0] == kNegInf ? 0.f : m[nb][0] - kTopWeight<BF>;
+      const float u1m = m[nb][1] == kNegInf ? 0.f : m[nb][1] - kTopWeight<BF>;
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         const float e0 = exp2_approx(x[mb][nb][0] - u0m), e1 = exp2_approx(x[mb][nb][1] - u1m);
@@ -600,6 +604,7 @@ __global__ void __launch_bounds__(32 * kWarps)
           float sum = l[nb][i];
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const float ref = m[nb][i] - kTopWeight<BF>;
           const int r = 8 * nb + t2 + i;
           if (r0 + r >= rows) continue;
           if (!whole) {
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(32 * kWarps)
               dst[d * 16] = o[nb][d][i];
               dst[d * 16 + 8] = o[nb][d][2 + i];
             }
-            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(m[nb][i], sum);
+            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(ref, sum);
           } else {
             const int tok = fast_div(r0 + r, p.divG);
             const int head = use.h * p.G + (r0 + r - tok * p.G);
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(32 * kWarps)
             }
             if (g == 0 && p.lse)
               p.lse[(long long)(use.s.t0 + tok) * p.Hq + head] =
-                  sum == 0.f ? kNegInf : kLn2 * m[nb][i] + logf(sum);
+                  sum == 0.f ? kNegInf : kLn2 * ref + logf(sum);
           }
         }
       fresh = true;

@@ -1,4 +1,5 @@
 """Narrow cases of the paged-cache calls (include/paged.h) on the GPU."""
+import numpy as np
 import pytest
 import torch
 
@@ -116,3 +117,37 @@ def test_nan_queries_show_in_output_and_lse(nq, kv, d):
     assert torch.equal(torch.isnan(lse), want)
     assert torch.equal(torch.isnan(o).all(-1), want) and torch.equal(torch.isnan(o).any(-1), want)
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("few", [True, False], ids=["rows", "chunk"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_fp16_keeps_the_tail_behind_a_sink(d, few):
+    """One key that takes nearly all of the weight and 20,000 that are 17.4 nats
+    below it, each less than half of fp16's smallest step: together they are the
+    whole result (the key's value is 0).  So many items that no key is split off."""
+    kv, page = 20_000, 64
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, nq = (4 * sms, 1) if few else (1, 256 * sms)
+    pages = -(-kv // page)
+    k = torch.zeros(pages, page, 1, d, dtype=FP, device="cuda")
+    k[0, 0, 0, 0] = 1.0
+    v = torch.full((pages, page, 1, d), 1.0, dtype=FP, device="cuda")
+    v[0, 0] = 0.0
+    q = torch.zeros(n * nq, 1, d, dtype=FP, device="cuda")
+    q[:, 0, 0] = 17.4
+    z = q[0, 0, 0].double().item()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(n, pages)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda") * nq
+    o, lse = M.paged_attention(q, k, v, table, cu, torch.full((n,), kv, dtype=torch.int32, device="cuda"),
+                               scale=1.0, causal=False, max_q=nq, max_kv=kv, return_lse=True)
+    assert M.paged_device_error() == 0
+    tail = (kv - 1) * np.exp(-z)
+    ref, l_ref = tail / (1 + tail), z + np.log1p(tail)
+    # A weight is off by half a step: 2^-11 of itself, or 2^-25 where it is subnormal, in
+    # a scale where the largest is 2^15 (rows) or the reference 2^7 (chunk); the result
+    # by 2^-11; fp32 sums of kv terms, the score's fp32 error, the exponential's 2^-21.
+    f = ((d + 4) * z + kv) * 2.0 ** -24 + 2.0 ** -21
+    small = (kv - 1) * 2.0 ** -(25 + (15 if few else 7))
+    err = (o.double() - ref).abs().max().item()
+    assert err <= ref * (2 * 2.0 ** -11 + 2 * f) + small, f"off by {err / ref:.3f} of the result"
+    assert (lse.double() - l_ref).abs().max().item() <= f + 4 * 2.0 ** -24 * l_ref
