@@ -132,15 +132,15 @@ moe_status rope_append(const void* q, int64_t q_token_stride, void* q_out, int H
 /*
  * Attention of the new tokens over the cache (their own keys and values
  * written before).  Query head h reads key/value head h / (Hq / heads).  For
- * a query at position p, over the keys j < kv_len[n] with
+ * a query at position p >= 0, over the keys j < kv_len[n] with
  *   causal: j <= p;   window > 0: p - j < window
  *   o = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j)
  * A query that sees no key gets o = 0 and lse = -inf.  Scores, softmax
  * statistics and sums are fp32; the weights are rounded to the cache's type
- * (in fp16 at the upper end of its range) for the product with v.  Rows of the cache at or past kv_len, or whose page
- * number is bad, may hold anything, NaN included; values of visible rows are
- * expected to be finite (a non-finite value may reach queries of its chunk
- * that do not see it).
+ * (in fp16 at the upper end of its range) for the product with v.  Rows of
+ * the cache at or past kv_len, or whose page number is bad, may hold anything,
+ * NaN included; values of visible rows are expected to be finite (a non-finite
+ * value may reach queries of its chunk that do not see it).
  *   q, o   cache dtype [T][Hq][D], token and head strides in elements,
  *          multiples of 8, 16-byte aligned; must not overlap
  *   lse    fp32 [T][Hq] dense, or NULL

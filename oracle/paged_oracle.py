@@ -69,7 +69,7 @@ def attention(q, k_pages, v_pages, table, cu, kv_len, scale, causal=True, window
         for i in range(nq):
             pos = kv - nq + i
             see = good.copy()
-            if causal:
+            if causal or pos < 0:   # a token that stands before position 0 sees no key
                 see &= j <= pos
             if window:
                 see &= pos - j < window

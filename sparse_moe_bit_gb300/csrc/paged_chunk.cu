@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int vlo = 0, vhi = 0x7fffffff;
     if (valid) {
       const int pos = s.kv - s.nq + tok;
-      vhi = p.causal ? min(s.kv, pos + 1) : s.kv;
+      vhi = p.causal || pos < 0 ? min(s.kv, pos + 1) : s.kv;
       vlo = p.window > 0 ? pos - p.window + 1 : 0;
     } else {
       vhi = s.kv;

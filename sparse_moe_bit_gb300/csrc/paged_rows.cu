@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       const int pos0 = use.s.kv - use.s.nq;
       auto vis = [&](int r, int& a, int& b) {
         const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
-        b = p.causal ? min(use.s.kv, pos + 1) : use.s.kv;
+        b = p.causal || pos < 0 ? min(use.s.kv, pos + 1) : use.s.kv;
         a = p.window > 0 ? pos - p.window + 1 : 0;
       };
 #pragma unroll

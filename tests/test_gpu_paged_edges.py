@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sparse_moe_bit_gb300 as M
-from tests.paged_cases import make_batch
+from tests.paged_cases import attention_reference, check_attention, make_batch
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -127,7 +127,7 @@ def test_fp16_keeps_the_tail_behind_a_sink(d, few):
     whole result (the key's value is 0).  So many items that no key is split off."""
     kv, page = 20_000, 64
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    n, nq = (4 * sms, 1) if few else (1, 256 * sms)
+    n, nq = (4 * sms, 1) if few else (sms, 256)
     pages = -(-kv // page)
     k = torch.zeros(pages, page, 1, d, dtype=FP, device="cuda")
     k[0, 0, 0, 0] = 1.0
@@ -151,3 +151,23 @@ def test_fp16_keeps_the_tail_behind_a_sink(d, few):
     err = (o.double() - ref).abs().max().item()
     assert err <= ref * (2 * 2.0 ** -11 + 2 * f) + small, f"off by {err / ref:.3f} of the result"
     assert (lse.double() - l_ref).abs().max().item() <= f + 4 * 2.0 ** -24 * l_ref
+
+
+@pytest.mark.parametrize("window", [0, 4, 500])
+@pytest.mark.parametrize("nq", [3, 60])
+def test_tokens_before_position_0_see_nothing(nq, window):
+    """A context shorter than the chunk: the tokens that stand before position 0 see
+    no key, causal or not."""
+    new, kv, causal = [nq, nq, 2], [nq - 2, 0, 40], False
+    b = make_batch(6, new, kv, 16, 2, 128, BF, 4, device="cuda", fill=float("nan"))
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], causal=causal,
+                               window=window, max_q=nq, max_kv=max(kv), return_lse=True)
+    early = torch.zeros(sum(new), dtype=torch.bool, device="cuda")
+    early[:2] = early[nq:2 * nq] = True
+    assert torch.all(o[early] == 0) and torch.all(torch.isneginf(lse[early]))
+    assert torch.all(torch.isfinite(lse[~early])) and torch.all(torch.isfinite(o))
+    ref = attention_reference(b, 128 ** -0.5, causal, window)
+    keep = (~early).cpu().numpy()
+    for r in ref:
+        r[~keep] = np.nan        # (rows that the comparison leaves out)
+    check_attention(o, lse, ref, BF, 128, max(kv))
