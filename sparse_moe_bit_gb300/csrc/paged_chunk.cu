@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (valid) {
       const int pos = s.kv - s.nq + tok;
       vhi = p.causal || pos < 0 ? min(s.kv, pos + 1) : s.kv;
-      vlo = p.window > 0 ? pos - p.window + 1 : 0;
+      vlo = p.window > 0 ? window_begin(pos, p.window) : 0;
     } else {
       vhi = s.kv;
     }

@@ -122,6 +122,9 @@ struct AttnParams {
   float2* part_ml;  // [..]: running maximum (log2 units) and sum
   int* err;
 };
+// The first key in a query's window.  (A query before position 0 sees none; its
+// position less a window near 2^31 would not fit.)
+__device__ __forceinline__ int window_begin(int pos, int window) { return max(pos, 0) - window + 1; }
 // the first and one past the last key that rows [r0, r1) of a sequence see
 // (r1 > r0; row r is new token r / G)
 __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int r0, int r1) {
@@ -129,7 +132,7 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int
   const int p1 = s.kv - s.nq + fast_div(r1 - 1, p.divG);
   int lo = 0, hi = s.kv;
   if (p.causal) hi = min(hi, p1 + 1);
-  if (p.window > 0) lo = max(0, p0 - p.window + 1);
+  if (p.window > 0) lo = max(0, window_begin(p0, p.window));
   return make_int2(lo, max(hi, lo));
 }
 // A tensor map over one of the cache's arrays (innermost first: feature, row of a

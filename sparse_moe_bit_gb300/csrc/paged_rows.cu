@@ -157,7 +157,7 @@ struct Extent {
 };
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Seq& s, int kg, int tile) {
   Extent e;
-  e.first = p.window > 0 ? max(0, s.kv - s.nq - p.window + 1) : 0;
+  e.first = p.window > 0 ? max(0, window_begin(s.kv - s.nq, p.window)) : 0;
   e.lo = e.first & ~(kg - 1);  // groups do not straddle pages that hold whole ones
   e.groups = max((s.kv - e.lo + kg - 1) / kg, 1);
   e.items = (s.nq * p.G + tile - 1) / tile * p.c.heads;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       auto vis = [&](int r, int& a, int& b) {
         const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
         b = p.causal || pos < 0 ? min(use.s.kv, pos + 1) : use.s.kv;
-        a = p.window > 0 ? pos - p.window + 1 : 0;
+        a = p.window > 0 ? window_begin(pos, p.window) : 0;
       };
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {

@@ -271,6 +271,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     softmax's sums [T, Hq].  ``workspace``: a byte tensor to use instead of one
     made here (paged_attention_workspace() in include/paged.h)."""
     lib = _library()
+    if max(window, max_q, max_kv) > 0x7fffffff:  # beyond any context, and beyond an int
+        window, max_q, max_kv = (min(x, 0x7fffffff) for x in (window, max_q, max_kv))
     T, Hq, D = q.shape
     _placed(q, k_pages, v_pages, table, cu_q, kv_len, out, workspace)
     c = _cache(k_pages, v_pages)

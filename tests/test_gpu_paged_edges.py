@@ -171,3 +171,15 @@ def test_tokens_before_position_0_see_nothing(nq, window):
     for r in ref:
         r[~keep] = np.nan        # (rows that the comparison leaves out)
     check_attention(o, lse, ref, BF, 128, max(kv))
+
+
+@pytest.mark.parametrize("nq", [2, 12, 60])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 8, 1 << 31, 1 << 40])
+def test_windows_larger_than_every_context_hide_nothing(nq, window):
+    new, kv = [nq, nq], [max(nq - 9, 1), 100]
+    b = make_batch(7, new, kv, 16, 1, 64, BF, 4, device="cuda")
+    a = (b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"])
+    for causal in (True, False):
+        kw = dict(causal=causal, max_q=nq, max_kv=100, return_lse=True)
+        for x, y in zip(M.paged_attention(*a, window=window, **kw), M.paged_attention(*a, **kw)):
+            assert torch.equal(x, y)
