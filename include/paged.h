@@ -182,7 +182,8 @@ moe_status pages_fork(int32_t* refs, int P, int32_t* table, int64_t table_stride
  * page}, whose rows the caller copies (pages_copy) before it writes; otherwise
  * moves[s] = {-1, -1}.  Pages go to slots in order of s, each slot's exchanged
  * page first.  All or nothing: status[0] = pages that were missing, status[1]
- * = slots whose row of the table is too short; where either is not 0 nothing
+ * = slots whose row of the table is too short (or whose length would pass
+ * 2^31 - 1); where either is not 0 nothing
  * but status and moves (all -1) is written.
  * scratch: int32 [S + 1]. */
 moe_status pages_reserve(int32_t* refs, int P, int32_t* table, int64_t table_stride, int width,

@@ -107,7 +107,7 @@ __device__ __forceinline__ Need need_of(int s, const int32_t* refs, int P, const
   const long long len = max(lens[s], 0), more = max(add[s], 0);
   n.have = (int)((len + page - 1) / page);
   const long long want = (len + more + page - 1) / page;
-  n.narrow = more > 0 && want > width;
+  n.narrow = more > 0 && (want > width || len + more > 0x7fffffff);  // (lens is int32)
   n.want = n.narrow ? n.have : (int)want;
   n.own = 0;
   n.last = -1;

@@ -183,3 +183,16 @@ def test_windows_larger_than_every_context_hide_nothing(nq, window):
         kw = dict(causal=causal, max_q=nq, max_kv=100, return_lse=True)
         for x, y in zip(M.paged_attention(*a, window=window, **kw), M.paged_attention(*a, **kw)):
             assert torch.equal(x, y)
+
+
+def test_reserve_past_the_largest_length_is_refused():
+    """A length that does not fit its int32 counts as a row that is too short."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    page = 1 << 30
+    refs, table, lens = i32(1, 1, 0, 0), i32(0, 1, -1, -1)[None].clone(), i32(2 ** 31 - 10)
+    keep = refs.clone(), table.clone(), lens.clone()
+    moves, status = M.pages_reserve(refs, table, lens, i32(10), page)
+    assert status.tolist() == [0, 1] and moves.tolist() == [[-1, -1]]
+    assert torch.equal(refs, keep[0]) and torch.equal(table, keep[1]) and torch.equal(lens, keep[2])
+    moves, status = M.pages_reserve(refs, table, lens, i32(9), page)
+    assert status.tolist() == [0, 0] and lens.tolist() == [2 ** 31 - 1]
