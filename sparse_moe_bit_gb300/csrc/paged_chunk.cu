@@ -924,13 +924,9 @@ template <int D, bool BF, bool TMA>
 cudaError_t chunk_launch_t(const ChunkParams& cp, cudaStream_t st) {
   using C = ChunkCfg<D>;
   const AttnParams& p = cp.a;
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        paged_chunk_kernel<D, BF, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem((const void*)paged_chunk_kernel<D, BF, TMA>, C::SMEM, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(2ll * p.tiles * p.c.heads * p.chunks));
   c.blockDim = dim3(kThreads);

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "moe_internal.h"
@@ -174,5 +175,8 @@ cudaError_t launch_pages_copy(uint8_t* pools, int B, long long pool_stride, int 
 int* paged_error_word();
 // multiprocessors of the current device
 int device_sms();
+// Lets `kern` have `bytes` of dynamic shared memory on the current device, where it
+// takes effect; `done`, the kernel's own, says on which it has been set.
+cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done);
 
 }  // namespace moe

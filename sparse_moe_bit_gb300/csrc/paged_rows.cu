@@ -736,13 +736,9 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
 template <int D, int NB, bool BF, bool TMA>
 cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
   using C = RowsCfg<D>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        paged_rows_kernel<D, NB, BF, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem((const void*)paged_rows_kernel<D, NB, BF, TMA>, C::SMEM, allowed);
+  if (e != cudaSuccess) return e;
   return launch_kernel(paged_rows_kernel<D, NB, BF, TMA>, dim3(rp.a.warps / kWarps), dim3(32 * kWarps),
                        C::SMEM, st, rp);
 }
