@@ -214,7 +214,8 @@ moe_status pages_copy(void* pools, int B, int64_t pool_stride, int P, int64_t pa
                       void* stream);
 
 /* Synchronise `stream` and read (then clear) the current device's error word
- * of this header's calls (PAGED_DEVERR_* bits). */
+ * of this header's calls (PAGED_DEVERR_* bits).  One word serves all streams
+ * of the device; a bit that is set after the read stays for the next call. */
 moe_status paged_get_device_error(void* stream, int* code);
 
 #ifdef __cplusplus

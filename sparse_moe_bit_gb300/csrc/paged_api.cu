@@ -12,7 +12,12 @@ namespace moe {
 namespace {
 __device__ int g_paged_err;
 constexpr int kMaxDevices = 64;
+__global__ void clear_bits_kernel(int* word, int bits) { atomicAnd(word, ~bits); }
 }  // namespace
+
+static cudaError_t launch_clear_bits(int* word, int bits, cudaStream_t st) {
+  return launch_kernel(clear_bits_kernel, dim3(1), dim3(1), 0, st, word, bits);
+}
 
 int* paged_error_word() {
   static int* at[kMaxDevices] = {};
@@ -529,8 +534,11 @@ moe_status paged_get_device_error(void* stream, int* code) {
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int v = 0;
   PAGED_CK(cudaMemcpyAsync(&v, w, 4, cudaMemcpyDeviceToHost, st), "read error word");
-  PAGED_CK(cudaMemsetAsync(w, 0, 4, st), "clear error word");
   PAGED_CK(cudaStreamSynchronize(st), "synchronise");
+  if (v) {  // what was read and no more: kernels of other streams may set bits meanwhile
+    PAGED_CK(launch_clear_bits(w, v, st), "clear error word");
+    PAGED_CK(cudaStreamSynchronize(st), "synchronise");
+  }
   *code = v;
   return v ? MOE_ERR_DEVICE : MOE_OK;
 }

@@ -120,3 +120,19 @@ var("fake_fail_attribute").value = 1
 print(json.dumps([attend(128, 1), attend(128, 1)]))
 """)
     assert r[0] == 3 and r[1] == 0
+
+
+def test_error_bits_set_while_the_word_is_read_are_not_lost(run):
+    """A kernel on another stream sets a bit between the read of the error word and
+    its clearing: the next call reports it."""
+    r = run(r"""
+code = ctypes.c_int()
+out = []
+var("fake_word").value = 2
+var("fake_or_after_read").value = 1
+for i in range(3):
+    out.append([lib.paged_get_device_error(None, ctypes.byref(code)), code.value])
+    var("fake_or_after_read").value = 0
+print(json.dumps(out))
+""")
+    assert r == [[5, 2], [5, 1], [0, 0]]
