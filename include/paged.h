@@ -146,7 +146,7 @@ moe_status rope_append(const void* q, int64_t q_token_stride, void* q_out, int H
  *   lse    fp32 [T][Hq] dense, or NULL
  *   max_q, max_kv  what the caller knows of the longest chunk and context;
  *          they choose the kernel and the split over the keys and bound
- *          nothing (0: not known)
+ *          nothing (0: not known; T / N and the table's width stand in)
  *   workspace  16-byte aligned, paged_attention_workspace() bytes for the
  *          same sizes (which may be 0); holds nothing between calls
  */

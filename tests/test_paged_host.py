@@ -136,3 +136,25 @@ for i in range(3):
 print(json.dumps(out))
 """)
     assert r == [[5, 2], [5, 1], [0, 0]]
+
+
+def test_a_batch_of_single_tokens_takes_the_kernel_for_few_rows_unasked(run):
+    """Without max_q the mean number of new tokens chooses: a decode batch gets the
+    plan that max_q = 1 gets, more than 8 rows a key/value head (4 query heads each
+    here) the plan of chunks."""
+    r = run(r"""
+def size(N, T, max_q, max_kv=0):
+    c = Cache(A, A, 1, 4096, 16, 2, 128, 16 * 256, 256, 128)
+    b = Batch(A, A, A, N, T, 256, 256)
+    n = ctypes.c_size_t()
+    assert lib.paged_attention_workspace(ctypes.byref(c), ctypes.byref(b), 8, 0, max_q, max_kv,
+                                         ctypes.byref(n)) == 0
+    return n.value
+few = [[size(64, 64, 0), size(64, 64, 1), size(64, 64, 64)],
+       [size(64, 128, 0), size(64, 128, 2), size(64, 128, 65)]]
+many = [[size(8, 24, 0), size(8, 24, 17), size(8, 24, 3)],
+        [size(8, 800, 0), size(8, 800, 100), size(8, 800, 1)]]
+print(json.dumps([few, many, size(0, 0, 0), size(0, 5, 0)]))
+""")
+    for none, mean, other in r[0] + r[1]:
+        assert none == mean and none != other
