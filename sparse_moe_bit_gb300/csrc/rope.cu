@@ -18,8 +18,9 @@
 // Measured: 16385 tokens x 32 heads x 128, bf16, all turned: 46 us, 5.8 TB/s of
 // reads and writes (0.87 of the copy rate, 40 registers); 8313 new tokens of 32
 // query and 8 key/value heads of 128 into the cache 38 us, 0.80 of it.
-// Vectors need r (half layout) or 2r (interleaved) a multiple of the 16 bytes and
-// aligned rows; everything else takes the same loop one pair at a time.
+// Vectors need r and the rest of the head (D - 2r) to be multiples of the 16 bytes' 8
+// (fp32: 4) values, in either layout, and aligned rows; everything else takes the same
+// loop one pair at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
