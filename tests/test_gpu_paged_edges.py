@@ -196,3 +196,55 @@ def test_reserve_past_the_largest_length_is_refused():
     assert torch.equal(refs, keep[0]) and torch.equal(table, keep[1]) and torch.equal(lens, keep[2])
     moves, status = M.pages_reserve(refs, table, lens, i32(9), page)
     assert status.tolist() == [0, 0] and lens.tolist() == [2 ** 31 - 1]
+
+
+@pytest.mark.parametrize("page", [16, 64, 6])
+@pytest.mark.parametrize("d,dtype", [(64, FP), (128, BF), (256, BF)])
+@pytest.mark.parametrize("nq,window", [(1, 40), (3, 129), (70, 33), (130, 200)])
+def test_keys_before_every_window_may_be_gone(nq, window, d, dtype, page):
+    """A sliding window's server gives pages back: what lies before the first query's
+    window is NaN, and the pages that hold nothing else have bad numbers."""
+    new, kv = [nq, 1], [nq + 500, 450]
+    b = make_batch(8, new, kv, page, 2, d, dtype, 4, device="cpu")
+    ref = attention_reference(b, d ** -0.5, True, window)
+    for n, (q, x) in enumerate(zip(new, kv)):
+        first = x - q - window + 1
+        for j in range(first // page + 1):
+            pg = b["table"][n, j].item()
+            rows = slice(0, min(page, first - j * page))
+            b["k"][pg, rows] = b["v"][pg, rows] = float("nan")
+        b["table"][n, :first // page] = torch.tensor([-1, 1 << 30], dtype=torch.int32).repeat(
+            first // page)[:first // page]
+    b = {x: t.cuda() for x, t in b.items()}
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], window=window,
+                               max_q=nq, max_kv=max(kv), return_lse=True)
+    check_attention(o, lse, ref, dtype, d, max(kv))
+    assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 3000])
+def test_chunk_split_over_the_keys(window, d, dtype):
+    """Few tiles over a long context: parts of the keys, joined, at every head size."""
+    new, kv = [30, 41], [6000, 777]
+    b = make_batch(9, new, kv, 32, 1, d, dtype, 8, device="cuda", fill=float("nan"))
+    ref = attention_reference(b, d ** -0.5, True, window)
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], window=window,
+                               max_q=41, max_kv=6000, return_lse=True)
+    check_attention(o, lse, ref, dtype, d, 6000)
+    assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("few", [True, False], ids=["rows", "chunk"])
+def test_thousands_of_sequences(few):
+    """More sequences than threads that look for them, empty ones among them."""
+    rng = np.random.default_rng(10)
+    new = [int(x) for x in rng.integers(0, 3, 3001)]
+    kv = [int(n + x) if n else int(x) for n, x in zip(new, rng.integers(0, 40, 3001))]
+    b = make_batch(10, new, kv, 8, 1, 64, BF, 2, device="cuda", fill=float("nan"))
+    ref = attention_reference(b, 0.125)
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"],
+                               max_q=2 if few else 64, max_kv=42, return_lse=True)
+    check_attention(o, lse, ref, BF, 64, 42)
+    assert M.paged_device_error() == 0
