@@ -135,12 +135,13 @@ moe_status rope_append(const void* q, int64_t q_token_stride, void* q_out, int H
  * a query at position p >= 0, over the keys j < kv_len[n] with
  *   causal: j <= p;   window > 0: p - j < window
  *   o = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j)
- * A query that sees no key gets o = 0 and lse = -inf.  Scores, softmax
- * statistics and sums are fp32; the weights are rounded to the cache's type
- * (in fp16 at the upper end of its range) for the product with v.  Rows of
- * the cache at or past kv_len, or whose page number is bad, may hold anything,
- * NaN included; values of visible rows are expected to be finite (a non-finite
- * value may reach queries of its chunk that do not see it).
+ * A query that sees no key gets o = 0 and lse = -inf; the rows of o and lse of
+ * tokens outside every sequence are not written.  Scores, softmax statistics
+ * and sums are fp32; the weights are rounded to the cache's type (in fp16 at
+ * the upper end of its range) for the product with v.  Rows of the cache at or
+ * past kv_len, or whose page number is bad, may hold anything, NaN included;
+ * values of visible rows are expected to be finite (a non-finite value may
+ * reach queries of its chunk that do not see it).
  *   q, o   cache dtype [T][Hq][D], token and head strides in elements,
  *          multiples of 8, 16-byte aligned; must not overlap
  *   lse    fp32 [T][Hq] dense, or NULL
@@ -178,13 +179,13 @@ moe_status pages_fork(int32_t* refs, int P, int32_t* table, int64_t table_stride
 
 /* Room for add[s] >= 0 more tokens in every slot (negative counts as 0); lens
  * grows by it.  A slot that grows and whose last page is partly filled and
- * shared gets a page of its own in its place: moves[s] = {shared page, own
- * page}, whose rows the caller copies (pages_copy) before it writes; otherwise
- * moves[s] = {-1, -1}.  Pages go to slots in order of s, each slot's exchanged
- * page first.  All or nothing: status[0] = pages that were missing, status[1]
- * = slots whose row of the table is too short (or whose length would pass
- * 2^31 - 1); where either is not 0 nothing
- * but status and moves (all -1) is written.
+ * shared gets a page of its own in its place (each such slot, also where all
+ * that share the page grow): moves[s] = {shared page, own page}, whose rows the
+ * caller copies (pages_copy) before it writes; otherwise moves[s] = {-1, -1}.
+ * Pages go to slots in order of s, each slot's exchanged page first.  All or
+ * nothing: status[0] = pages that were missing, status[1] = slots whose row of
+ * the table is too short (or whose length would pass 2^31 - 1); where either is
+ * not 0 nothing but status and moves (all -1) is written.
  * scratch: int32 [S + 1]. */
 moe_status pages_reserve(int32_t* refs, int P, int32_t* table, int64_t table_stride, int width,
                          int32_t* lens, const int32_t* add, int S, int page, int32_t* moves,

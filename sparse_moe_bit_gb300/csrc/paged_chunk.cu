@@ -27,15 +27,17 @@
 // so that small weights stay in the type's range, off by half a step or 2^-32 of the
 // reference's; l and O likewise, with m' - 7 as their reference.)
 //
-// Measured, bf16, 16 query and 2 key/value heads, in one launch: D = 256, 4096 new
-// tokens over 32768 keys 1.14 ms, 1.81 PFLOP/s (0.95 of cuBLAS's burst), 2048 over
-// 16384 1.75 PFLOP/s, tensor pipe 88 % active; 2048 over 16384 with D = 128
-// 1.43 PFLOP/s and with D = 64 0.76, where the exponentials (one a score, whatever
-// D) and the softmax's instructions take longer than the products.  Tried for the
-// small heads and slower: P in TMEM columns of its own with a second warp that
-// issues P V (D = 128 1.32, D = 64 0.66: the two warps' MMAs interleave and each
-// product finishes late), and with a whole row a thread at 200 registers (1.37 and
-// 0.71).
+// Measured, bf16, 16 query and 2 key/value heads: D = 256, 4096 new tokens over 32768
+// keys 1.14 ms at 2070 MHz, 1.80 PFLOP/s (0.95 of cuBLAS's burst; 1.21 ms at the 1.82
+// GHz that the power limit leaves launches back to back), 2048 over 16384 1.79 PFLOP/s,
+// tensor pipe 88 % active; 2048 over 16384 with D = 128 1.44 PFLOP/s and with D = 64
+// 0.75, in the same time a tile.  There no unit is full (D = 128: tensor 67 %, issue
+// 56 %, ALU 40 %, XU 35 %; D = 64: tensor 34 %, the others alike): a tile's chain of
+// scores out of TMEM, maxima, exponentials, weights back and hand-over bounds it, which
+// the two groups overlap in part.  Tried for the small heads and slower: P in TMEM
+// columns of its own with a second warp that issues P V (D = 128 1.32, D = 64 0.66: the
+// two warps' MMAs interleave and each product finishes late), and with a whole row a
+// thread at 200 registers (1.37 and 0.71).
 //
 // Warps: 0 copies keys, 2 copies values, 1 issues the MMAs (the even CTA's),
 // 4..19 softmax, correction and epilogue.  Every wait is bounded.  The copies

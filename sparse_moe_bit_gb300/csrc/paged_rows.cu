@@ -25,7 +25,7 @@
 // to 8192: the last wave ran half empty.)
 // Measured, bf16, 16 query and 2 key/value heads of 256, 64 sequences: contexts of
 // 8192 178 us, 1.075 GB read, 6.0 TB/s (0.90 of the copy rate; tensor pipe 9 %,
-// issue 18 %); ragged contexts up to 8192 108 us with the join.  With cp.async in
+// issue 18 %); ragged contexts up to 8192 110 us with the join.  With cp.async in
 // place of TMA the ragged batch took 137 us, with the rows as the products' wide
 // side 123.  One sequence of 1027 keys takes 13.5 us, all of it latency.
 //

@@ -17,7 +17,7 @@
 // to 4: what counts is the loads that many threads have in flight.)
 // Measured: 16385 tokens x 32 heads x 128, bf16, all turned: 46 us, 5.8 TB/s of
 // reads and writes (0.87 of the copy rate, 40 registers); 8313 new tokens of 32
-// query and 8 key/value heads of 128 into the cache 38 us, 0.80 of it.
+// query and 8 key/value heads of 128 into the cache 39.5 us, 0.77 of it.
 // Vectors need r and the rest of the head (D - 2r) to be multiples of the 16 bytes' 8
 // (fp32: 4) values, in either layout, and aligned rows; everything else takes the same
 // loop one pair at a time.

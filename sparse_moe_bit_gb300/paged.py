@@ -4,7 +4,8 @@ attention over it (argument marshalling only; no fallback path).
 Tensors are CUDA tensors of the current device; that, shapes, types and strides
 are checked here, values that only the GPU can see are handled by the kernels
 (include/paged.h says how).  Every call enqueues on ``stream`` (default: torch's
-current one)."""
+current one).  Like the package's other calls they leave no autograd graph: a
+gradient is a call of its own (rope's is rope with ``inverse``)."""
 from __future__ import annotations
 
 import ctypes
