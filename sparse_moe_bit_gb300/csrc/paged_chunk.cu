@@ -70,6 +70,10 @@ constexpr float kRise = 8.f;  // log2 units the maximum may lag behind
 template <bool BF>
 constexpr float kShift = BF ? 0.f : kTopWeight<BF> - kRise;
 
+// log2 units of a reference whose fp32 step is small enough for x c - mc with mc rounded;
+// past it scores are taken relative to the reference first
+constexpr float kFar = 4096.f;
+
 template <int D>
 struct ChunkCfg {
   static constexpr int Q_BYTES = 128 * D * 2;
@@ -749,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a wait has given up, the warp runs on without waiting (others may
     // stand at a common barrier) and writes no result
     bool ok = true;
+    bool far = false;  // some row of the warp has a reference past kFar
     for (int j = group; j < nb; j += 2) {
       const int sb = j % C::NS;
       ok = ok && warp_wait(B.moved(sb), (j / C::NS) & 1, abort_flag, p.err);
@@ -822,8 +827,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         l *= f;
         extra *= f;
         m = now;
+        far = __any_sync(0xffffffffu, m != kNegInf && fabsf(m * c) > kFar);
       }
-      const float mc = m == kNegInf ? 0.f : fmaf(m, c, -kShift<BF>);
+      float mc = m == kNegInf ? 0.f : fmaf(m, c, -kShift<BF>);
+      if (far) {
+        const float s = m == kNegInf ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          x[i >> 5][i & 31] = __float_as_uint(__uint_as_float(x[i >> 5][i & 31]) - s);
+        mx -= s;
+        mc = -kShift<BF>;
+      }
       {
         const float top = ex2(fmaf(mx, c, -mc));
         extra += round16<BF>(top) - top;

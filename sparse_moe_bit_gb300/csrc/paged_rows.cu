@@ -8,8 +8,7 @@
 //   S = Q K^T, m' = max(m, rowmax S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
 //   O = O 2^(m - m') + P V                         (S in log2 units, all fp32)
 // (fp16: P = 2^(S - m' + 15), so that small weights stay in the type's range, off by
-// half a step or 2^-40 of the largest; l and O likewise, with m' - 15 as their
-// reference.)
+// half a step or 2^-40 of the largest; l and O likewise, until they are stored.)
 //
 // Bound: HBM (2 bytes x 2 D per key against 2 x 4 D x rows operations).  What
 // counts is bytes in flight and an even share for every SM, so the keys are cut
@@ -137,6 +136,14 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The weight of a score that is `d` above the maximum, in P's scale.  (The difference
+// comes first: it is exact where it matters, and a large maximum would swallow the scale.)
+template <bool BF>
+__device__ __forceinline__ float weight(float d) {
+  if constexpr (!BF) d += kTopWeight<BF>;
+  return exp2_approx(d);
 }
 
 // the 8x8 matrix of 16-bit values whose row i the lanes 4i .. 4i+3 hold, transposed
@@ -569,12 +576,11 @@ __global__ void __launch_bounds__(32 * kWarps)
     uint32_t pb[MB][NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const float u0m = m[nb][0] == kNegInf ? 0.f : m[nb][0] - kTopWeight<BF>;
-      const float u1m = m[nb][1] == kNegInf ? 0.f : m[nb][1] - kTopWeight<BF>;
+      const float u0m = m[nb][0] == kNegInf ? 0.f : m[nb][0], u1m = m[nb][1] == kNegInf ? 0.f : m[nb][1];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
-        const float e0 = exp2_approx(x[mb][nb][0] - u0m), e1 = exp2_approx(x[mb][nb][1] - u1m);
-        const float e2 = exp2_approx(x[mb][nb][2] - u0m), e3 = exp2_approx(x[mb][nb][3] - u1m);
+        const float e0 = weight<BF>(x[mb][nb][0] - u0m), e1 = weight<BF>(x[mb][nb][1] - u1m);
+        const float e2 = weight<BF>(x[mb][nb][2] - u0m), e3 = weight<BF>(x[mb][nb][3] - u1m);
         l[nb][0] += e0 + e2;
         l[nb][1] += e1 + e3;
         pb[mb][nb][0] = transpose8(pack2<BF>(e0, e1));
@@ -604,17 +610,17 @@ __global__ void __launch_bounds__(32 * kWarps)
           float sum = l[nb][i];
 #pragma unroll
           for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          const float ref = m[nb][i] - kTopWeight<BF>;
+          constexpr float kDown = BF ? 1.f : 0x1p-15f;  // 2^-kTopWeight
           const int r = 8 * nb + t2 + i;
           if (r0 + r >= rows) continue;
           if (!whole) {
             float* dst = p.part_o + (slot * kRowTile + r) * D + g;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-              dst[d * 16] = o[nb][d][i];
-              dst[d * 16 + 8] = o[nb][d][2 + i];
+              dst[d * 16] = o[nb][d][i] * kDown;
+              dst[d * 16 + 8] = o[nb][d][2 + i] * kDown;
             }
-            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(ref, sum);
+            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(m[nb][i], sum * kDown);
           } else {
             const int tok = fast_div(r0 + r, p.divG);
             const int head = use.h * p.G + (r0 + r - tok * p.G);
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(32 * kWarps)
             }
             if (g == 0 && p.lse)
               p.lse[(long long)(use.s.t0 + tok) * p.Hq + head] =
-                  sum == 0.f ? kNegInf : kLn2 * ref + logf(sum);
+                  sum == 0.f ? kNegInf : kLn2 * m[nb][i] + logf(sum * kDown);
           }
         }
       fresh = true;

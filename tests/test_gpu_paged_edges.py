@@ -248,3 +248,31 @@ def test_thousands_of_sequences(few):
                                max_q=2 if few else 64, max_kv=42, return_lse=True)
     check_attention(o, lse, ref, BF, 64, 42)
     assert M.paged_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq", [1, 100])
+@pytest.mark.parametrize("e", [10, 20, 23, 24, 25, 26, 27, 28, 31, 40])
+@pytest.mark.parametrize("times", [1.0, 1.37, 1.913])
+def test_scores_whose_steps_pass_the_weights_range(times, e, nq, dtype):
+    """Scores of some 2^e in log2 units, where fp32's steps (2^(e - 23)) are larger than what
+    a reference is off by: two keys take all of the weight, the later one 2^8 ahead or
+    level, and the result is their common value."""
+    kv, d = 300, 64
+    b = make_batch(11, [nq], [kv], 16, 1, d, dtype, 1, device="cpu")
+    b["q"].zero_(), b["k"].zero_(), b["v"].fill_(1.0)
+    b["q"][:, 0, 0], b["q"][:, 0, 1] = 1000.0, 1.0
+    for key, more in ((5, 0.0), (200, 7.9e6 * 2.0 ** -e)):
+        pg, r = b["table"][0, key // 16].item(), key % 16
+        b["k"][pg, r, 0, 0], b["k"][pg, r, 0, 1] = 1000.0, more
+        b["v"][pg, r] = 3.0
+    b = {x: t.cuda() for x, t in b.items()}
+    scale = times * 2.0 ** e / 1e6 * np.log(2.0)
+    o, lse = M.paged_attention(b["q"], b["k"], b["v"], b["table"], b["cu"], b["kv_len"], scale=scale,
+                               causal=False, max_q=nq, max_kv=kv, return_lse=True)
+    assert M.paged_device_error() == 0
+    # two roundings of the weights that meet one value, one of the result: half a step each
+    u = torch.finfo(dtype).eps / 2
+    assert (o.double() - 3).abs().max().item() <= 3 * 3 * u + 2.0 ** -18
+    low, high = times * 2.0 ** e * np.log(2.0), times * (2.0 ** e + 9) * np.log(2.0)
+    assert torch.all(lse >= low * (1 - 2.0 ** -20)) and torch.all(lse <= high * (1 + 2.0 ** -20) + 1)
