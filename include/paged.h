@@ -160,6 +160,38 @@ moe_status paged_attention(const void* q, int64_t q_token_stride, int64_t q_head
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * paged_attention for a batch in which groups of adjacent sequences share their
+ * first keys (the continuations of one prompt, pages_fork): a group's shared
+ * keys are read once for all of its new tokens.  Results are paged_attention's
+ * (without a window), up to the rounding of another order of sums.
+ *   cu_group  int32 [groups + 1]: group g holds the sequences cu_group[g] ..
+ *             cu_group[g+1]-1; read clamped into [0, N] and non-decreasing.
+ *             Sequences outside every group share nothing.
+ *   shared    int32 [groups]: the group's sequences hold the same keys and values at
+ *             their first shared[g] positions; those of the first sequence with new
+ *             tokens are read, through its row of the table (the pages themselves
+ *             need not be the same).  Read as no less than 0 and no more than every
+ *             sequence with new tokens has before them; a group with fewer than two
+ *             of those shares nothing.
+ *   max_q, max_group, max_shared, max_tail  what the caller knows of the longest
+ *             chunk, the most new tokens of a group, the most keys of a group and
+ *             the most keys of a sequence behind them (0: not known); as max_q and
+ *             max_kv of paged_attention they bound nothing
+ *   workspace paged_attention_shared_workspace() bytes
+ * groups = 0 is paged_attention.
+ */
+moe_status paged_attention_shared_workspace(const paged_cache* cache, const paged_batch* batch,
+                                            int Hq, int groups, int max_q, int max_group,
+                                            int max_shared, int max_tail, size_t* bytes);
+moe_status paged_attention_shared(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  int Hq, const paged_cache* cache, const paged_batch* batch,
+                                  const int32_t* cu_group, const int32_t* shared, int groups,
+                                  float scale, int causal, int max_q, int max_group,
+                                  int max_shared, int max_tail, void* o, int64_t o_token_stride,
+                                  int64_t o_head_stride, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * Page maintenance.  State, all int32 on the device and updated in place:
  *   refs  [P]         sequences that hold page p; 0 = free
  *   table [S][width]  pages of sequence slot s in order, rows table_stride

@@ -18,7 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["moe_api.cu", "grouped_mma.cu", "routing.cu", "repack.cu", "decode.cu",
            "gdn_scan.cu", "rope.cu", "pages.cu", "paged_rows.cu", "paged_chunk.cu",
-           "paged_api.cu", "norm.cu", "linear4.cu", "sample.cu", "step_api.cu"]
+           "paged_shared.cu", "paged_api.cu", "norm.cu", "linear4.cu", "sample.cu", "step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

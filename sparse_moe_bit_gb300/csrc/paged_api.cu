@@ -154,7 +154,7 @@ moe_status check_rope(int D, const double* freq, int r, float mscale) {
   return MOE_OK;
 }
 
-// Choice of kernel and split for one call.
+// Choice of kernel and split for one attention over a batch.
 struct Plan {
   bool wide;  // 256-row tiles on the tensor cores, else 8- or 16-row tiles
   int tiles, chunks, chunk;  // 256-row tiles
@@ -227,6 +227,49 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
   return r;
 }
 
+void set_plan(AttnParams* p, const Plan& r, void* workspace) {
+  p->tiles = r.tiles;
+  p->chunks = r.chunks;
+  p->chunk = r.chunk;
+  p->split = r.wide && r.chunks > 1;
+  p->warps = r.warps;
+  p->row_tile = r.row_tile;
+  p->parts = r.parts;
+  p->part_o = static_cast<float*>(workspace);
+  p->part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + r.ml);
+  p->before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + r.before);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// An attention over shared keys: two plans, of the groups as a batch and of the
+// sequences' own keys, whose results are partial, whatever their split; behind them the
+// results that a warp of the small tiles has whole, and the groups.
+struct SharedPlan {
+  Plan g, p;
+  size_t at_p, whole_g, whole_p, groups, ws;
+};
+SharedPlan plan_shared(const CacheView& c, const BatchView& b, int Hq, int G, int max_q, int max_group,
+                       int max_shared, int max_tail) {
+  SharedPlan r{};
+  BatchView gb = b;
+  gb.N = G;
+  r.g = plan(c, gb, Hq, 0, max_group, max_shared);
+  r.p = plan(c, b, Hq, 0, max_q, max_tail);
+  const size_t rows = (size_t)b.T * Hq, row = (size_t)c.dim * 4 + 8;
+  for (Plan* x : {&r.g, &r.p}) {
+    if (!x->wide || x->chunks > 1) continue;
+    x->ml = rows * c.dim * 4;
+    x->before = x->ws = up256(x->ml + rows * 8);
+  }
+  r.at_p = up256(r.g.ws);
+  r.whole_g = r.at_p + up256(r.p.ws);
+  r.whole_p = r.whole_g + (r.g.wide ? 0 : up256(rows * row));
+  r.groups = r.whole_p + (r.p.wide ? 0 : up256(rows * row));
+  r.ws = r.groups + ((size_t)3 * G + 1 + b.N) * 4;
+  return r;
+}
+
 moe_status check_attention(const paged_cache* cache, const paged_batch* batch, int Hq, int window,
                            int max_q, int max_kv, CacheView* c, BatchView* b) {
   moe_status s = check_cache(cache, c);
@@ -239,6 +282,35 @@ moe_status check_attention(const paged_cache* cache, const paged_batch* batch, i
     return fail(MOE_ERR_INVALID_ARG, "negative window, max_q or max_kv");
   if ((long long)batch->T * Hq >= (1ll << 31) - 256)
     return fail(MOE_ERR_UNSUPPORTED, "T * Hq = %lld", (long long)batch->T * Hq);
+  return MOE_OK;
+}
+
+// An attention call's arguments; p gets all of them but the mask and the split.
+moe_status check_queries(const void* q, int64_t q_ts, int64_t q_hs, int Hq, const paged_cache* cache,
+                         const paged_batch* batch, float scale, int window, int max_q, int max_kv,
+                         void* o, int64_t o_ts, int64_t o_hs, float* lse, void* workspace,
+                         AttnParams* p) {
+  moe_status s = check_attention(cache, batch, Hq, window, max_q, max_kv, &p->c, &p->b);
+  if (s != MOE_OK) return s;
+  if (!(scale > 0) || !std::isfinite(scale))
+    return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (batch->T == 0 || batch->N == 0) return MOE_OK;
+  if (!q || !o) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (q_ts % 8 || q_hs % 8 || o_ts % 8 || o_hs % 8 || q_ts < 0 || q_hs < 0 || o_ts < 0 || o_hs < 0)
+    return fail(MOE_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  p->q = static_cast<const uint16_t*>(q);
+  p->o = static_cast<uint16_t*>(o);
+  p->lse = lse;
+  p->q_ts = q_ts;
+  p->q_hs = q_hs;
+  p->o_ts = o_ts;
+  p->o_hs = o_hs;
+  p->Hq = Hq;
+  p->G = Hq / cache->heads;
+  p->divG = make_fastdiv(p->G);
+  p->scale_log2 = scale * 1.44269504088896340736f;
   return MOE_OK;
 }
 
@@ -396,50 +468,106 @@ moe_status paged_attention(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
                            int64_t o_hs, float* lse, void* workspace, size_t workspace_bytes,
                            void* stream) {
   AttnParams p{};
-  moe_status s = check_attention(cache, batch, Hq, window, max_q, max_kv, &p.c, &p.b);
-  if (s != MOE_OK) return s;
-  if (!(scale > 0) || !std::isfinite(scale))
-    return fail(MOE_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (batch->T == 0 || batch->N == 0) return MOE_OK;
-  if (!q || !o) return fail(MOE_ERR_INVALID_ARG, "NULL tensor");
-  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
-    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
-  if (q_ts % 8 || q_hs % 8 || o_ts % 8 || o_hs % 8 || q_ts < 0 || q_hs < 0 || o_ts < 0 || o_hs < 0)
-    return fail(MOE_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  moe_status s = check_queries(q, q_ts, q_hs, Hq, cache, batch, scale, window, max_q, max_kv, o, o_ts,
+                               o_hs, lse, workspace, &p);
+  if (s != MOE_OK || batch->T == 0 || batch->N == 0) return s;
   const Plan r = plan(p.c, p.b, Hq, window, max_q, max_kv);
   if (r.ws > 0 && (!workspace || workspace_bytes < r.ws))
     return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, r.ws);
   if (2ll * r.tiles * p.c.heads * r.chunks >= (1ll << 31))
     return fail(MOE_ERR_UNSUPPORTED, "too many row tiles");
-  p.q = static_cast<const uint16_t*>(q);
-  p.o = static_cast<uint16_t*>(o);
-  p.lse = lse;
-  p.q_ts = q_ts;
-  p.q_hs = q_hs;
-  p.o_ts = o_ts;
-  p.o_hs = o_hs;
-  p.Hq = Hq;
-  p.G = Hq / cache->heads;
-  p.divG = make_fastdiv(p.G);
-  p.scale_log2 = scale * 1.44269504088896340736f;
-  p.causal = causal != 0;
-  p.window = window;
-  p.tiles = r.tiles;
-  p.chunks = r.chunks;
-  p.chunk = r.chunk;
-  p.warps = r.warps;
-  p.row_tile = r.row_tile;
-  p.parts = r.parts;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + r.ml);
-  p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(workspace) + r.before);
   p.err = paged_error_word();
   if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
+  p.causal = causal != 0;
+  p.window = window;
+  set_plan(&p, r, workspace);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == PAGED_BF16;
   PAGED_CK(r.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
            "paged_attention launch");
   if (!r.wide || r.chunks > 1) PAGED_CK(launch_paged_join(p, bf, st), "paged_attention join launch");
+  return MOE_OK;
+}
+
+moe_status paged_attention_shared_workspace(const paged_cache* cache, const paged_batch* batch,
+                                            int Hq, int groups, int max_q, int max_group,
+                                            int max_shared, int max_tail, size_t* bytes) {
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  CacheView c;
+  BatchView b{};
+  moe_status s = check_attention(cache, batch, Hq, 0, max_q, max_tail, &c, &b);
+  if (s != MOE_OK) return s;
+  if (groups < 0 || max_group < 0 || max_shared < 0)
+    return fail(MOE_ERR_INVALID_ARG, "negative groups, max_group or max_shared");
+  *bytes = groups == 0 ? plan(c, b, Hq, 0, max_q, max_tail).ws
+                       : plan_shared(c, b, Hq, groups, max_q, max_group, max_shared, max_tail).ws;
+  return MOE_OK;
+}
+
+moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int Hq,
+                                  const paged_cache* cache, const paged_batch* batch,
+                                  const int32_t* cu_group, const int32_t* shared, int groups,
+                                  float scale, int causal, int max_q, int max_group, int max_shared,
+                                  int max_tail, void* o, int64_t o_ts, int64_t o_hs, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (groups < 0 || max_group < 0 || max_shared < 0)
+    return fail(MOE_ERR_INVALID_ARG, "negative groups, max_group or max_shared");
+  if (groups == 0)
+    return paged_attention(q, q_ts, q_hs, Hq, cache, batch, scale, causal, 0, max_q, max_tail, o, o_ts,
+                           o_hs, lse, workspace, workspace_bytes, stream);
+  AttnParams p{};
+  moe_status s = check_queries(q, q_ts, q_hs, Hq, cache, batch, scale, 0, max_q, max_tail, o, o_ts, o_hs,
+                               lse, workspace, &p);
+  if (s != MOE_OK || batch->T == 0 || batch->N == 0) return s;
+  if (!cu_group || !shared || !aligned(cu_group, 4) || !aligned(shared, 4))
+    return fail(MOE_ERR_INVALID_ARG, "cu_group or shared NULL or misaligned");
+  const SharedPlan r = plan_shared(p.c, p.b, Hq, groups, max_q, max_group, max_shared, max_tail);
+  if (!workspace || workspace_bytes < r.ws)
+    return fail(MOE_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, r.ws);
+  for (const Plan* x : {&r.g, &r.p})
+    if (2ll * x->tiles * p.c.heads * x->chunks >= (1ll << 31))
+      return fail(MOE_ERR_UNSUPPORTED, "too many row tiles");
+  p.err = paged_error_word();
+  if (!p.err) return fail(MOE_ERR_CUDA, "no CUDA device");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t rows = (size_t)p.b.T * Hq, whole_ml = rows * p.c.dim * 4;
+  GroupView gv{};
+  gv.cu_group = cu_group;
+  gv.shared = shared;
+  gv.G = groups;
+  gv.cu = reinterpret_cast<int32_t*>(ws + r.groups);
+  gv.len = gv.cu + groups + 1;
+  gv.rows = gv.len + groups;
+  gv.skip = gv.rows + groups;
+  AttnParams g = p;
+  set_plan(&g, r.g, ws);
+  g.split = r.g.wide;
+  g.causal = 0;
+  g.flat = 1;
+  g.b.N = groups;
+  g.b.cu = gv.cu;
+  g.b.kv_len = gv.len;
+  g.b.rows = gv.rows;
+  if (!r.g.wide) {
+    g.whole_o = reinterpret_cast<float*>(ws + r.whole_g);
+    g.whole_ml = reinterpret_cast<float2*>(ws + r.whole_g + whole_ml);
+  }
+  set_plan(&p, r.p, ws + r.at_p);
+  p.causal = causal != 0;
+  p.split = r.p.wide;
+  if (!r.p.wide) {
+    p.whole_o = reinterpret_cast<float*>(ws + r.whole_p);
+    p.whole_ml = reinterpret_cast<float2*>(ws + r.whole_p + whole_ml);
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == PAGED_BF16;
+  PAGED_CK(launch_paged_groups(p.b, gv, st), "paged_attention_shared groups launch");
+  p.b.skip = gv.skip;
+  PAGED_CK(r.g.wide ? launch_paged_chunk(g, bf, st) : launch_paged_rows(g, bf, st),
+           "paged_attention_shared launch");
+  PAGED_CK(r.p.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
+           "paged_attention_shared launch");
+  PAGED_CK(launch_paged_join_shared(p, g, bf, st), "paged_attention_shared join launch");
   return MOE_OK;
 }
 

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hi = ck == p.chunks - 1 ? kr.y : kr.x + (int)min(c0 + p.chunk, (long long)span);
   const int first = TMA ? lo & ~63 : lo;
   const int nb = hi > lo ? (hi - first + kTileKeys - 1) / kTileKeys : 0;
-  const int32_t* table = p.b.table + n * p.b.table_stride;
+  const int32_t* table = table_row(p.b, n);
 
   // this thread's row in the softmax warps (the other warps: unused)
   const int quarter = warp & 3, half = ((warp - kSoftWarp0) >> 2) & 1;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (nb == 0) {  // nothing to see in this chunk (uniform over the pair)
     if (warp >= kSoftWarp0 && valid) {
       const int part = half + 2 * group;  // a quarter of the features
-      if (p.chunks > 1) {
+      if (p.split) {
         if (part == 0) p.part_ml[rid * p.chunks + ck] = make_float2(kNegInf, 0.f);
       } else {
         uint16_t* o = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + part * (D / 4);
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int vlo = 0, vhi = 0x7fffffff;
     if (valid) {
       const int pos = s.kv - s.nq + tok;
-      vhi = p.causal || pos < 0 ? min(s.kv, pos + 1) : s.kv;
+      vhi = !p.flat && (p.causal || pos < 0) ? min(s.kv, pos + 1) : s.kv;
       vlo = p.window > 0 ? window_begin(pos, p.window) : 0;
     } else {
       vhi = s.kv;
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       tc_fence_after();
       // (a part of a row: for a join that divides by the sum of the l)
-      const float inv = l == 0.f ? 0.f : (p.chunks > 1 ? l : 1.f) / (l + extra);
+      const float inv = l == 0.f ? 0.f : (p.split ? l : 1.f) / (l + extra);
       const float mlog = fmaf(m, c, -kShift<BF>);  // (-inf: no key seen)
 #pragma unroll 1
       for (int f0 = 0; f0 < D / 4; f0 += 16) {
@@ -907,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(tmem + lanes + f, o);
         tmem_ld_wait();
         if (!valid) continue;
-        if (p.chunks > 1) {
+        if (p.split) {
           float4* d4 = reinterpret_cast<float4*>(p.part_o + (rid * p.chunks + ck) * D + f);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid && part == 0) {
-        if (p.chunks > 1) p.part_ml[rid * p.chunks + ck] = make_float2(mlog, l);
+        if (p.split) p.part_ml[rid * p.chunks + ck] = make_float2(mlog, l);
         else if (p.lse) p.lse[rid] = l == 0.f ? kNegInf : kLn2 * mlog + logf(l);
       }
     }

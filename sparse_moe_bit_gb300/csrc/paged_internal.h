@@ -47,11 +47,18 @@ struct BatchView {
   int N, T, width;
   long long table_stride;
   int capacity;  // min(width * page, 2^31 - 1): the longest context a table row holds
+  // attention over shared keys: the sequences' rows of the table where they are not
+  // their own numbers, and the first key that each looks at (NULL: 0)
+  const int32_t *rows, *skip;
 };
+__device__ __forceinline__ const int32_t* table_row(const BatchView& b, int n) {
+  return b.table + (b.rows ? b.rows[n] : n) * b.table_stride;
+}
 
 // One sequence of a batch with its metadata made safe.
 struct Seq {
   int t0, nq, kv;  // first new token, new tokens, context
+  int lo;          // first key that is looked at
 };
 __device__ __forceinline__ Seq load_seq(const BatchView& b, int n) {
   Seq s;
@@ -60,6 +67,7 @@ __device__ __forceinline__ Seq load_seq(const BatchView& b, int n) {
   s.t0 = t0;
   s.nq = t1 - t0;
   s.kv = min(max(b.kv_len[n], 0), b.capacity);
+  s.lo = b.skip ? b.skip[n] : 0;
   return s;
 }
 // The sequence of new token t: the last n with cu[n] <= t (-1: none).
@@ -109,10 +117,11 @@ struct AttnParams {
   BatchView b;
   float scale_log2;  // scale * log2(e)
   int causal, window;
+  int flat;  // every row sees every key (a group's rows and the keys that it shares)
   // 256-row tiles: `tiles` of the batch; chunk c of a tile covers the keys
   // [c, c+1) * chunk behind its first visible one, the last goes to the end.
-  // Partial results [T * Hq][chunks] where chunks > 1.
-  int tiles, chunks, chunk;
+  // Partial results [T * Hq][chunks] where `split`.
+  int tiles, chunks, chunk, split;
   // tiles of `row_tile` = 8 or 16 rows: `warps` (a multiple of kRowWarps) share the
   // work; partial results [2 * warps][16], groups of keys before each sequence
   // [N + 1].
@@ -121,6 +130,10 @@ struct AttnParams {
   long long* before;
   float* part_o;    // [..][D], unnormalised
   float2* part_ml;  // [..]: running maximum (log2 units) and sum
+  // small tiles whose results are joined with another kernel's: items that one warp
+  // covers leave theirs here, [T * Hq] (NULL: the warp writes o and lse)
+  float* whole_o;
+  float2* whole_ml;
   int* err;
 };
 // The first key in a query's window.  (A query before position 0 sees none; its
@@ -131,9 +144,9 @@ __device__ __forceinline__ int window_begin(int pos, int window) { return max(po
 __device__ __forceinline__ int2 key_range(const AttnParams& p, const Seq& s, int r0, int r1) {
   const int p0 = s.kv - s.nq + fast_div(r0, p.divG);
   const int p1 = s.kv - s.nq + fast_div(r1 - 1, p.divG);
-  int lo = 0, hi = s.kv;
+  int lo = s.lo, hi = s.kv;
   if (p.causal) hi = min(hi, p1 + 1);
-  if (p.window > 0) lo = max(0, window_begin(p0, p.window));
+  if (p.window > 0) lo = max(lo, window_begin(p0, p.window));
   return make_int2(lo, max(hi, lo));
 }
 // A tensor map over one of the cache's arrays (innermost first: feature, row of a
@@ -153,6 +166,19 @@ cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st);
 constexpr int kPairRows = 256;
 cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st);
+// The join of two attentions' partial results: over the keys that groups of sequences
+// share (`g`, its batch the groups) and over the sequences' own (`p`).
+cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, bool bf16,
+                                     cudaStream_t st);
+// The groups of a batch made safe (paged_shared.cu): cu [G + 1], len [G] and rows [G]
+// are the groups as a batch of sequences (their tokens, shared keys, a member's row of
+// the table), skip [N] the members' first own key.
+struct GroupView {
+  const int32_t *cu_group, *shared;
+  int G;
+  int32_t *cu, *len, *rows, *skip;
+};
+cudaError_t launch_paged_groups(const BatchView& b, const GroupView& g, cudaStream_t st);
 
 // ---- pages (pages.cu)
 cudaError_t launch_pages_fork(int32_t* refs, int P, int32_t* table, long long ts, int width,

@@ -164,7 +164,7 @@ struct Extent {
 };
 __device__ __forceinline__ Extent extent_of(const AttnParams& p, const Seq& s, int kg, int tile) {
   Extent e;
-  e.first = p.window > 0 ? max(0, window_begin(s.kv - s.nq, p.window)) : 0;
+  e.first = p.window > 0 ? max(s.lo, window_begin(s.kv - s.nq, p.window)) : s.lo;
   e.lo = e.first & ~(kg - 1);  // groups do not straddle pages that hold whole ones
   e.groups = max((s.kv - e.lo + kg - 1) / kg, 1);
   e.items = (s.nq * p.G + tile - 1) / tile * p.c.heads;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (c.e.items > 0) break;
     }
     // (behind the last group there may be none: nothing reads it)
-    c.table = p.b.table + min(c.n, p.b.N - 1) * p.b.table_stride;
+    c.table = table_row(p.b, min(c.n, p.b.N - 1));
   };
   auto advance = [&](Cursor& c) {
     if (++c.g < c.e.groups) return;
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(32 * kWarps)
       const int pos0 = use.s.kv - use.s.nq;
       auto vis = [&](int r, int& a, int& b) {
         const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
-        b = p.causal || pos < 0 ? min(use.s.kv, pos + 1) : use.s.kv;
-        a = p.window > 0 ? window_begin(pos, p.window) : 0;
+        b = !p.flat && (p.causal || pos < 0) ? min(use.s.kv, pos + 1) : use.s.kv;
+        a = p.window > 0 ? max(use.s.lo, window_begin(pos, p.window)) : use.s.lo;
       };
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -613,17 +613,18 @@ __global__ void __launch_bounds__(32 * kWarps)
           constexpr float kDown = BF ? 1.f : 0x1p-15f;  // 2^-kTopWeight
           const int r = 8 * nb + t2 + i;
           if (r0 + r >= rows) continue;
-          if (!whole) {
-            float* dst = p.part_o + (slot * kRowTile + r) * D + g;
+          const int tok = fast_div(r0 + r, p.divG);
+          const int head = use.h * p.G + (r0 + r - tok * p.G);
+          if (!whole || p.whole_o) {
+            const long long at = whole ? (long long)(use.s.t0 + tok) * p.Hq + head : slot * kRowTile + r;
+            float* dst = (whole ? p.whole_o : p.part_o) + at * D + g;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
               dst[d * 16] = o[nb][d][i] * kDown;
               dst[d * 16 + 8] = o[nb][d][2 + i] * kDown;
             }
-            if (g == 0) p.part_ml[slot * kRowTile + r] = make_float2(m[nb][i], sum * kDown);
+            if (g == 0) (whole ? p.whole_ml : p.part_ml)[at] = make_float2(m[nb][i], sum * kDown);
           } else {
-            const int tok = fast_div(r0 + r, p.divG);
-            const int head = use.h * p.G + (r0 + r - tok * p.G);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             uint16_t* dst = p.o + (use.s.t0 + tok) * p.o_ts + head * p.o_hs + g;
 #pragma unroll
@@ -663,10 +664,53 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 }
 
+// A row's partial results: part c lies in slot (c ? rest + c * step : at).
+struct Parts {
+  const float* o;
+  const float2* ml;
+  long long at, rest, step;
+  int n;
+  __device__ __forceinline__ long long slot(int c) const { return c == 0 ? at : rest + c * step; }
+};
+// ... of query head `head` of new token t, which is sequence n's (none: it has been
+// written to o, or there is no such row)
+template <int D>
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, int n, const Seq& s, int t, int head) {
+  const long long rid = (long long)t * p.Hq + head;
+  Parts r{p.part_o, p.part_ml, 0, 0, 0, 0};
+  if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return r;
+  if (p.split) {
+    r.at = r.rest = rid * p.chunks;
+    r.step = 1;
+    r.n = p.chunks;
+    return r;
+  }
+  const int row = (t - s.t0) * p.G + head % p.G, tile = row / p.row_tile;
+  const Extent e = extent_of(p, s, RowsCfg<D>::KG, p.row_tile);
+  const long long U = p.before[p.b.N];
+  const long long u = p.before[n] + (long long)(tile * p.c.heads + head / p.G) * e.groups;
+  const int warps = (int)min((long long)p.warps, U);
+  const int w0 = owner_of(U, warps, u), w1 = owner_of(U, warps, u + e.groups - 1);
+  if (w0 == w1) {  // one warp's: written, or left whole
+    r.o = p.whole_o;
+    r.ml = p.whole_ml;
+    r.at = rid;
+    r.n = p.whole_o ? 1 : 0;
+    return r;
+  }
+  r.at = (2ll * w0 + 1) * kRowTile + row % p.row_tile;
+  r.rest = 2ll * w0 * kRowTile + row % p.row_tile;
+  r.step = 2 * kRowTile;
+  r.n = w1 - w0 + 1;
+  return r;
+}
+
 // Join of a row's parts, in their order: warp w of the row's CTA takes parts
-// w, w + W, ...; the warps' sums meet in shared memory.
-template <int D, bool BF, int W>
-__global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) {
+// w, w + W, ...; the warps' sums meet in shared memory.  SHARED: the parts over the
+// group's keys (g), then those over the sequence's own.
+template <int D, bool BF, int W, bool SHARED>
+__global__ void __launch_bounds__(32 * W)
+    paged_join_kernel(const AttnParams p, const __grid_constant__ AttnParams g) {
   constexpr int E = D / 32;  // features of a lane
   __shared__ float sh_o[W][D];
   __shared__ float sh_l[W];
@@ -680,31 +724,19 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   // grid must not be over before the first one, whose workspace may be another's
   // from then on.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // new tokens outside every sequence have no partial results
-  if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
-  // part c of this row: slot (c ? rest + c * step : at), in rows
-  long long at, rest, step;
-  int parts;
-  if (p.chunks > 1) {
-    at = rest = rid * p.chunks;
-    step = 1;
-    parts = p.chunks;
-  } else {
-    const int r = (t - s.t0) * p.G + head % p.G, tile = r / p.row_tile;
-    const Extent e = extent_of(p, s, RowsCfg<D>::KG, p.row_tile);
-    const long long U = p.before[p.b.N];
-    const long long u = p.before[n] + (long long)(tile * p.c.heads + head / p.G) * e.groups;
-    const int warps = (int)min((long long)p.warps, U);
-    const int w0 = owner_of(U, warps, u), w1 = owner_of(U, warps, u + e.groups - 1);
-    if (w0 == w1) return;  // written by its warp
-    at = (2ll * w0 + 1) * kRowTile + r % p.row_tile;
-    rest = 2ll * w0 * kRowTile + r % p.row_tile;
-    step = 2 * kRowTile;
-    parts = w1 - w0 + 1;
+  const Parts own = parts_of<D>(p, n, s, t, head);
+  Parts grp{nullptr, nullptr, 0, 0, 0, 0};
+  if constexpr (SHARED) {
+    if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
+    const int k = find_seq(g.b, t);
+    grp = parts_of<D>(g, k, load_seq(g.b, max(k, 0)), t, head);
   }
-  auto slot = [&](int c) { return c == 0 ? at : rest + c * step; };
+  const int parts = grp.n + own.n;
+  // new tokens outside every sequence have no partial results, nor those that a warp wrote
+  if (!SHARED && parts == 0) return;
+  auto ml = [&](int c) { return c < grp.n ? grp.ml[grp.slot(c)] : own.ml[own.slot(c - grp.n)]; };
   float m = kNegInf;
-  for (int c = lane; c < parts; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+  for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml(c).x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float u = m == kNegInf ? 0.f : m;
@@ -713,8 +745,8 @@ __global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) 
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 8
   for (int c = warp; c < parts; c += W) {
-    const float2 x = p.part_ml[slot(c)];
-    const float* po = p.part_o + slot(c) * D;
+    const float2 x = ml(c);
+    const float* po = c < grp.n ? grp.o + grp.slot(c) * D : own.o + own.slot(c - grp.n) * D;
     const float a = exp2_approx(x.x - u);
     l += a * x.y;
     if (x.y != 0.f) {  // (a part without keys need not hold numbers; NaN sums pass)
@@ -764,8 +796,8 @@ cudaError_t rows_launch(const AttnParams& p, cudaStream_t st) {
   return tma ? rows_launch_t<D, 2, BF, true>(rp, st) : rows_launch_t<D, 2, BF, false>(rp, st);
 }
 
-template <int D, bool BF, int W>
-cudaError_t join_w(const AttnParams& p, cudaStream_t st) {
+template <int D, bool BF, int W, bool SHARED>
+cudaError_t join_w(const AttnParams& p, const AttnParams& g, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)((long long)p.b.T * p.Hq));
   c.blockDim = dim3(32 * W);
@@ -776,15 +808,20 @@ cudaError_t join_w(const AttnParams& p, cudaStream_t st) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_join_kernel<D, BF, W>, p);
+  return cudaLaunchKernelEx(&c, paged_join_kernel<D, BF, W, SHARED>, p, g);
 }
 
 template <int D, bool BF>
 cudaError_t join_launch(const AttnParams& p, cudaStream_t st) {
   // a warp for four parts or so: a row's parts, a kilobyte each at D = 256, are
   // read in as many rounds of latency as a warp has parts
-  if (p.parts <= 16) return join_w<D, BF, 4>(p, st);
-  return join_w<D, BF, 32>(p, st);
+  if (p.parts <= 16) return join_w<D, BF, 4, false>(p, p, st);
+  return join_w<D, BF, 32, false>(p, p, st);
+}
+template <int D, bool BF>
+cudaError_t join_shared_launch(const AttnParams& p, const AttnParams& g, cudaStream_t st) {
+  if (p.parts + g.parts <= 32) return join_w<D, BF, 4, true>(p, g, st);
+  return join_w<D, BF, 32, true>(p, g, st);
 }
 
 }  // namespace
@@ -802,6 +839,10 @@ cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st) {
 }
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st) {
   PAGED_BY_DIM(join_launch, p, st);
+}
+cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, bool bf16,
+                                     cudaStream_t st) {
+  PAGED_BY_DIM(join_shared_launch, p, g, st);
 }
 
 }  // namespace moe

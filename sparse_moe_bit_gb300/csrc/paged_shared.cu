@@ -1,0 +1,56 @@
+// The groups of a batch whose sequences share their first keys, as a batch of their own
+// (include/paged.h, paged_attention_shared).
+#include "paged_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 128;
+
+// A CTA a group.  What a group can share: no more than its members all have before their
+// new tokens, so that every one of these keys is visible to all of its rows, and nothing
+// where fewer than two of them have new tokens.
+__global__ void __launch_bounds__(kThreads) groups_kernel(const BatchView b, const GroupView g) {
+  __shared__ int sh_first, sh_least, sh_with, sh_at;
+  const int me = blockIdx.x;
+  if (threadIdx.x == 0) {
+    sh_first = b.N;
+    sh_least = 0x7fffffff;
+    sh_with = 0;
+    sh_at = 0;
+  }
+  __syncthreads();
+  // cu_group made non-decreasing within [0, N]
+  for (int i = threadIdx.x; i <= me; i += kThreads) atomicMax(&sh_at, min(g.cu_group[i], b.N));
+  __syncthreads();
+  const int n0 = sh_at, n1 = min(max(g.cu_group[me + 1], n0), b.N);
+  for (int n = n0 + threadIdx.x; n < n1; n += kThreads) {
+    const Seq s = load_seq(b, n);
+    if (s.nq == 0) continue;
+    atomicMin(&sh_first, n);
+    atomicMin(&sh_least, s.kv - s.nq);
+    atomicAdd(&sh_with, 1);
+  }
+  __syncthreads();
+  const int len = sh_with < 2 ? 0 : max(min(g.shared[me], sh_least), 0);
+  for (int n = n0 + threadIdx.x; n < n1; n += kThreads) g.skip[n] = len;
+  // (sequences of no group)
+  if (me == 0)
+    for (int n = threadIdx.x; n < n0; n += kThreads) g.skip[n] = 0;
+  if (me == g.G - 1)
+    for (int n = n1 + threadIdx.x; n < b.N; n += kThreads) g.skip[n] = 0;
+  if (threadIdx.x == 0) {
+    g.len[me] = len;
+    g.rows[me] = min(sh_first, b.N - 1);
+    g.cu[me] = b.cu[n0];
+    if (me == g.G - 1) g.cu[g.G] = b.cu[n1];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_groups(const BatchView& b, const GroupView& g, cudaStream_t st) {
+  return launch_kernel(groups_kernel, dim3(g.G), dim3(kThreads), 0, st, b, g);
+}
+
+}  // namespace moe

@@ -21,7 +21,7 @@ PAGED_DEVERR_LENGTH = 4
 
 # names of the functions include/paged.h declares (checked by its ABI test)
 EXPORTS = ["rope", "rope_frequencies", "rope_append", "paged_attention_workspace",
-           "paged_attention", "pages_fork", "pages_reserve", "pages_free", "pages_compact",
+           "paged_attention", "paged_attention_shared_workspace", "paged_attention_shared", "pages_fork", "pages_reserve", "pages_free", "pages_compact",
            "pages_copy", "paged_get_device_error"]
 
 _DTYPE = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}
@@ -59,6 +59,9 @@ def _library():
         "rope_append": [P, L, P, I, P, L, P, L, C, B, P, I, F, I, P],
         "paged_attention_workspace": [C, B, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
         "paged_attention": [P, L, L, I, C, B, F, I, I, I, I, P, L, L, P, P, ctypes.c_size_t, P],
+        "paged_attention_shared_workspace": [C, B, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)],
+        "paged_attention_shared": [P, L, L, I, C, B, P, P, I, F, I, I, I, I, I, P, L, L, P, P,
+                                   ctypes.c_size_t, P],
         "pages_fork": [P, I, P, L, I, P, I, P, P, I, P, P],
         "pages_reserve": [P, I, P, L, I, P, P, I, I, P, P, P, P],
         "pages_free": [P, I, P, L, I, P, I, P, I, P],
@@ -313,6 +316,75 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                                None if lse is None else lse.data_ptr(), ws, size,
                                _stream(stream, q)))
     if stream is not None:  # (a workspace made here is let go of on the stream that uses it)
+        _used(stream, (lse,) if given[0] is out else (out, lse), given)
+    return (out, lse) if return_lse else out
+
+
+def paged_attention_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                           table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor,
+                           cu_group: torch.Tensor, shared: torch.Tensor,
+                           scale: float | None = None, causal: bool = True, max_q: int = 0,
+                           max_group: int = 0, max_shared: int = 0, max_tail: int = 0,
+                           return_lse: bool = False, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """paged_attention for groups of adjacent sequences that share their first keys, which
+    are read once a group: group g holds the sequences cu_group[g] .. cu_group[g + 1] - 1
+    (int32 [groups + 1]), whose first shared[g] keys (int32 [groups]) are the same; they are
+    read through the first one's row of the table.  ``max_q``, ``max_group``, ``max_shared``
+    and ``max_tail`` (the longest chunk, the most new tokens of a group, the most keys of a
+    group, the most keys of a sequence behind them, if the caller knows them) choose kernels
+    and splits and bound nothing.  The rest is as for paged_attention;
+    paged_attention_shared_workspace() in include/paged.h sizes ``workspace``."""
+    lib = _library()
+    if max(max_q, max_group, max_shared, max_tail) > 0x7fffffff:
+        max_q, max_group, max_shared, max_tail = (min(x, 0x7fffffff) for x in
+                                                  (max_q, max_group, max_shared, max_tail))
+    T, Hq, D = q.shape
+    _placed(q, k_pages, v_pages, table, cu_q, kv_len, cu_group, shared, out, workspace)
+    c = _cache(k_pages, v_pages)
+    if q.dtype is not k_pages.dtype or D != k_pages.shape[3]:
+        raise ValueError("q must match the cache's type and dim")
+    _i32(cu_group, 1, "cu_group")
+    _i32(shared, 1, "shared")
+    G = shared.shape[0]
+    if cu_group.shape[0] != G + 1:
+        raise ValueError("cu_group is [groups + 1], shared [groups]")
+    given = (out, workspace)
+    if out is None:
+        out = _new(stream, (T, Hq, D), (Hq * D, D, 1), q.dtype, q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must be like q")
+    qs, os_ = q.stride(), out.stride()
+    if qs[2] != 1 or os_[2] != 1:
+        raise ValueError("features must be contiguous")
+    b = _batch(table, cu_q, kv_len, T)
+    lse = _new(stream, (T, Hq), (Hq, 1), torch.float32, q.device) if return_lse else None
+    if scale is None:
+        scale = D ** -0.5
+    if workspace is None:
+        key = (T, Hq, k_pages.dtype, *k_pages.shape[1:], *table.shape, G, max_q, max_group,
+               max_shared, max_tail)
+        size, ws = _sizes.get(key), None
+        if size is None:
+            need = ctypes.c_size_t(0)
+            _check(lib.paged_attention_shared_workspace(c, b, Hq, G, max_q, max_group, max_shared,
+                                                        max_tail, ctypes.byref(need)))
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            size = _sizes[key] = need.value
+        if size:
+            workspace = _new(stream, (size,), (1,), torch.uint8, q.device)
+            ws = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    _check(lib.paged_attention_shared(q.data_ptr(), qs[0], qs[1], Hq, c, b, cu_group.data_ptr(),
+                                      shared.data_ptr(), G, scale, causal, max_q, max_group,
+                                      max_shared, max_tail, out.data_ptr(), os_[0], os_[1],
+                                      None if lse is None else lse.data_ptr(), ws, size,
+                                      _stream(stream, q)))
+    if stream is not None:
         _used(stream, (lse,) if given[0] is out else (out, lse), given)
     return (out, lse) if return_lse else out
 
