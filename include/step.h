@@ -103,7 +103,7 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_str
  *   token    int32 [B]
  *   logprob  fp32 [B], or NULL: the logarithm of the probability with which the
  *            token was drawn (0 at temperature 0)
- *   V        1 .. 393216
+ *   V        1 .. 360448
  */
 moe_status sample(const void* logits, int dtype, int B, int V, int64_t stride, const float* u,
                   const float* temperature, const int32_t* top_k, const float* top_p,

@@ -2,23 +2,33 @@
 // given random number (include/step.h).
 //
 // A row's tokens are ordered by (logit descending, index ascending); every filter keeps a
-// first part of that order, so a row's choice is a threshold: a key, how many tokens of
-// that very key stay (the first by index), and a least weight.  No sort: the threshold
-// comes from histograms of the keys' bits (11, 11, 10 of them), of counts for top-k and of
-// weights for top-p, each level among the keys of the bin before.  The token is then the
+// first part of that order, so a row's choice is a threshold: a logit, how many tokens of
+// that very logit stay (the first by index), and a least weight.  The token is then the
 // first whose cumulative kept weight, in order of index, passes u times the total.
 //
 // Weights w = 2^(-x), x = (max - logit) log2(e) / temperature, are 64-bit integers in
 // units of 2^-45 and their sums exact, so that the result depends neither on the order of
 // atomics nor on how a row is split.  x is taken in pairs of fp32 numbers (Dekker's
-// products and sums), split into a whole number, 1024ths, and a rest r below 2^-11;
+// products and sums), split into a whole number, 1024ths, and a rest r of at most 2^-11;
 // 2^(-i/1024) is read from a table, 2^r - 1 is r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6.  In
 // all a weight is off by 2^-36 of itself; fp32's 2^-22 would put one draw in a few
 // hundred of a flat row on the wrong side of a border.
 //
-// Bound: latency for a few rows, HBM (and the weights' arithmetic, some 40 operations
-// an element) for many.  A cluster of up to eight CTAs takes a row: each holds a slice of
-// its keys in shared memory, read from HBM once, and histograms, sums and positions meet
+// No row is sorted.  A histogram over 1024 bins of x (22 to a factor of two), of counts and
+// of mean places within the bin, gives counts exactly and sums of weights to some 1e-3, and
+// with them the few bins in which the threshold can lie:
+//   top-k    the bin of the k-th token; it and what is above (up to 2048 tokens) go to one
+//            CTA of the row, which has all that is left to do
+//   top-p    the bins that hold 1 - p of the weights behind them, give or take the
+//            histogram's error; one pass sums the weights of all tokens and of those above
+//            the band, the band's tokens go to one CTA, which finds the threshold among them
+// That CTA sorts the up to 2048 tokens that are left.  Where more are left, the threshold
+// comes from histograms over the whole row of the ordered bits (11, 11, 10 of them), of
+// counts or of weights, each level among the tokens of the bin before.
+//
+// Bound: latency for a few rows, HBM and the weights' arithmetic (some 50 operations an
+// element, once) for many.  A cluster of up to eight CTAs takes a row: each holds a slice
+// of it in shared memory, read from HBM once, and histograms, sums and positions meet
 // through distributed shared memory.
 #include <algorithm>
 
@@ -32,12 +42,15 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 2048;
-constexpr int kOneBit = 45;  // a weight of 1 is 2^45
+constexpr int kBins = 2048;     // of ordered bits
+constexpr int kCoarse = 1024;   // of x
+constexpr float kPerOctave = 22.f;
+constexpr int kList = 2048;     // tokens that one CTA of a row takes over
+constexpr int kOneBit = 45;     // a weight of 1 is 2^45
 constexpr unsigned long long kOne = 1ull << kOneBit;
 
 // 2^(-i/32) and 2^(-i/1024), i = 0 .. 31, times 2^63
-__device__ const unsigned long long kCoarse[32] = {
+__device__ const unsigned long long kTable32[32] = {
     0x8000000000000000ull, 0x7d41d96db915019dull, 0x7a92be8a92436616ull, 0x77f25ccdee6d7ae6ull,
     0x75606373ee921c97ull, 0x72dc8373be41a454ull, 0x70666f76154a7089ull, 0x6dfddbcbed791babull,
     0x6ba27e656b4eb57aull, 0x69540ec8f895722dull, 0x6712460a8fc24072ull, 0x64dcdec3371793d1ull,
@@ -46,7 +59,7 @@ __device__ const unsigned long long kCoarse[32] = {
     0x52ff6b54d8a89c75ull, 0x513821818624b40cull, 0x4f7a993048d088d7ull, 0x4dc69cdceaa72a9cull,
     0x4c1bf828c6dc54b8ull, 0x4a7a77d47f7b84b1ull, 0x48e1e9b9d588e19bull, 0x47521cc5a2e6a9e0ull,
     0x45cae0f1f545eb73ull, 0x444c0740496d4294ull, 0x42d561b3e6243d8aull, 0x4166c34c5615d0ecull};
-__device__ const unsigned long long kFine[32] = {
+__device__ const unsigned long long kTable1024[32] = {
     0x8000000000000000ull, 0x7fe9d3a8e07bf086ull, 0x7fd3ab290e46d769ull, 0x7fbd867fdf0acb3bull,
     0x7fa765aca88f6453ull, 0x7f9148aec0b9b7b1ull, 0x7f7b2f857d8c51e5ull, 0x7f651a30352731eeull,
     0x7f4f08ae3dc7c426ull, 0x7f38fafeedc8dd26ull, 0x7f22f1219ba2b4aeull, 0x7f0ceb159deae091ull,
@@ -59,17 +72,27 @@ __device__ const unsigned long long kFine[32] = {
 struct Shared {
   unsigned long long table[1024];  // 2^(-i/1024) in units of 2^-45
   float tablef[1024];
-  unsigned long long hist[kBins];
-  unsigned long long warp[kWarps + 1];
-  unsigned long long slot[2][kMaxCluster];  // totals of the cluster's CTAs, by turns
+  union {
+    unsigned long long hist[kBins];
+    struct {
+      uint32_t mine[kCoarse];                   // this CTA's
+      uint32_t count[kCoarse], place[kCoarse];  // the row's
+    } coarse;
+  };
+  uint32_t list_key[kList];  // the tokens that this CTA takes over, in order of index
+  int list_at[kList];
+  uint16_t local[kList];     // those of its own slice
+  unsigned long long warp[kWarps], warp_kept[kWarps];
+  unsigned long long slot[2][3][kMaxCluster];  // totals of the cluster's CTAs, by turns
   unsigned long long found[4];
-  uint32_t best[kMaxCluster][2];
+  float warpf[kWarps];
+  uint32_t warpc[kWarps];
+  int band[4];
 };
 
-// ordered bits: larger numbers have larger keys; -0 is +0, NaN is -inf
+// ordered bits: larger numbers have larger keys (of numbers without -0 and NaN)
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (!(x == x)) x = -INFINITY;
-  const uint32_t b = __float_as_uint(x + 0.f);
+  const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
@@ -86,12 +109,30 @@ __device__ __forceinline__ unsigned long long peer_u64(const void* p, int rank) 
                : "=l"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t peer_u32(const void* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];"
+               : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
 __device__ __forceinline__ void peer_put(void* p, int rank, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void peer_put32(void* p, int rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
   return v;
 }
 // x * f rounded down (UP: up), for 0 <= f <= 1
@@ -116,20 +157,22 @@ __device__ __forceinline__ unsigned long long times(unsigned long long x, float 
 }
 
 struct Row {
-  uint32_t top;         // the largest key
-  // a quarter of its logit, and 4 log2(e) / temperature: a difference of two logits may
-  // lie past fp32's end, a quarter of it does not
-  float max, c_hi, c_lo;
+  float max;    // the largest logit
+  // a quarter of it, and 4 log2(e) / temperature: a difference of two logits may lie past
+  // fp32's end, a quarter of it does not
+  float quarter, c_hi, c_lo;
+  float bins;   // bins of x for a unit of logits
 };
-__device__ __forceinline__ unsigned long long weight_of(const Shared& sh, const Row& r, uint32_t key) {
-  if (key == r.top) return kOne;
-  const dflt d = df_two_sum(0.25f * value_of(key), -r.max);
+__device__ __forceinline__ unsigned long long weight_of(const Shared& sh, const Row& r, float v) {
+  if (v == r.max) return kOne;
+  const dflt d = df_two_sum(0.25f * v, -r.quarter);
   const float p = d.hi * r.c_hi;  // -x
   if (!(p > -46.f)) return 0;
   const float lo = fmaf(d.hi, r.c_lo, fmaf(d.lo, r.c_hi, fmaf(d.hi, r.c_hi, -p)));
-  const float jn = rintf(p * 1024.f);
-  const float z = fmaf(jn, -0x1p-10f, p);  // exact
-  const int j = -(int)jn;
+  // the nearest whole number of 1024ths: in the last bits of a sum with 1.5 2^23
+  const float t = fmaf(p, 1024.f, 12582912.f);
+  const int j = 0x4b400000 - __float_as_int(t);
+  const float z = fmaf(t - 12582912.f, -0x1p-10f, p);  // exact
   // 2^(z + lo) - 1
   constexpr float kLn2 = 0x1.62e43p-1f, kLn2Lo = -0x1.05c61p-29f;
   const float y = (z + lo) * kLn2;
@@ -139,9 +182,239 @@ __device__ __forceinline__ unsigned long long weight_of(const Shared& sh, const 
   const long long add = (long long)__float2int_rn(sh.tablef[i] * e * 0x1p41f) << 4;
   return (sh.table[i] + add + (1ull << n >> 1)) >> n;
 }
+// where x lies among the bins (monotone in v)
+__device__ __forceinline__ float place_of(const Row& r, float v) {
+  return fminf(v == r.max ? 0.f : (r.max - v) * r.bins, (float)(kCoarse - 1));
+}
 
-// the row's kept tokens: those above `thr`, of its own the ones up to index `cut`, and none
-// of a weight below `least`
+// Tokens to look at: a CTA's slice of the row, or the list that one CTA has taken over.
+struct View {
+  const float* v;         // (list: nullptr)
+  const uint32_t* key;
+  const int* at;
+  int n, begin, chunk;    // chunk: of a warp, contiguous
+  int cluster, rank;
+  __device__ __forceinline__ uint32_t key_at(int i) const { return v ? key_of(v[i]) : key[i]; }
+  __device__ __forceinline__ int index(int i) const { return v ? begin + i : at[i]; }
+  __device__ __forceinline__ void sync() const {
+    if (cluster > 1) cluster_sync(); else __syncthreads();
+  }
+};
+
+// A row's CTA: the steps that several of its paths share.
+struct Worker {
+  Shared& sh;
+  const Row& r;
+  const int tid, lane, warp;
+  int turn = 1;  // of sh.slot: two sets, so that one may still be read while the other is written
+
+  // the sums over the cluster's CTAs: before this one, and of all
+  __device__ void totals(const View& w, unsigned long long mine, unsigned long long& before,
+                         unsigned long long& all) {
+    if (tid < w.cluster) peer_put(&sh.slot[turn][0][w.rank], tid, mine);
+    w.sync();
+    before = all = 0;
+    for (int c = 0; c < w.cluster; ++c) {
+      const unsigned long long x = sh.slot[turn][0][c];
+      if (c < w.rank) before += x;
+      all += x;
+    }
+    turn ^= 1;
+  }
+
+  // The key at which the sum over (key descending) of 1 (counts) or of weights reaches
+  // `target`; `above` gets the sum over larger keys, `here` that of the key itself.  Weights:
+  // of keys above `low` alone, whose own tokens count as `tie` together.
+  __device__ uint32_t select(const View& w, bool mass, unsigned long long target, uint32_t low,
+                             unsigned long long tie, unsigned long long& above, unsigned long long& here) {
+    const int w0 = min(warp * w.chunk, w.n), w1 = min(w0 + w.chunk, w.n);
+    uint32_t prefix = 0;
+    above = 0;
+    for (int level = 0; level < 3; ++level) {
+      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+      for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+      __syncthreads();
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t key = w.key_at(i);
+        if (level > 0 && key >> (shift + bits) != prefix) continue;
+        const int bin = key >> shift & ((1u << bits) - 1);
+        if (!mass) atomicAdd(reinterpret_cast<uint32_t*>(&sh.hist[bin]), 1u);
+        else if (key > low) atomicAdd(&sh.hist[bin], weight_of(sh, r, value_of(key)));
+      }
+      if (mass && tie && w.rank == 0 && tid == 0 && (level == 0 || low >> (shift + bits) == prefix))
+        atomicAdd(&sh.hist[low >> shift & ((1u << bits) - 1)], tie);
+      w.sync();
+      // this CTA's share of the bins, over the cluster, largest first
+      const int share = kBins / w.cluster, b0 = kBins - 1 - w.rank * share;
+      const int each = max(share / kThreads, 1);
+      const bool has = tid < share;
+      unsigned long long v[kBins / kThreads], sum = 0;
+#pragma unroll
+      for (int e = 0; e < kBins / kThreads; ++e) {
+        v[e] = 0;
+        if (has && e < each)
+          for (int c = 0; c < w.cluster; ++c) v[e] += peer_u64(&sh.hist[b0 - tid * each - e], w.cluster > 1 ? c : w.rank);
+        sum += v[e];
+      }
+      const unsigned long long inc = warp_scan(sum, lane);
+      if (lane == 31) sh.warp[warp] = inc;
+      __syncthreads();
+      unsigned long long before = 0, all = 0, less, whole;
+      for (int x = 0; x < kWarps; ++x) {
+        if (x < warp) before += sh.warp[x];
+        all += sh.warp[x];
+      }
+      totals(w, all, less, whole);
+      unsigned long long at = above + less + before + inc - sum;
+      if (has) {
+#pragma unroll
+        for (int e = 0; e < kBins / kThreads; ++e) {
+          if (e < each && at < target && target <= at + v[e]) {
+            for (int c = 0; c < w.cluster; ++c) {
+              peer_put(&sh.found[0], w.cluster > 1 ? c : w.rank, at);
+              peer_put(&sh.found[1], w.cluster > 1 ? c : w.rank, v[e]);
+              peer_put(&sh.found[2], w.cluster > 1 ? c : w.rank, (unsigned long long)(b0 - tid * each - e));
+            }
+          }
+          at += v[e];
+        }
+      }
+      w.sync();
+      above = sh.found[0];
+      here = sh.found[1];
+      prefix = prefix << bits | (uint32_t)sh.found[2];
+    }
+    return prefix;
+  }
+
+  // sums of f over the warps' chunks, into `out`
+  template <typename F>
+  __device__ void chunk_sums(const View& w, F f, unsigned long long* out) {
+    const int w0 = min(warp * w.chunk, w.n), w1 = min(w0 + w.chunk, w.n);
+    unsigned long long sum = 0;
+    for (int i = w0 + lane; i < w1; i += 32) sum += f(w.key_at(i), w.index(i));
+    sum = warp_sum(sum);
+    __syncthreads();  // (out may still be read)
+    if (lane == 0) out[warp] = sum;
+    __syncthreads();
+  }
+
+  // The first token at which the sum of f(key, index), in order of index, passes
+  // `target(total)`, where `sums` are the warps' sums; its index, the total, and f there.
+  template <typename F, typename G>
+  __device__ int locate(const View& w, F f, G target_of, const unsigned long long* sums,
+                        unsigned long long& total, unsigned long long& value) {
+    unsigned long long all = 0, at;
+    for (int x = 0; x < kWarps; ++x) all += sums[x];
+    totals(w, all, at, total);
+    const unsigned long long target = target_of(total);
+    if (at <= target && target < at + all) {  // here: which warp's chunk, then which token
+      int x = 0;
+      while (at + sums[x] <= target) at += sums[x++];
+      __syncthreads();
+      const int c0 = min(x * w.chunk, w.n), c1 = min(c0 + w.chunk, w.n);
+      const int each = (c1 - c0 + kThreads - 1) / kThreads;
+      const int i0 = min(c0 + tid * each, c1), i1 = min(i0 + each, c1);
+      unsigned long long mine = 0;
+      for (int i = i0; i < i1; ++i) mine += f(w.key_at(i), w.index(i));
+      const unsigned long long inc = warp_scan(mine, lane);
+      if (lane == 31) sh.warp[warp] = inc;
+      __syncthreads();
+      for (int y = 0; y < warp; ++y) at += sh.warp[y];
+      at += inc - mine;
+      if (at <= target && target < at + mine) {
+        for (int i = i0; i < i1; ++i) {
+          const unsigned long long v = f(w.key_at(i), w.index(i));
+          if (target < at + v) {
+            for (int c = 0; c < w.cluster; ++c) {
+              peer_put(&sh.found[0], w.cluster > 1 ? c : w.rank, (unsigned long long)w.index(i));
+              peer_put(&sh.found[1], w.cluster > 1 ? c : w.rank, v);
+            }
+            break;
+          }
+          at += v;
+        }
+      }
+    }
+    w.sync();
+    value = sh.found[1];
+    return (int)sh.found[0];
+  }
+};
+
+// The filters over the up to kList tokens of a view that one CTA has: sorted by (key
+// descending, index ascending).  total: the weights that top_p is a part of (0: those of the
+// first k tokens here); above: of tokens that are not here, larger than all.  False where the
+// threshold does not lie here.
+__device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top_p, unsigned long long total,
+                       unsigned long long above, uint32_t& thr, int& cut) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned long long* s = sh.hist;
+  int size = 64;
+  while (size < w.n) size *= 2;
+  __syncthreads();
+  for (int i = tid; i < size; i += kThreads)
+    s[i] = i < w.n ? (unsigned long long)w.key_at(i) << 32 | (uint32_t)~w.index(i) : 0ull;
+  __syncthreads();
+  // bitonic; a warp's pairs lie in blocks of 64 while the distance is up to 32
+  for (int m = 2; m <= size; m *= 2) {
+    for (int d = m / 2; d > 0; d /= 2) {
+      for (int i = tid; i < size / 2; i += kThreads) {
+        const int a = 2 * i - (i & (d - 1)), b = a + d;
+        const unsigned long long x = s[a], y = s[b];
+        if ((x < y) == ((a & m) == 0)) {
+          s[a] = y;
+          s[b] = x;
+        }
+      }
+      if (d > 32 || (d == 1 && m >= 64)) __syncthreads(); else __syncwarp();
+    }
+  }
+  __syncthreads();
+  // weights, each thread's in order
+  constexpr int E = kList / kThreads;
+  const int each = (size + kThreads - 1) / kThreads;
+  unsigned long long v[E], sum = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * each + e;
+    v[e] = e < each && i < w.n && (k == 0 || i < k) ? weight_of(sh, r, value_of((uint32_t)(s[i] >> 32))) : 0ull;
+    sum += v[e];
+  }
+  const unsigned long long inc = warp_scan(sum, lane);
+  if (lane == 31) sh.warp[warp] = inc;
+  __syncthreads();
+  unsigned long long at = inc - sum, all = 0;
+  for (int x = 0; x < kWarps; ++x) {
+    if (x < warp) at += sh.warp[x];
+    all += sh.warp[x];
+  }
+  if (total == 0) total = all;
+  unsigned long long target = ~0ull;
+  if (top_p < 1.f) {
+    target = max(times<true>(total, top_p), 1ull);
+    if (target <= above || target > above + all) return false;  // (the same in all threads)
+    target -= above;
+  }
+  int stay = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    stay += v[e] > 0 && at < target;
+    at += v[e];
+  }
+  stay = __reduce_add_sync(0xffffffffu, stay);
+  if (lane == 0) sh.warpc[warp] = stay;
+  __syncthreads();
+  stay = 0;
+  for (int x = 0; x < kWarps; ++x) stay += sh.warpc[x];
+  const unsigned long long last = s[stay - 1];  // (the largest is always here, or above: stay > 0)
+  thr = (uint32_t)(last >> 32);
+  cut = (int)~(uint32_t)last;
+  return true;
+}
+
+// what is kept: tokens above `thr`, of its own the ones up to index `cut`, and none of a
+// weight below `least`
 struct Kept {
   uint32_t thr;
   int cut;
@@ -149,18 +422,30 @@ struct Kept {
 };
 
 template <typename T>
+__device__ __forceinline__ float logit_of(uint32_t bits) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(bits);
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((uint16_t)bits));
+  else return __uint_as_float(bits << 16);
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p, int cluster,
                                                           int slice) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(Shared));
+  float* vals = reinterpret_cast<float*>(smem + sizeof(Shared));
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int begin = rank * slice, n = max(min(p.V - begin, slice), 0);
-  const int chunk = (slice + kThreads - 1) / kThreads * 32;  // of a warp: contiguous
+  // The slices begin at 16-byte boundaries of memory: the first one's up to VEC - 1 places
+  // before the row are filled with -inf, which no filter ever draws from.
+  constexpr int VEC = 16 / sizeof(T);
+  const T* const src = static_cast<const T*>(p.logits) + row * p.stride;
+  const int begin = rank * slice - (int)(reinterpret_cast<uintptr_t>(src) / sizeof(T) % VEC);
+  const int n = max(min(p.V - begin, slice), 0);
+  const int chunk = (slice + kThreads - 1) / kThreads * 32;
   const int w0 = min(warp * chunk, n), w1 = min(w0 + chunk, n);
 
-  float temperature = p.temperature ? p.temperature[row] : 1.f;
+  const float temperature = p.temperature ? p.temperature[row] : 1.f;
   const bool greedy = !(temperature > 0.f);
   int k = p.top_k ? p.top_k[row] : 0;
   if (k <= 0 || k >= p.V) k = 0;
@@ -174,256 +459,359 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (!(u > 0.f)) u = 0.f;
   u = fminf(u, 0x1.fffffep-1f);
 
-  // ---- keys into shared memory, the largest and its first index
-  uint32_t best = 0;
-  int best_at = 0x7fffffff;
-  {
-    const T* src = static_cast<const T*>(p.logits) + row * p.stride + begin;
-#pragma unroll 8
-    for (int i = w0 + lane; i < w1; i += 32) {
-      float x;
-      if constexpr (sizeof(T) == 4) x = src[i];
-      else if constexpr (std::is_same<T, __half>::value) x = __half2float(src[i]);
-      else x = __bfloat162float(src[i]);
-      const uint32_t key = key_of(x);
-      keys[i] = key;
-      if (key > best) {
-        best = key;
-        best_at = begin + i;
+  // ---- the slice into shared memory, the largest logit and its first index
+  constexpr int AHEAD = 32 / VEC;  // vectors of a thread in flight
+  const int vecs = (n + VEC - 1) / VEC;
+  auto load = [&](int i, uint4& v) {
+    const int at = begin + i * VEC;
+    if (at >= 0 && at + VEC <= p.V) {
+      v = __ldg(reinterpret_cast<const uint4*>(src + at));
+    } else {
+      uint32_t u[4] = {0, 0, 0, 0};
+      for (int e = 0; e < VEC; ++e) {
+        uint32_t bits = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
+        if (at + e >= 0 && at + e < p.V) {
+          if constexpr (sizeof(T) == 4) bits = __float_as_uint(src[at + e]);
+          else bits = reinterpret_cast<const uint16_t*>(src)[at + e];
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w == e * 4 / VEC) u[w] |= sizeof(T) == 4 ? bits : bits << (16 * (e & 1));
       }
+      v = make_uint4(u[0], u[1], u[2], u[3]);
     }
-  }
+  };
+  uint4 ahead[AHEAD];
+#pragma unroll
+  for (int j = 0; j < AHEAD; ++j)
+    if (tid + j * kThreads < vecs) load(tid + j * kThreads, ahead[j]);
   for (int i = tid; i < 1024; i += kThreads) {
-    const unsigned long long t = __umul64hi(kCoarse[i >> 5], kFine[i & 31]);  // 2^62 x
+    const unsigned long long t = __umul64hi(kTable32[i >> 5], kTable1024[i & 31]);  // 2^62 x
     sh.tablef[i] = (float)t * 0x1p-62f;
     sh.table[i] = (t + (1ull << (61 - kOneBit))) >> (62 - kOneBit);
   }
+  float best = -INFINITY;
+  int best_at = 0x7fffffff;
+  for (int base = tid; base < vecs; base += AHEAD * kThreads) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, best, d);
-    const int at = __shfl_xor_sync(0xffffffffu, best_at, d);
-    if (o > best || (o == best && at < best_at)) best = o, best_at = at;
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = base + j * kThreads;
+      if (i >= vecs) break;
+      const uint32_t u[4] = {ahead[j].x, ahead[j].y, ahead[j].z, ahead[j].w};
+      if (i + AHEAD * kThreads < vecs) load(i + AHEAD * kThreads, ahead[j]);
+      float x[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        x[e] = logit_of<T>(sizeof(T) == 4 ? u[e & 3] : u[e / 2 & 3] >> (16 * (e & 1)) & 0xffffu);
+        x[e] = x[e] == x[e] ? x[e] + 0.f : -INFINITY;  // (-0 is +0)
+        if (x[e] > best) {
+          best = x[e];
+          best_at = begin + i * VEC + e;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4)
+        *reinterpret_cast<float4*>(vals + i * VEC + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    }
   }
-  if (lane == 0) sh.warp[warp] = (unsigned long long)best << 32 | (uint32_t)~best_at;
+  unsigned long long first = (unsigned long long)key_of(best) << 32 | (uint32_t)~best_at;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) first = max(first, __shfl_xor_sync(0xffffffffu, first, d));
+  if (lane == 0) sh.warp[warp] = first;
   __syncthreads();
-  if (tid == 0) {
+  if (tid < cluster) {
     unsigned long long m = 0;
     for (int w = 0; w < kWarps; ++w) m = max(m, sh.warp[w]);
-    for (int c = 0; c < cluster; ++c) peer_put(&sh.slot[0][rank], c, m);
+    peer_put(&sh.slot[0][0][rank], tid, m);
   }
   cluster_sync();
-  unsigned long long first = 0;
-  for (int c = 0; c < cluster; ++c) first = max(first, sh.slot[0][c]);
-  Row r;
-  r.top = (uint32_t)(first >> 32);
-  r.max = 0.25f * value_of(r.top);
-  int turn = 1;  // of sh.slot: two sets, so that one may still be read while the other is written
-
-  if (greedy || r.top <= kLowest) {
+  first = 0;
+  for (int c = 0; c < cluster; ++c) first = max(first, sh.slot[0][0][c]);
+  const bool none = (uint32_t)(first >> 32) <= kLowest;
+  if (greedy || none) {
     if (rank == 0 && tid == 0) {
-      const bool none = r.top <= kLowest;
       p.token[row] = none ? -1 : (int)~(uint32_t)first;
       if (p.logprob) p.logprob[row] = none ? __int_as_float(0x7fffffff) : 0.f;
     }
-    cluster_sync();
     return;
   }
+  Row r;
+  r.max = value_of((uint32_t)(first >> 32));
+  r.quarter = 0.25f * r.max;
   {
     const double c = 4 * 1.4426950408889634 / (double)temperature;
     r.c_hi = (float)c;
     r.c_lo = r.c_hi < INFINITY ? (float)(c - (double)r.c_hi) : 0.f;
+    r.bins = fminf(0.25f * r.c_hi * kPerOctave, 1e38f);
   }
-
-  // The key at which the sum over (key descending) of 1 (counts) or of weights reaches
-  // `target`; `above` gets the sum over larger keys, `here` that of the key itself.  Of the
-  // weights, tokens of key `tie` count as `tie_n` together.
-  auto select = [&](bool mass, unsigned long long target, uint32_t low, unsigned long long tie_weight,
-                    unsigned long long& above, unsigned long long& here) -> uint32_t {
-    uint32_t prefix = 0;
-    above = 0;
-    for (int level = 0; level < 3; ++level) {
-      const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-      for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-      __syncthreads();
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t key = keys[i];
-        if (level > 0 && key >> (shift + bits) != prefix) continue;
-        const int bin = key >> shift & ((1u << bits) - 1);
-        if (!mass) atomicAdd(reinterpret_cast<uint32_t*>(&sh.hist[bin]), 1u);
-        else if (key > low) atomicAdd(&sh.hist[bin], weight_of(sh, r, key));
-      }
-      if (mass && tie_weight && rank == 0 && tid == 0 && (level == 0 || low >> (shift + bits) == prefix))
-        atomicAdd(&sh.hist[low >> shift & ((1u << bits) - 1)], tie_weight);
-      cluster_sync();
-      // this CTA's share of the bins, over the cluster, largest first
-      const int share = kBins / cluster, b0 = kBins - 1 - rank * share;
-      unsigned long long v[kBins / kThreads], sum = 0;
-      const int each = max(share / kThreads, 1);
-      const bool has = tid < share;
-      for (int e = 0; e < each; ++e) {
-        v[e] = 0;
-        if (has)
-          for (int c = 0; c < cluster; ++c) v[e] += peer_u64(&sh.hist[b0 - tid * each - e], c);
-        sum += v[e];
-      }
-      unsigned long long inc = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-      }
-      if (lane == 31) sh.warp[warp] = inc;
-      __syncthreads();
-      unsigned long long before = 0, all = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh.warp[w];
-        all += sh.warp[w];
-      }
-      if (tid < cluster) peer_put(&sh.slot[turn][rank], tid, all);
-      cluster_sync();
-      unsigned long long at = above + before + inc - sum;
-      for (int c = 0; c < rank; ++c) at += sh.slot[turn][c];
-      turn ^= 1;
-      if (has) {
-        for (int e = 0; e < each; ++e) {
-          if (at < target && target <= at + v[e]) {
-            for (int c = 0; c < cluster; ++c) {
-              peer_put(&sh.found[0], c, at);
-              peer_put(&sh.found[1], c, v[e]);
-              peer_put(&sh.found[2], c, (unsigned long long)(b0 - tid * each - e));
-            }
-          }
-          at += v[e];
-        }
-      }
-      cluster_sync();
-      above = sh.found[0];
-      here = sh.found[1];
-      prefix = prefix << bits | (uint32_t)sh.found[2];
-    }
-    return prefix;
-  };
-
-  // The first index at which the sum of f(key, index) passes `target(total)`; total and
-  // f there are returned, in every CTA.
-  auto locate = [&](auto f, auto target_of, unsigned long long& total, unsigned long long& value) -> int {
-    unsigned long long sum = 0;
-    for (int i = w0 + lane; i < w1; i += 32) sum += f(keys[i], begin + i);
-    sum = warp_sum(sum);
-    __syncthreads();  // (sh.warp may still be read)
-    if (lane == 0) sh.warp[warp] = sum;
-    __syncthreads();
-    unsigned long long all = 0;
-    for (int w = 0; w < kWarps; ++w) all += sh.warp[w];
-    if (tid < cluster) peer_put(&sh.slot[turn][rank], tid, all);
-    cluster_sync();
-    unsigned long long at = 0;
-    total = 0;
-    for (int c = 0; c < cluster; ++c) {
-      if (c < rank) at += sh.slot[turn][c];
-      total += sh.slot[turn][c];
-    }
-    turn ^= 1;
-    const unsigned long long target = target_of(total);
-    if (at <= target && target < at + all) {  // here: which warp's chunk, then which token
-      int w = 0;
-      while (at + sh.warp[w] <= target) at += sh.warp[w++];
-      __syncthreads();
-      const int c0 = min(w * chunk, n), c1 = min(c0 + chunk, n);
-      const int each = (c1 - c0 + kThreads - 1) / kThreads;
-      const int i0 = min(c0 + tid * each, c1), i1 = min(i0 + each, c1);
-      unsigned long long mine = 0;
-      for (int i = i0; i < i1; ++i) mine += f(keys[i], begin + i);
-      unsigned long long inc = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-      }
-      if (lane == 31) sh.warp[warp] = inc;
-      __syncthreads();
-      for (int x = 0; x < warp; ++x) at += sh.warp[x];
-      at += inc - mine;
-      if (at <= target && target < at + mine) {
-        for (int i = i0; i < i1; ++i) {
-          const unsigned long long v = f(keys[i], begin + i);
-          if (target < at + v) {
-            for (int c = 0; c < cluster; ++c) {
-              peer_put(&sh.found[0], c, (unsigned long long)(begin + i));
-              peer_put(&sh.found[1], c, v);
-            }
-            break;
-          }
-          at += v;
-        }
-      }
-    }
-    cluster_sync();
-    value = sh.found[1];
-    return (int)sh.found[0];
-  };
-
+  Worker work{sh, r, tid, lane, warp};
+  const View whole{vals, nullptr, nullptr, n, begin, chunk, cluster, rank};
   Kept keep{kLowest, -1, 1};  // (nothing at -inf)
-  unsigned long long equal = 0, of_equal = 0;  // tokens of the threshold's key; how many stay
-  if (k > 0) {
-    unsigned long long above;
-    keep.thr = select(false, k, 0, 0, above, equal);
-    of_equal = k - above;
-  }
-  if (top_p < 1.f) {
-    const unsigned long long w_thr = k > 0 ? weight_of(sh, r, keep.thr) : 0, tie = of_equal * w_thr;
-    unsigned long long total, value, above, here;
-    // (the kept tokens' weights)
-    {
-      unsigned long long sum = 0;
-      for (int i = w0 + lane; i < w1; i += 32)
-        if (keys[i] > keep.thr) sum += weight_of(sh, r, keys[i]);
-      sum = warp_sum(sum);
-      __syncthreads();
-      if (lane == 0) sh.warp[warp] = sum;
-      __syncthreads();
-      unsigned long long all = 0;
-      for (int w = 0; w < kWarps; ++w) all += sh.warp[w];
-      if (tid < cluster) peer_put(&sh.slot[turn][rank], tid, all);
-      cluster_sync();
-      total = tie;
-      for (int c = 0; c < cluster; ++c) total += sh.slot[turn][c];
-      turn ^= 1;
-    }
-    (void)value;
-    const unsigned long long target = max(times<true>(total, top_p), 1ull);
-    const uint32_t thr = select(true, target, keep.thr, tie, above, here);
-    const unsigned long long w = weight_of(sh, r, thr);
-    if (thr != keep.thr) equal = here / w;
-    of_equal = (target - above + w - 1) / w;
-    keep.thr = thr;
-  }
   if (min_p > 0.f) keep.least = max(times<true>(kOne, min_p), 1ull);
-  if (k > 0 || top_p < 1.f) {
-    keep.cut = 0x7fffffff;
-    if (of_equal < equal) {
-      unsigned long long total, value;
-      const uint32_t thr = keep.thr;
-      keep.cut = locate([thr](uint32_t key, int) -> unsigned long long { return key == thr; },
-                        [of_equal](unsigned long long) { return of_equal - 1; }, total, value);
-      cluster_sync();  // (sh.found is read before it is written again)
-    }
-  }
-  unsigned long long total, value;
-  const int token = locate(
-      [&](uint32_t key, int at) -> unsigned long long {
-        if (key < keep.thr || (key == keep.thr && at > keep.cut)) return 0;
-        const unsigned long long w = weight_of(sh, r, key);
-        return w >= keep.least ? w : 0;
-      },
-      [u](unsigned long long total) { return times<false>(total, u); }, total, value);
-  if (rank == 0 && tid == 0) {
+  auto kept_weight = [&](uint32_t key, int at) -> unsigned long long {
+    if (key < keep.thr || (key == keep.thr && at > keep.cut)) return 0;
+    const unsigned long long w = weight_of(sh, r, value_of(key));
+    return w >= keep.least ? w : 0;
+  };
+  auto draw = [u](unsigned long long total) { return times<false>(total, u); };
+  auto put = [&](int token, unsigned long long total, unsigned long long value) {
     p.token[row] = token;
     if (p.logprob) {
       const unsigned long long rest = total - value;
       p.logprob[row] = rest < value ? log1pf(-((float)rest / (float)total)) : logf((float)value / (float)total);
     }
+  };
+  // the filters over the tokens of a view, all of which they concern
+  auto filter = [&](const View& w) {
+    unsigned long long equal = 0, of_equal = 0, above;  // tokens of the threshold's key; how many stay
+    bool cut = false;
+    if (k > 0) {
+      keep.thr = work.select(w, false, k, 0, 0, above, equal);
+      of_equal = k - above;
+      cut = true;
+    }
+    if (top_p < 1.f) {
+      const unsigned long long tie = k > 0 ? of_equal * weight_of(sh, r, value_of(keep.thr)) : 0;
+      unsigned long long here, all = 0, before, total;
+      const uint32_t low = keep.thr;
+      work.chunk_sums(w, [&](uint32_t key, int) { return key > low ? weight_of(sh, r, value_of(key)) : 0ull; }, sh.warp);
+      for (int x = 0; x < kWarps; ++x) all += sh.warp[x];
+      work.totals(w, all, before, total);
+      const unsigned long long target = max(times<true>(total + tie, top_p), 1ull);
+      const uint32_t thr = work.select(w, true, target, low, tie, above, here);
+      const unsigned long long one = weight_of(sh, r, value_of(thr));
+      if (thr != low || k == 0) equal = here / one;
+      of_equal = (target - above + one - 1) / one;
+      keep.thr = thr;
+      cut = true;
+    }
+    if (cut) {
+      keep.cut = 0x7fffffff;
+      if (of_equal < equal) {
+        unsigned long long total, value;
+        const uint32_t thr = keep.thr;
+        auto is = [thr](uint32_t key, int) -> unsigned long long { return key == thr; };
+        work.chunk_sums(w, is, sh.warp_kept);
+        keep.cut = work.locate(w, is, [of_equal](unsigned long long) { return of_equal - 1; }, sh.warp_kept,
+                               total, value);
+      }
+    }
+  };
+  unsigned long long total, value;
+
+  if (p.V + VEC > kList && (k > 0 || top_p < 1.f)) {
+    // ---- counts and mean places in the bins of x: a token is 2^place_bits + its place in
+    // the bin, in as many of its leading bits as the sums of a slice leave room for
+    auto& co = sh.coarse;
+    const int count_bits = 32 - __clz(slice), level_bits = max(32 - 2 * count_bits, 0);
+    const int place_bits = level_bits ? count_bits + level_bits : 0;
+    const float levels = (float)(1 << level_bits);
+    for (int i = tid; i < kCoarse; i += kThreads) co.mine[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const float x = place_of(r, vals[i]);
+      const int b = (int)x;
+      atomicAdd(&co.mine[b], level_bits ? (1u << place_bits) + (uint32_t)((x - (float)b) * levels) : 1u);
+    }
+    cluster_sync();
+    {
+      const int share = kCoarse / cluster;
+      for (int i = tid; i < share; i += kThreads) {
+        const int b = rank * share + i;
+        uint32_t count = 0, place = 0;
+        for (int c = 0; c < cluster; ++c) {
+          const uint32_t v = peer_u32(&co.mine[b], c);
+          count += v >> place_bits;
+          if (level_bits) place += v & ((1u << place_bits) - 1);
+        }
+        for (int c = 0; c < cluster; ++c) {
+          peer_put32(&co.count[b], c, count);
+          peer_put32(&co.place[b], c, place);
+        }
+      }
+    }
+    cluster_sync();
+    // ---- which bins: two a thread
+    const int b0 = 2 * tid;
+    const uint32_t n0 = co.count[b0], n1 = co.count[b0 + 1];
+    const uint32_t inc = warp_scan(n0 + n1, lane);
+    if (lane == 31) sh.warpc[warp] = inc;
+    if (tid < 4) sh.band[tid] = kCoarse;  // first bin, last bin, tokens above the first, up to the last
+    __syncthreads();
+    uint32_t upto = inc - n0 - n1;
+    for (int x = 0; x < warp; ++x) upto += sh.warpc[x];
+    const uint32_t c0 = upto + n0, c1 = c0 + n1;  // tokens up to either bin
+    if (k > 0) {
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t before = e ? c0 : upto, after = e ? c1 : c0;
+        if (before < (uint32_t)k && (uint32_t)k <= after) {
+          sh.band[0] = 0;
+          sh.band[1] = b0 + e;
+          sh.band[2] = 0;
+          sh.band[3] = (int)after;
+        }
+      }
+      __syncthreads();
+    } else {
+      // weights: the bin's at its edge, less the mean place's part of the bin's span;
+      // summed from the far end, so that small sums keep their bits
+      constexpr float kSpan = 0.031015526f;  // 1 - 2^(-1/22)
+      auto mass = [&](int b, uint32_t count) {
+        if (count == 0 || b == kCoarse - 1) return 0.f;
+        // (a level stands for its middle)
+        const float places = ((float)co.place[b] + 0.5f * (float)count) / levels;
+        return exp2f(-(float)b * (1.f / kPerOctave)) * ((float)count - places * kSpan);
+      };
+      const float m0 = mass(b0, n0), m1 = mass(b0 + 1, n1);
+      float suffix = m0 + m1;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float o = __shfl_down_sync(0xffffffffu, suffix, d);
+        if (lane + d < 32) suffix += o;
+      }
+      if (lane == 0) sh.warpf[warp] = suffix;
+      float after = __shfl_down_sync(0xffffffffu, suffix, 1);
+      if (lane == 31) after = 0.f;
+      __syncthreads();
+      float sum = 0.f;
+      for (int x = kWarps - 1; x >= 0; --x) {
+        if (x > warp) after += sh.warpf[x];
+        sum += sh.warpf[x];
+      }
+      // the first bins behind which there is surely no more, and surely less, than the rest
+      const float rest = (1.f - top_p) * sum;
+      // (half a level, 1.3e-4 for the chord of 2^(-x) over a bin, fp32's sums)
+      const float off = kSpan * 0.5f / levels + 5e-4f;
+      const float hi = rest * (1.f + 2.f * off) + 1e-6f * sum, lo = rest * (1.f - 2.f * off) - 1e-6f * sum;
+      for (int e = 0; e < 2; ++e) {
+        const float s = e ? after : after + m1;  // behind bin b0 + e
+        if (s <= hi) atomicMin(&sh.band[0], b0 + e);
+        if (s <= lo) atomicMin(&sh.band[1], b0 + e);
+      }
+      __syncthreads();
+      for (int e = 0; e < 2; ++e) {
+        if (sh.band[0] == b0 + e) sh.band[2] = (int)(e ? c0 : upto);
+        if (sh.band[1] == b0 + e) sh.band[3] = (int)(e ? c1 : c0);
+      }
+      __syncthreads();
+    }
+    const int first_bin = sh.band[0], last_bin = sh.band[1];
+    const bool fits = first_bin <= last_bin && last_bin < kCoarse && sh.band[3] - sh.band[2] <= kList;
+    if (fits) {  // (the same in all CTAs of the row, which hold the same sums)
+      // ---- one pass: the band's tokens are counted; top-p: weights of all tokens, of those
+      // above the band, and of those that min-p leaves of them
+      unsigned long long sum = 0, above = 0, kept = 0;
+      uint32_t in = 0;
+      if (k > 0) {
+#pragma unroll 4
+        for (int i = w0 + lane; i < w1; i += 32) in += (int)place_of(r, vals[i]) <= last_bin;
+      } else {
+#pragma unroll 2
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const float v = vals[i];
+          const int b = (int)place_of(r, v);
+          const unsigned long long w = weight_of(sh, r, v);
+          in += b >= first_bin && b <= last_bin;
+          sum += w;
+          if (b < first_bin) {
+            above += w;
+            if (w >= keep.least) kept += w;
+          }
+        }
+      }
+      in = __reduce_add_sync(0xffffffffu, in);
+      sum = warp_sum(sum);
+      above = warp_sum(above);
+      kept = warp_sum(kept);
+      __syncthreads();
+      if (lane == 0) {
+        sh.warpc[warp] = in;
+        sh.hist[warp] = sum;
+        sh.hist[kWarps + warp] = above;
+        sh.warp_kept[warp] = kept;
+      }
+      __syncthreads();
+      unsigned long long mine[3] = {0, 0, 0};
+      uint32_t off = 0;
+      for (int x = 0; x < kWarps; ++x) {
+        if (x < warp) off += sh.warpc[x];
+        mine[0] += sh.warpc[x];
+        mine[1] += sh.hist[x];
+        mine[2] += sh.hist[kWarps + x];
+      }
+      if (tid < cluster)
+#pragma unroll
+        for (int e = 0; e < 3; ++e) peer_put(&sh.slot[work.turn][e][rank], tid, mine[e]);
+      cluster_sync();
+      unsigned long long got[3] = {0, 0, 0};
+      uint32_t before = 0;
+      for (int c = 0; c < cluster; ++c) {
+        if (c < rank) before += (uint32_t)sh.slot[work.turn][0][c];
+#pragma unroll
+        for (int e = 0; e < 3; ++e) got[e] += sh.slot[work.turn][e][c];
+      }
+      work.turn ^= 1;
+      // ---- to the first CTA, in order of index
+#pragma unroll 4
+      for (int base = w0; base < w1; base += 32) {
+        const int i = base + lane;
+        const int b = i < w1 ? (int)place_of(r, vals[i]) : kCoarse;
+        const bool is = b >= first_bin && b <= last_bin;
+        const uint32_t all = __ballot_sync(0xffffffffu, is);
+        if (is && before + off + __popc(all) <= (uint32_t)kList) {
+          const uint32_t at = off + __popc(all & ((1u << lane) - 1));
+          sh.local[at] = (uint16_t)i;
+          peer_put32(&sh.list_key[before + at], 0, key_of(vals[i]));
+          peer_put32(&sh.list_at[before + at], 0, (uint32_t)(begin + i));
+        }
+        off += __popc(all);
+      }
+      cluster_sync();
+      const int listed = (int)got[0];
+      const View list{nullptr, sh.list_key, sh.list_at, listed, 0, (listed + kThreads - 1) / kThreads * 32, 1, 0};
+      if (k > 0) {  // all that is left is in the list
+        if (rank != 0) return;
+        settle(sh, r, list, k, top_p, 0, 0, keep.thr, keep.cut);
+        work.chunk_sums(list, kept_weight, sh.warp_kept);
+        const int token = work.locate(list, kept_weight, draw, sh.warp_kept, total, value);
+        if (tid == 0) put(token, total, value);
+        return;
+      }
+      if (rank == 0) {
+        const bool good = settle(sh, r, list, 0, top_p, got[1], got[2], keep.thr, keep.cut);
+        if (tid < cluster) {
+          peer_put(&sh.found[2], tid, good ? keep.thr : 0ull);
+          peer_put(&sh.found[3], tid, (unsigned long long)(uint32_t)keep.cut);
+        }
+      }
+      cluster_sync();
+      if (sh.found[2] != 0) {
+        keep.thr = (uint32_t)sh.found[2];
+        keep.cut = (int)(uint32_t)sh.found[3];
+        // the band's tokens that stay join their chunks' sums
+        for (int i = tid; i < (int)mine[0]; i += kThreads) {
+          const int at = sh.local[i];
+          const unsigned long long w = kept_weight(key_of(vals[at]), begin + at);
+          if (w) atomicAdd(&sh.warp_kept[at / chunk], w);
+        }
+        __syncthreads();
+        const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
+        if (rank == 0 && tid == 0) put(token, total, value);
+        return;
+      }
+      keep.thr = kLowest;
+      keep.cut = -1;
+      cluster_sync();
+    }
   }
+  if (k > 0 || top_p < 1.f) {
+    if (p.V + VEC <= kList) settle(sh, r, whole, k, top_p, 0, 0, keep.thr, keep.cut);
+    else filter(whole);
+  }
+  work.chunk_sums(whole, kept_weight, sh.warp_kept);
+  const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
+  if (rank == 0 && tid == 0) put(token, total, value);
 }
 
 template <typename T>
@@ -432,7 +820,8 @@ cudaError_t sample_launch(const SampleParams& p, cudaStream_t st) {
   int cluster = 1;
   while (cluster < kMaxCluster && (p.V > 24576 * cluster || (p.V > 2048 * cluster && (long long)p.B * cluster < 2 * sms)))
     cluster *= 2;
-  const int slice = (p.V + cluster - 1) / cluster;
+  // (the row may begin up to seven places behind a 16-byte boundary)
+  const int slice = ((p.V + 7 + cluster - 1) / cluster + 7) / 8 * 8;
   const int smem = (int)sizeof(Shared) + slice * 4;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem((const void*)sample_kernel<T>, 232448 - 1024, allowed);

@@ -50,7 +50,7 @@ struct SampleParams {
   long long stride;
   int dtype, B, V;
 };
-constexpr int kSampleMaxV = 393216;
+constexpr int kSampleMaxV = 360448;
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st);
 
 }  // namespace moe

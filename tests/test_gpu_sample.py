@@ -63,7 +63,7 @@ def test_settings(V, kw):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP], ids=["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("B,V", [(1, 130001), (3, 65521), (40, 8191), (300, 700), (2, 393216), (1, 393215)])
+@pytest.mark.parametrize("B,V", [(1, 130001), (3, 65521), (40, 8191), (300, 700), (2, 360448), (1, 360447)])
 def test_sizes(dtype, B, V):
     z, u = logits(B + V, B, V, dtype)
     rows = torch.arange(B)
@@ -97,6 +97,33 @@ def test_ties_across_the_slices_of_a_row():
     z = (torch.randn(4, 100003, generator=g) * 2).round()
     u = torch.tensor([0.03, 0.37, 0.71, 0.9999])
     for kw in (dict(k=100), dict(k=5000), dict(p=0.7), dict(p=0.93, k=30000), dict(m=0.3)):
+        run(z, u, **kw)
+
+
+@pytest.mark.parametrize("V", [2049, 9000, 131072])
+@pytest.mark.parametrize("scale", [0.01, 0.5, 2.5, 8.0, 30.0])
+def test_nuclei_of_all_sizes(V, scale):
+    """From one token to nearly all of the row; logits that differ by less than a bin among them."""
+    z, u = logits(V, 4, V, FP, scale)
+    for p in (1e-6, 0.1, 0.5, 0.9, 0.99, 0.9999, 1 - 2.0 ** -24):
+        run(z, u, p=p)
+    run(z.to(BF), u, p=torch.tensor([0.3, 0.8, 0.95, 0.999]), m=torch.tensor([0.0, 1e-3, 0.2, 0.0]))
+
+
+def test_top_k_of_all_sizes():
+    z, u = logits(9, 4, 40000)
+    for k in (1, 2, 100, 1000, 2047, 2048, 2049, 3000, 39999, 40000):
+        run(z, u, k=k)
+        run(z, u, k=k, p=0.8, m=0.001)
+    run(z.to(BF), u, k=torch.tensor([3, 300, 1500, 20000]), p=0.97)
+
+
+def test_few_distinct_logits():
+    """Every bin holds one value: a threshold's key is most of its band."""
+    g = torch.Generator().manual_seed(12)
+    z = torch.randint(0, 12, (5, 30011), generator=g).float() * 0.75
+    u = torch.tensor([0.0, 0.21, 0.5, 0.83, 0.9999])
+    for kw in (dict(p=0.2), dict(p=0.55, m=0.01), dict(p=0.9), dict(k=1000), dict(k=9000, p=0.5), dict(k=29000)):
         run(z, u, **kw)
 
 

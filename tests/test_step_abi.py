@@ -84,7 +84,7 @@ def _sample(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), 1), (dict(u=None), 1), (dict(token=None), 1), (dict(dtype=4), 1), (dict(dtype=0), 1),
-    (dict(B=-1), 1), (dict(V=0), 1), (dict(V=393217), 2), (dict(logits=_A + 2), 1), (dict(u=_B + 2), 1),
+    (dict(B=-1), 1), (dict(V=0), 1), (dict(V=360449), 2), (dict(logits=_A + 2), 1), (dict(u=_B + 2), 1),
     (dict(t=_C + 1), 1), (dict(k=_C + 1), 1), (dict(p=_C + 2), 1), (dict(m=_C + 2), 1), (dict(token=_D + 2), 1),
     (dict(logprob=_D + 2), 1)])
 def test_sample_rejects_bad_arguments(lib, kw, status):
