@@ -69,7 +69,7 @@ __device__ const unsigned long long kTable1024[32] = {
     0x7deff6b672f84e24ull, 0x7dda25d7d6b2177full, 0x7dc458c0af549908ull, 0x7dae8f7055489813ull,
     0x7d98c9e62113e1faull, 0x7d8308216b594720ull, 0x7d6d4a218cd895e5ull, 0x7d578fe5de6e95a0ull};
 
-struct Shared {
+struct __align__(16) Shared {
   unsigned long long table[1024];  // 2^(-i/1024) in units of 2^-45
   float tablef[1024];
   union {
@@ -79,16 +79,18 @@ struct Shared {
       uint32_t count[kCoarse], place[kCoarse];  // the row's
     } coarse;
   };
-  uint32_t list_key[kList];  // the tokens that this CTA takes over, in order of index
+  uint32_t list_key[kList];  // the tokens that this CTA takes over
   int list_at[kList];
   uint16_t local[kList];     // those of its own slice
-  unsigned long long warp[kWarps], warp_kept[kWarps];
+  unsigned long long warp[kWarps], warp_kept[kWarps], warp_above[kWarps];
   unsigned long long slot[2][3][kMaxCluster];  // totals of the cluster's CTAs, by turns
   unsigned long long found[4];
   float warpf[kWarps];
   uint32_t warpc[kWarps];
   int band[4];
+  uint32_t listed, taken;  // tokens of the list; of this CTA's slice
 };
+static_assert(sizeof(Shared) % 16 == 0, "the slice behind it is written 16 bytes at a time");
 
 // ordered bits: larger numbers have larger keys (of numbers without -0 and NaN)
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -120,6 +122,12 @@ __device__ __forceinline__ void peer_put(void* p, int rank, unsigned long long v
 }
 __device__ __forceinline__ void peer_put32(void* p, int rank, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_add32(void* p, int rank, uint32_t v) {
+  uint32_t r;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;"
+               : "=r"(r) : "r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
+  return r;
 }
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -342,53 +350,94 @@ struct Worker {
   }
 };
 
+// Sorts size <= E kThreads numbers (a power of two of at least 32 E; thread t has those at
+// E t .. E t + E - 1), largest first: bitonic, within a thread, a warp, or through `s`.
+template <int E>
+__device__ __forceinline__ void sort(unsigned long long (&v)[E], int size, unsigned long long* s) {
+  const int i0 = threadIdx.x * E;
+  for (int m = 2; m <= size; m *= 2) {
+    for (int d = m / 2; d > 0; d /= 2) {
+      if (d < E) {
+#pragma unroll
+        for (int b = 1; b < E; b *= 2) {
+          if (b != d) continue;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (e & b) continue;
+            const unsigned long long x = v[e], y = v[e | b];
+            const bool swap = (x < y) == (((i0 + e) & m) == 0);
+            v[e] = swap ? y : x;
+            v[e | b] = swap ? x : y;
+          }
+        }
+      } else if (d < 32 * E) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const unsigned long long x = v[e], y = __shfl_xor_sync(0xffffffffu, x, d / E);
+          const bool larger = (((i0 + e) & d) == 0) == (((i0 + e) & m) == 0);
+          v[e] = larger == (x > y) ? x : y;
+        }
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[i0 + e] = v[e];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const unsigned long long x = v[e], y = s[(i0 + e) ^ d];
+          const bool larger = (((i0 + e) & d) == 0) == (((i0 + e) & m) == 0);
+          v[e] = larger == (x > y) ? x : y;
+        }
+      }
+    }
+  }
+}
+__device__ __forceinline__ int sort_size(int n, int E) {
+  int size = 32 * E;
+  while (size < n) size *= 2;
+  return size;
+}
+
+// The sums over the CTA of what the threads before have, and of all.
+__device__ __forceinline__ void block_scan(Shared& sh, unsigned long long mine, unsigned long long& before,
+                                           unsigned long long& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned long long inc = warp_scan(mine, lane);
+  __syncthreads();
+  if (lane == 31) sh.warp[warp] = inc;
+  __syncthreads();
+  before = inc - mine;
+  all = 0;
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) {
+    if (x < warp) before += sh.warp[x];
+    all += sh.warp[x];
+  }
+}
+
 // The filters over the up to kList tokens of a view that one CTA has: sorted by (key
 // descending, index ascending).  total: the weights that top_p is a part of (0: those of the
 // first k tokens here); above: of tokens that are not here, larger than all.  False where the
 // threshold does not lie here.
-__device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top_p, unsigned long long total,
-                       unsigned long long above, uint32_t& thr, int& cut) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <int E>
+__device__ bool settle_n(Shared& sh, const Row& r, const View& w, int k, float top_p, unsigned long long total,
+                         unsigned long long above, uint32_t& thr, int& cut) {
+  const int tid = threadIdx.x;
   unsigned long long* s = sh.hist;
-  int size = 64;
-  while (size < w.n) size *= 2;
-  __syncthreads();
-  for (int i = tid; i < size; i += kThreads)
-    s[i] = i < w.n ? (unsigned long long)w.key_at(i) << 32 | (uint32_t)~w.index(i) : 0ull;
-  __syncthreads();
-  // bitonic; a warp's pairs lie in blocks of 64 while the distance is up to 32
-  for (int m = 2; m <= size; m *= 2) {
-    for (int d = m / 2; d > 0; d /= 2) {
-      for (int i = tid; i < size / 2; i += kThreads) {
-        const int a = 2 * i - (i & (d - 1)), b = a + d;
-        const unsigned long long x = s[a], y = s[b];
-        if ((x < y) == ((a & m) == 0)) {
-          s[a] = y;
-          s[b] = x;
-        }
-      }
-      if (d > 32 || (d == 1 && m >= 64)) __syncthreads(); else __syncwarp();
-    }
-  }
-  __syncthreads();
-  // weights, each thread's in order
-  constexpr int E = kList / kThreads;
-  const int each = (size + kThreads - 1) / kThreads;
-  unsigned long long v[E], sum = 0;
+  unsigned long long key[E], v[E], sum = 0, at, all;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int i = tid * each + e;
-    v[e] = e < each && i < w.n && (k == 0 || i < k) ? weight_of(sh, r, value_of((uint32_t)(s[i] >> 32))) : 0ull;
+    const int i = tid * E + e;
+    key[e] = i < w.n ? (unsigned long long)w.key_at(i) << 32 | (uint32_t)~w.index(i) : 0ull;
+  }
+  sort<E>(key, sort_size(w.n, E), s);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    v[e] = i < w.n && (k == 0 || i < k) ? weight_of(sh, r, value_of((uint32_t)(key[e] >> 32))) : 0ull;
     sum += v[e];
   }
-  const unsigned long long inc = warp_scan(sum, lane);
-  if (lane == 31) sh.warp[warp] = inc;
-  __syncthreads();
-  unsigned long long at = inc - sum, all = 0;
-  for (int x = 0; x < kWarps; ++x) {
-    if (x < warp) at += sh.warp[x];
-    all += sh.warp[x];
-  }
+  block_scan(sh, sum, at, all);
   if (total == 0) total = all;
   unsigned long long target = ~0ull;
   if (top_p < 1.f) {
@@ -396,21 +445,23 @@ __device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top
     if (target <= above || target > above + all) return false;  // (the same in all threads)
     target -= above;
   }
-  int stay = 0;
+  // the last token that stays has weight, begins before the target, and the next does not
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    stay += v[e] > 0 && at < target;
-    at += v[e];
+    const unsigned long long next = at + v[e];
+    if (v[e] > 0 && at < target && (next >= target || next == all)) sh.found[0] = key[e];
+    at = next;
   }
-  stay = __reduce_add_sync(0xffffffffu, stay);
-  if (lane == 0) sh.warpc[warp] = stay;
   __syncthreads();
-  stay = 0;
-  for (int x = 0; x < kWarps; ++x) stay += sh.warpc[x];
-  const unsigned long long last = s[stay - 1];  // (the largest is always here, or above: stay > 0)
-  thr = (uint32_t)(last >> 32);
-  cut = (int)~(uint32_t)last;
+  thr = (uint32_t)(sh.found[0] >> 32);
+  cut = (int)~(uint32_t)sh.found[0];
   return true;
+}
+__device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top_p, unsigned long long total,
+                       unsigned long long above, uint32_t& thr, int& cut) {
+  __syncthreads();
+  return w.n <= kThreads ? settle_n<1>(sh, r, w, k, top_p, total, above, thr, cut)
+                         : settle_n<kList / kThreads>(sh, r, w, k, top_p, total, above, thr, cut);
 }
 
 // what is kept: tokens above `thr`, of its own the ones up to index `cut`, and none of a
@@ -420,6 +471,44 @@ struct Kept {
   int cut;
   unsigned long long least;
 };
+
+// The draw among the tokens of a list (in any order) that are kept.
+template <int E, typename Put>
+__device__ void draw_n(Shared& sh, const Row& r, const View& w, const Kept& keep, float u, Put put) {
+  const int tid = threadIdx.x;
+  unsigned long long key[E], v[E], sum = 0, at, total;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {  // by index, the first first
+    const int i = tid * E + e;
+    key[e] = i < w.n ? (unsigned long long)(uint32_t)~w.index(i) << 32 | (uint32_t)i : 0ull;
+  }
+  sort<E>(key, sort_size(w.n, E), sh.hist);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    v[e] = 0;
+    if (tid * E + e < w.n) {
+      const int i = (int)(uint32_t)key[e];
+      const uint32_t k = w.key_at(i);
+      if (k > keep.thr || (k == keep.thr && w.index(i) <= keep.cut)) {
+        const unsigned long long x = weight_of(sh, r, value_of(k));
+        v[e] = x >= keep.least ? x : 0;
+      }
+    }
+    sum += v[e];
+  }
+  block_scan(sh, sum, at, total);
+  const unsigned long long target = times<false>(total, u);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (at <= target && target < at + v[e]) put((int)~(uint32_t)(key[e] >> 32), total, v[e]);
+    at += v[e];
+  }
+}
+template <typename Put>
+__device__ void draw_sorted(Shared& sh, const Row& r, const View& w, const Kept& keep, float u, Put put) {
+  if (w.n <= kThreads) draw_n<1>(sh, r, w, keep, u, put);
+  else draw_n<kList / kThreads>(sh, r, w, keep, u, put);
+}
 
 template <typename T>
 __device__ __forceinline__ float logit_of(uint32_t bits) {
@@ -518,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
   for (int d = 16; d; d >>= 1) first = max(first, __shfl_xor_sync(0xffffffffu, first, d));
   if (lane == 0) sh.warp[warp] = first;
+  if (tid == 0) sh.listed = sh.taken = 0;
   __syncthreads();
   if (tid < cluster) {
     unsigned long long m = 0;
@@ -539,9 +629,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   r.max = value_of((uint32_t)(first >> 32));
   r.quarter = 0.25f * r.max;
   {
-    const double c = 4 * 1.4426950408889634 / (double)temperature;
-    r.c_hi = (float)c;
-    r.c_lo = r.c_hi < INFINITY ? (float)(c - (double)r.c_hi) : 0.f;
+    // (fp64 costs microseconds here)
+    const dflt c = df_div(dflt{4 * 0x1.715476p+0f, 4 * 0x1.4ae0cp-26f}, dflt{temperature, 0.f});
+    const bool finite = c.hi < INFINITY;  // (else one of 0, or past fp32's end)
+    r.c_hi = finite ? c.hi : temperature < 1.f ? INFINITY : 0.f;
+    r.c_lo = finite ? c.lo : 0.f;
     r.bins = fminf(0.25f * r.c_hi * kPerOctave, 1e38f);
   }
   Worker work{sh, r, tid, lane, warp};
@@ -608,22 +700,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const float levels = (float)(1 << level_bits);
     for (int i = tid; i < kCoarse; i += kThreads) co.mine[i] = 0;
     __syncthreads();
+    if (k > 0 && k <= kThreads * cluster / 4) {
+      // of the threads' largest logits alone: the bin up to which there are k of those holds
+      // no fewer than k of all tokens, and few more
+      if (best > -INFINITY) atomicAdd(&co.mine[(int)place_of(r, best)], 1u << place_bits);
+    } else {
 #pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const float x = place_of(r, vals[i]);
-      const int b = (int)x;
-      atomicAdd(&co.mine[b], level_bits ? (1u << place_bits) + (uint32_t)((x - (float)b) * levels) : 1u);
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const float x = place_of(r, vals[i]);
+        const int b = (int)x;
+        atomicAdd(&co.mine[b], level_bits ? (1u << place_bits) + (uint32_t)((x - (float)b) * levels) : 1u);
+      }
     }
     cluster_sync();
     {
       const int share = kCoarse / cluster;
       for (int i = tid; i < share; i += kThreads) {
         const int b = rank * share + i;
-        uint32_t count = 0, place = 0;
-        for (int c = 0; c < cluster; ++c) {
-          const uint32_t v = peer_u32(&co.mine[b], c);
-          count += v >> place_bits;
-          if (level_bits) place += v & ((1u << place_bits) - 1);
+        uint32_t v[kMaxCluster], count = 0, place = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) v[c] = c < cluster ? peer_u32(&co.mine[b], c) : 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          count += v[c] >> place_bits;
+          if (level_bits) place += v[c] & ((1u << place_bits) - 1);
         }
         for (int c = 0; c < cluster; ++c) {
           peer_put32(&co.count[b], c, count);
@@ -682,8 +782,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // the first bins behind which there is surely no more, and surely less, than the rest
       const float rest = (1.f - top_p) * sum;
       // (half a level, 1.3e-4 for the chord of 2^(-x) over a bin, fp32's sums)
-      const float off = kSpan * 0.5f / levels + 5e-4f;
-      const float hi = rest * (1.f + 2.f * off) + 1e-6f * sum, lo = rest * (1.f - 2.f * off) - 1e-6f * sum;
+      const float off = 2.f * (kSpan * 0.5f / levels + 5e-4f);
+      const float hi = rest * (1.f + off) + 1e-6f * sum, lo = rest * (1.f - off) - 1e-6f * sum;
       for (int e = 0; e < 2; ++e) {
         const float s = e ? after : after + m1;  // behind bin b0 + e
         if (s <= hi) atomicMin(&sh.band[0], b0 + e);
@@ -699,110 +799,99 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int first_bin = sh.band[0], last_bin = sh.band[1];
     const bool fits = first_bin <= last_bin && last_bin < kCoarse && sh.band[3] - sh.band[2] <= kList;
     if (fits) {  // (the same in all CTAs of the row, which hold the same sums)
-      // ---- one pass: the band's tokens are counted; top-p: weights of all tokens, of those
-      // above the band, and of those that min-p leaves of them
+      // ---- one pass: the band's tokens go to the row's first CTA, in any order; top-p:
+      // weights of all tokens, of those above the band, and of those that min-p leaves of them
       unsigned long long sum = 0, above = 0, kept = 0;
-      uint32_t in = 0;
+      auto take = [&](int i, float v) {
+        const uint32_t mine = atomicAdd(&sh.taken, 1u);
+        if (mine < (uint32_t)kList) sh.local[mine] = (uint16_t)i;
+        const uint32_t at = peer_add32(&sh.listed, 0, 1);
+        if (at < (uint32_t)kList) {
+          peer_put32(&sh.list_key[at], 0, key_of(v));
+          peer_put32(&sh.list_at[at], 0, (uint32_t)(begin + i));
+        }
+      };
       if (k > 0) {
 #pragma unroll 4
-        for (int i = w0 + lane; i < w1; i += 32) in += (int)place_of(r, vals[i]) <= last_bin;
+        for (int i = w0 + lane; i < w1; i += 32) {
+          const float v = vals[i];
+          if ((int)place_of(r, v) <= last_bin) take(i, v);
+        }
       } else {
 #pragma unroll 2
         for (int i = w0 + lane; i < w1; i += 32) {
           const float v = vals[i];
           const int b = (int)place_of(r, v);
           const unsigned long long w = weight_of(sh, r, v);
-          in += b >= first_bin && b <= last_bin;
           sum += w;
           if (b < first_bin) {
             above += w;
             if (w >= keep.least) kept += w;
+          } else if (b <= last_bin) {
+            take(i, v);
           }
         }
-      }
-      in = __reduce_add_sync(0xffffffffu, in);
-      sum = warp_sum(sum);
-      above = warp_sum(above);
-      kept = warp_sum(kept);
-      __syncthreads();
-      if (lane == 0) {
-        sh.warpc[warp] = in;
-        sh.hist[warp] = sum;
-        sh.hist[kWarps + warp] = above;
-        sh.warp_kept[warp] = kept;
+        sum = warp_sum(sum);
+        above = warp_sum(above);
+        kept = warp_sum(kept);
+        if (lane == 0) {
+          sh.warp[warp] = sum;
+          sh.warp_above[warp] = above;
+          sh.warp_kept[warp] = kept;
+        }
       }
       __syncthreads();
-      unsigned long long mine[3] = {0, 0, 0};
-      uint32_t off = 0;
-      for (int x = 0; x < kWarps; ++x) {
-        if (x < warp) off += sh.warpc[x];
-        mine[0] += sh.warpc[x];
-        mine[1] += sh.hist[x];
-        mine[2] += sh.hist[kWarps + x];
+      unsigned long long mine[3] = {sh.taken, 0, 0};
+      if (k == 0) {
+        for (int x = 0; x < kWarps; ++x) {
+          mine[1] += sh.warp[x];
+          mine[2] += sh.warp_above[x];
+        }
       }
       if (tid < cluster)
 #pragma unroll
         for (int e = 0; e < 3; ++e) peer_put(&sh.slot[work.turn][e][rank], tid, mine[e]);
       cluster_sync();
       unsigned long long got[3] = {0, 0, 0};
-      uint32_t before = 0;
-      for (int c = 0; c < cluster; ++c) {
-        if (c < rank) before += (uint32_t)sh.slot[work.turn][0][c];
+      for (int c = 0; c < cluster; ++c)
 #pragma unroll
         for (int e = 0; e < 3; ++e) got[e] += sh.slot[work.turn][e][c];
-      }
       work.turn ^= 1;
-      // ---- to the first CTA, in order of index
-#pragma unroll 4
-      for (int base = w0; base < w1; base += 32) {
-        const int i = base + lane;
-        const int b = i < w1 ? (int)place_of(r, vals[i]) : kCoarse;
-        const bool is = b >= first_bin && b <= last_bin;
-        const uint32_t all = __ballot_sync(0xffffffffu, is);
-        if (is && before + off + __popc(all) <= (uint32_t)kList) {
-          const uint32_t at = off + __popc(all & ((1u << lane) - 1));
-          sh.local[at] = (uint16_t)i;
-          peer_put32(&sh.list_key[before + at], 0, key_of(vals[i]));
-          peer_put32(&sh.list_at[before + at], 0, (uint32_t)(begin + i));
-        }
-        off += __popc(all);
-      }
-      cluster_sync();
       const int listed = (int)got[0];
-      const View list{nullptr, sh.list_key, sh.list_at, listed, 0, (listed + kThreads - 1) / kThreads * 32, 1, 0};
-      if (k > 0) {  // all that is left is in the list
+      const View list{nullptr, sh.list_key, sh.list_at, listed, 0, 0, 1, 0};
+      if (listed <= kList && k > 0) {  // all that is left is in the list
         if (rank != 0) return;
         settle(sh, r, list, k, top_p, 0, 0, keep.thr, keep.cut);
-        work.chunk_sums(list, kept_weight, sh.warp_kept);
-        const int token = work.locate(list, kept_weight, draw, sh.warp_kept, total, value);
-        if (tid == 0) put(token, total, value);
+        draw_sorted(sh, r, list, keep, u, put);
         return;
       }
-      if (rank == 0) {
-        const bool good = settle(sh, r, list, 0, top_p, got[1], got[2], keep.thr, keep.cut);
-        if (tid < cluster) {
-          peer_put(&sh.found[2], tid, good ? keep.thr : 0ull);
-          peer_put(&sh.found[3], tid, (unsigned long long)(uint32_t)keep.cut);
+      if (listed <= kList) {
+        if (rank == 0) {
+          const bool good = settle(sh, r, list, 0, top_p, got[1], got[2], keep.thr, keep.cut);
+          if (tid < cluster) {
+            peer_put(&sh.found[2], tid, good ? keep.thr : 0ull);
+            peer_put(&sh.found[3], tid, (unsigned long long)(uint32_t)keep.cut);
+          }
         }
-      }
-      cluster_sync();
-      if (sh.found[2] != 0) {
-        keep.thr = (uint32_t)sh.found[2];
-        keep.cut = (int)(uint32_t)sh.found[3];
-        // the band's tokens that stay join their chunks' sums
-        for (int i = tid; i < (int)mine[0]; i += kThreads) {
-          const int at = sh.local[i];
-          const unsigned long long w = kept_weight(key_of(vals[at]), begin + at);
-          if (w) atomicAdd(&sh.warp_kept[at / chunk], w);
+        cluster_sync();
+        if (sh.found[2] != 0) {
+          keep.thr = (uint32_t)sh.found[2];
+          keep.cut = (int)(uint32_t)sh.found[3];
+          // the band's tokens that stay join their chunks' sums
+          for (int i = tid; i < (int)mine[0]; i += kThreads) {
+            const int at = sh.local[i];
+            const unsigned long long w = kept_weight(key_of(vals[at]), begin + at);
+            if (w) atomicAdd(&sh.warp_kept[at / chunk], w);
+          }
+          __syncthreads();
+          const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
+          if (rank == 0 && tid == 0) put(token, total, value);
+          return;
         }
-        __syncthreads();
-        const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
-        if (rank == 0 && tid == 0) put(token, total, value);
-        return;
+        keep.thr = kLowest;
+        keep.cut = -1;
+        cluster_sync();
       }
-      keep.thr = kLowest;
-      keep.cut = -1;
-      cluster_sync();
     }
   }
   if (k > 0 || top_p < 1.f) {
