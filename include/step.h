@@ -75,7 +75,7 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *           overlap x
  * Any T; the weights are read once for every 64 tokens (every 32 to 8 where K is
  * above 6144), so a prompt's products are better served by a matrix product of
- * 16-bit weights.  K up to 81920.  The result does not depend on timing.
+ * 16-bit weights.  K up to 65536.  The result does not depend on timing.
  */
 moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_stride,
                    const float* x_scale, int x_group, const void* codes, const void* scale,

@@ -4,24 +4,31 @@
 //   y[t][o] = sum over groups of (s sum c x + b sum x)
 // so the products of a group run on the codes themselves, which are exact in 16 bits,
 // and scale and bias enter once a group in fp32:
-//   bf16:  a code with the exponent of 128 in front is 128 + c (8 significant bits), and
-//          the group's sum is s (acc - 128 X) + b X with X = sum x
+//   bf16:  a code behind the leading bit of 16 is 16 + c, and the group's sum is
+//          s acc + (b - 16 s) X with X = sum x
 //   fp16 (8-bit x too, which fp16 holds exactly):  a code's bits alone are the subnormal
 //          c 2^-24, and the group's sum is (2^24 s) acc + b X
 // An 8-bit x has its own scale applied after a 64-wide part (or at the end, where a
 // token has one).
 //
-// Bound: HBM (half a byte a weight plus four a group).  A warp has 16 rows of weights as
-// the wide side of mma.sync (m16n8k16) and 8 NT tokens as the narrow one, so that up to
-// 64 tokens share one reading.  Lane (g, j) of a warp holds rows g and g + 8 and in each
-// part of 64 weights the codes 16 j .. 16 j + 15: 8 bytes a row, four lanes a sector, which
-// the shifts turn into operands in the order 0 4 1 5 2 6 3 7; the tokens are laid out in
-// shared memory in that order once.  Loads go straight to registers, four parts ahead
-// (2.3 KB a warp), across blocks of rows, so that a CTA that walks many never drains.
+// Bound: HBM (half a byte a weight plus four a group), and few instructions a byte to
+// reach it.  A warp has 16 rows of weights as the wide side of mma.sync (m16n8k16) and
+// 8 NT tokens as the narrow one, so that up to 64 tokens share one reading.  Lane (g, j)
+// of a warp takes rows g and g + 8 and of each part of 64 weights the codes 16 j .. 16 j
+// + 15, 8 bytes a row, which shifts turn into operands in the order 0 4 1 5 2 6 3 7; the
+// tokens are laid out in shared memory in that order once.  A warp's rows come through a
+// ring of its own by 16-byte copies, four parts a stage (2.3 KB), two stages ahead and
+// across blocks of rows, so that a CTA that walks many never drains.  (The same loads
+// into registers took 123 instructions a part of 16 x 64 weights, and 70 us where this
+// takes @VOC@: 130001 x 2048 weights, 8 tokens.)
 //
 // Split: a CTA holds WR row tiles x WK slices of K (WR WK = 8 warps), and a cluster of C
 // CTAs splits K again where there are few rows or the tokens of all of K do not fit
 // shared memory; partial sums meet in shared memory, in the order of K.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
 #include "paged_internal.h"
 #include "ptx.cuh"
 #include "step_internal.h"
@@ -30,6 +37,9 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kStages = 3;
+constexpr int kPitch = 160;                   // bytes of a row of a stage: no bank conflicts
+constexpr int kStage = 16 * kPitch + 16 * 16;  // codes of 16 rows x 4 parts, scales and biases
 
 struct Plan4 {
   Linear4Params a;
@@ -38,7 +48,7 @@ struct Plan4 {
   int cta_parts, warp_parts;  // ... of a CTA's and of a warp's slice (multiples of 4)
   int blocks;           // of 16 wr rows
   int t0;               // this launch's first token
-  int off_sum, off_xs, off_red;  // shared memory: x, then sums, scales, partial results
+  int off_sum, off_xs, off_ring, off_red;  // shared memory: x, its sums and scales, the rest
   int vec;              // a row's scales can be read four at a time
 };
 
@@ -61,29 +71,44 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // codes p and p + 4 of a word of eight as a pair of operands
 template <bool BF>
 __device__ __forceinline__ uint32_t codes_of(uint32_t w, int p) {
-  const uint32_t c = (w >> (4 * p)) & 0x000f000fu;
-  return BF ? c | 0x43004300u : c;
+  if constexpr (BF) {
+    // (one operation, not an AND and an OR: the constants have to be in registers)
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(r) : "r"(p == 0 ? w << 3 : w >> (4 * p - 3)), "r"(0x00780078u), "r"(0x41804180u));
+    return r;
+  } else {
+    return (w >> (4 * p)) & 0x000f000fu;
+  }
 }
 __device__ __forceinline__ float value16(uint16_t b, bool bf) {
   return bf ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
 }
 
-// eight values of x, as 16 bits (bf16, or fp16), from element i of a row on
-__device__ __forceinline__ void load_x8(const Linear4Params& p, const void* row, int i,
-                                        uint16_t (&v)[8]) {
-  if (p.x_dtype == STEP_BF16 || p.x_dtype == STEP_F16) {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + i);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// eight values of x from element i of a row on, as they lie in memory, and as 16 bits
+// (bf16, or fp16)
+__device__ __forceinline__ uint4 raw_x8(const Linear4Params& p, long long i) {
+  if (p.x_dtype <= STEP_F16)
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + i));
+  const uint2 a = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) + i));
+  return make_uint4(a.x, a.y, 0, 0);
+}
+__device__ __forceinline__ void unpack_x8(int dtype, uint4 a, uint16_t (&v)[8]) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+  if (dtype <= STEP_F16) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
   } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(row) + i);
-    const uint32_t u[2] = {a.x, a.y};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint8_t b = (uint8_t)(u[e / 4] >> (8 * (e & 3)));
-      v[e] = p.x_dtype == STEP_E4M3 ? __nv_cvt_fp8_to_halfraw(b, __NV_E4M3).x
-                                    : __half_as_ushort(__int2half_rn((int8_t)b));
+    for (int e = 0; e < 8; e += 2) {
+      const uint16_t b = (uint16_t)(u[e / 4] >> (8 * (e & 3)));
+      if (dtype == STEP_E4M3) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
+        v[e] = h.x, v[e + 1] = h.y;
+      } else {
+        v[e] = __half_as_ushort(__int2half_rn((int8_t)b));
+        v[e + 1] = __half_as_ushort(__int2half_rn((int8_t)(b >> 8)));
+      }
     }
   }
 }
@@ -112,82 +137,116 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
   const int quads = (mine + 3) / 4;
   const int rows = 16 * q.wr;
 
-  // ---- what is ahead: four parts of 64 codes of two rows, their scales and biases
-  struct Quad {
-    uint2 c[4][2];
-    uint2 s[2], b[2];
-  };
+  // ---- the ring: stage i of a warp's sequence (blocks of rows, of each its quads of parts)
+  uint8_t* const ring = smem + q.off_ring + warp * kStages * kStage;
+  const uint32_t ring_at = smem_u32(ring);
   const long long code_pitch = p.K / 2;
   const int sgroups = p.K / p.group, per = p.group / 64;  // scales of a row; parts of a scale
-  auto fetch = [&](int block, int quad, Quad& f) {
-    const int o0 = block * rows + wr * 16 + g;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int o = min(o0 + 8 * h, p.O - 1);
-      const int at = part0 + my0 + quad * 4;
-      const uint8_t* src = p.codes + o * code_pitch + (long long)at * 32 + j * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (quad * 4 + i < mine) f.c[i][h] = __ldg(reinterpret_cast<const uint2*>(src + i * 32));
-      const long long so = (long long)o * sgroups;
-      if (q.vec) {
-        f.s[h] = __ldg(reinterpret_cast<const uint2*>(p.scale + so + at));
-        f.b[h] = __ldg(reinterpret_cast<const uint2*>(p.bias + so + at));
-      } else {
-        uint32_t s[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+  int fb = first, fq = 0;  // the next block and quad to copy
+  // A lane copies 16 bytes of rows lane / 8, + 4, + 8 and + 12 of a stage, and the four
+  // scales or biases of row lane / 2: from these addresses on, which move with the quads.
+  const uint8_t* code_src = nullptr;
+  const uint16_t* scale_src = nullptr;
+  const int code_dst = (lane >> 3) * kPitch + (lane & 7) * 16;
+  const int part_first = part0 + my0;
+  int row_left = 0;  // rows of the block behind this lane's first
+  auto enter = [&]() {
+    const int o0 = fb * rows + wr * 16;
+    row_left = p.O - o0 - (lane >> 3);
+    code_src = p.codes + (o0 + (lane >> 3)) * code_pitch + (long long)part_first * 32 + (lane & 7) * 16;
+    scale_src = (lane & 1 ? p.bias : p.scale) + (long long)min(o0 + (lane >> 1), p.O - 1) * sgroups;
+    if (q.vec) scale_src += part_first;
+  };
+  enter();
+  uint2 pending = make_uint2(0, 0);  // scales whose rows are not 8-byte aligned come by way of
+  int pending_at = -1;               // registers, a stage later
+  auto fetch = [&](int slot) {
+    if (!q.vec && pending_at >= 0) {
+      *reinterpret_cast<uint2*>(ring + pending_at + lane * 8) = pending;
+      pending_at = -1;
+    }
+    if (fb < q.blocks && quads > 0) {
+      const uint32_t dst = ring_at + slot * kStage;
+      const int left = (mine - fq * 4) * 2;  // 16-byte pieces of a row
+      if (left >= 8 && row_left > 12) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (quad * 4 + i < mine) {
-            const int at_s = (at + i) / per;
-            s[i] = __ldg(p.scale + so + at_s);
-            b[i] = __ldg(p.bias + so + at_s);
-          }
-        f.s[h] = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
-        f.b[h] = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+          cp_async16(dst + code_dst + i * 4 * kPitch, code_src + i * 4 * code_pitch, 16u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool is = row_left > 4 * i && (lane & 7) < left;
+          cp_async16(dst + code_dst + i * 4 * kPitch, is ? code_src + i * 4 * code_pitch : p.codes,
+                     is ? 16u : 0u);
+        }
+      }
+      code_src += 128;
+      if (q.vec) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + 16 * kPitch + lane * 8),
+                     "l"(scale_src) : "memory");
+        scale_src += 4;
+      } else {
+        uint32_t v[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (2 * i < left) v[i] = __ldg(scale_src + (part_first + fq * 4 + i) / per);
+        pending = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        pending_at = slot * kStage + 16 * kPitch;
+      }
+      if (++fq == quads) {
+        fq = 0;
+        fb += stride;
+        enter();
       }
     }
+    cp_async_commit();
   };
-  int fb = first, fq = 0;  // the next quad to fetch
-  Quad ring[2];
-  auto next = [&](Quad& f) {
-    if (fb >= q.blocks || quads == 0) return;
-    fetch(fb, fq, f);
-    if (++fq == quads) {
-      fq = 0;
-      fb += stride;
-    }
-  };
-  next(ring[0]);
-  next(ring[1]);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
   // ---- the tokens' values of this CTA's slice, in the products' order
-  for (int i = threadIdx.x; i < cta_parts * 8 * TB; i += 32 * kWarps) {
-    // eight values: e8-th of a part's eight (j = e8 / 2, half = e8 & 1)
-    const int e8 = i & 7, t = (i >> 3) % TB, part = (i >> 3) / TB;
-    uint16_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (t < tokens) {
-      const long long o = (long long)(q.t0 + t) * p.x_ts;
-      const int es = p.x_dtype <= STEP_F16 ? 2 : 1;
-      load_x8(p, static_cast<const uint8_t*>(p.x) + o * es, (part0 + part) * 64 + e8 * 8, v);
-    }
-    float sum = 0.f;
+  // (eight loads of a thread in flight; eight values a step: the e8-th eight of a part of
+  // token t, which lane j = e8 / 2 of the products takes)
+  constexpr int AHEAD = 8;
+  const int items = cta_parts * 8 * TB;
+  for (int base = threadIdx.x; base < items; base += AHEAD * 32 * kWarps) {
+    uint4 raw[AHEAD];
+    float z[AHEAD];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += value16(v[e], BF);
-    // (the eight threads of a part of a token are lanes of one warp)
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-    uint4 u;
-    u.x = v[0] | (uint32_t)v[4] << 16;
-    u.y = v[1] | (uint32_t)v[5] << 16;
-    u.z = v[2] | (uint32_t)v[6] << 16;
-    u.w = v[3] | (uint32_t)v[7] << 16;
-    *reinterpret_cast<uint4*>(sx + ((((part * 2 + (e8 & 1)) * TB + t) * 4 + (e8 >> 1)) << 3)) = u;
-    if (e8 == 0) {
-      ssum[part * TB + t] = sum;
-      if (XS)
-        sxs[part * TB + t] =
-            t < tokens ? p.xs[(long long)(q.t0 + t) * (p.K / p.xg) + (part0 + part) * 64 / p.xg] : 0.f;
+    for (int a = 0; a < AHEAD; ++a) {
+      const int i = base + a * 32 * kWarps;
+      const int e8 = i & 7, t = (i >> 3) % TB, part = part0 + (i >> 3) / TB;
+      raw[a] = make_uint4(0, 0, 0, 0);
+      z[a] = 0.f;
+      if (i < items && t < tokens) {
+        raw[a] = raw_x8(p, (q.t0 + t) * p.x_ts + part * 64 + e8 * 8);
+        if (XS && e8 == 0) z[a] = __ldg(p.xs + (long long)(q.t0 + t) * (p.K / p.xg) + part * 64 / p.xg);
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) {
+      const int i = base + a * 32 * kWarps;
+      if (i >= items) break;  // (the same for a warp: items are a multiple of 64)
+      const int e8 = i & 7, t = (i >> 3) % TB, part = (i >> 3) / TB;
+      uint16_t v[8];
+      unpack_x8(p.x_dtype, raw[a], v);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += value16(v[e], BF);
+      // (the eight threads of a part of a token are lanes of one warp)
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      uint4 u;
+      u.x = v[0] | (uint32_t)v[4] << 16;
+      u.y = v[1] | (uint32_t)v[5] << 16;
+      u.z = v[2] | (uint32_t)v[6] << 16;
+      u.w = v[3] | (uint32_t)v[7] << 16;
+      *reinterpret_cast<uint4*>(sx + ((((part * 2 + (e8 & 1)) * TB + t) * 4 + (e8 >> 1)) << 3)) = u;
+      if (e8 == 0) {
+        ssum[part * TB + t] = sum;
+        if (XS) sxs[part * TB + t] = z[a];
+      }
     }
   }
   __syncthreads();
@@ -199,11 +258,48 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
 #pragma unroll
     for (int e = 0; e < 4; ++e) tot[n][e] = 0.f;
 
-  auto compute = [&](const Quad& f, int quad) {
+  // A stage's four parts (`left` of them, FULL: all) from part `quad * 4` of the slice on.
+  // This lane's operands lie at fixed distances from three addresses.
+  const uint8_t* const x_lane = smem + (g * 4 + j) * 16;
+  const float* const sum_lane = ssum + 2 * j;
+  const float* const xs_lane = sxs + 2 * j;
+  const int code_lane = g * kPitch + j * 8;
+  auto compute = [&](const uint8_t* st, int quad, int left, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const int part0 = my0 + quad * 4;
+    const uint8_t* const xq = x_lane + part0 * (TB * 128);
+    const float* const sq = sum_lane + part0 * TB;
+    [[maybe_unused]] const float* const zq = xs_lane + part0 * TB;
+    float s[4][2], b[4][2];  // of rows g and g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = *reinterpret_cast<const uint4*>(st + 16 * kPitch + (g + 8 * h) * 16);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      if (bf_scale) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i][h] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+          b[i][h] = __uint_as_float(i & 1 ? u[2 + i / 2] & 0xffff0000u : u[2 + i / 2] << 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i / 2]));
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[2 + i / 2]));
+          s[i][h] = x.x, s[i + 1][h] = x.y, b[i][h] = y.x, b[i + 1][h] = y.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (BF) b[i][h] = fmaf(-16.f, s[i][h], b[i][h]);
+        else s[i][h] *= 16777216.f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int part = my0 + quad * 4 + i;
-      if (quad * 4 + i >= mine) break;
+      if (!FULL && i >= left) break;
+      const uint2 c0 = *reinterpret_cast<const uint2*>(st + code_lane + i * 32);
+      const uint2 c1 = *reinterpret_cast<const uint2*>(st + code_lane + 8 * kPitch + i * 32);
       float acc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -211,7 +307,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint32_t w0 = half ? f.c[i][0].y : f.c[i][0].x, w1 = half ? f.c[i][1].y : f.c[i][1].x;
+        const uint32_t w0 = half ? c0.y : c0.x, w1 = half ? c1.y : c1.x;
         uint32_t a[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -222,34 +318,24 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 b = *reinterpret_cast<const uint4*>(
-              sx + ((((part * 2 + half) * TB + n * 8 + g) * 4 + j) << 3));
-          mma16816<BF>(acc[n], a[0], b.x, b.y);
-          mma16816<BF>(acc[n], a[1], b.z, b.w);
+          const uint4 x = *reinterpret_cast<const uint4*>(xq + (i * 2 + half) * (TB * 64) + n * 512);
+          mma16816<BF>(acc[n], a[0], x.x, x.y);
+          mma16816<BF>(acc[n], a[1], x.z, x.w);
         }
-      }
-      float s[2], b[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t sw = i < 2 ? f.s[h].x : f.s[h].y, bw = i < 2 ? f.b[h].x : f.b[h].y;
-        s[h] = value16((uint16_t)(sw >> (16 * (i & 1))), bf_scale);
-        b[h] = value16((uint16_t)(bw >> (16 * (i & 1))), bf_scale);
-        if (BF) b[h] = fmaf(-128.f, s[h], b[h]);
-        else s[h] *= 16777216.f;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float2 x = *reinterpret_cast<const float2*>(ssum + part * TB + n * 8 + 2 * j);
+        const float2 x = *reinterpret_cast<const float2*>(sq + i * TB + n * 8);
         if constexpr (XS) {
-          const float2 z = *reinterpret_cast<const float2*>(sxs + part * TB + n * 8 + 2 * j);
+          const float2 z = *reinterpret_cast<const float2*>(zq + i * TB + n * 8);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            tot[n][e] = fmaf(e & 1 ? z.y : z.x, fmaf(s[e >> 1], acc[n][e], b[e >> 1] * (e & 1 ? x.y : x.x)),
-                             tot[n][e]);
+            tot[n][e] = fmaf(e & 1 ? z.y : z.x,
+                             fmaf(s[i][e >> 1], acc[n][e], b[i][e >> 1] * (e & 1 ? x.y : x.x)), tot[n][e]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            tot[n][e] = fmaf(s[e >> 1], acc[n][e], fmaf(b[e >> 1], e & 1 ? x.y : x.x, tot[n][e]));
+            tot[n][e] = fmaf(s[i][e >> 1], acc[n][e], fmaf(b[i][e >> 1], e & 1 ? x.y : x.x, tot[n][e]));
         }
       }
     }
@@ -264,23 +350,20 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
     else static_cast<float*>(p.y)[at] = v;
   };
 
-  int buf = 0;
+  int slot = 0;
   for (int block = first; block < q.blocks; block += stride) {
-    for (int quad = 0; quad < quads; quad += 2) {
-      compute(ring[0], quad);
-      next(ring[0]);
-      if (quad + 1 < quads) {
-        compute(ring[1], quad + 1);
-        next(ring[1]);
-      } else {  // an odd number of quads: the other one comes first in the next block
-        const Quad x = ring[0];
-        ring[0] = ring[1];
-        ring[1] = x;
-      }
+    for (int quad = 0; quad < quads; ++quad) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // the stage is there for all lanes, and the one before has been read
+      fetch(slot == 0 ? kStages - 1 : slot - 1);
+      const int left = mine - quad * 4;
+      if (left >= 4) compute(ring + slot * kStage, quad, 4, std::true_type{});
+      else compute(ring + slot * kStage, quad, left, std::false_type{});
+      if (++slot == kStages) slot = 0;
     }
     // partial results of a warp: [token][row], rows of 16 and padding of 4 floats
     constexpr int PITCH = 20;
-    float* out = red + ((ALONE ? 0 : buf) * kWarps + warp) * TB * PITCH;
+    float* out = red + warp * TB * PITCH;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -300,30 +383,47 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
       } else {
         __syncthreads();
       }
-      // this CTA's share: every cluster-th group of 16 rows x tokens
-      const uint32_t at0 = smem_u32(red) + (uint32_t)(buf * kWarps * TB * PITCH) * 4;
-      const int items = q.wr * tokens * 16;
-      for (int i = rank * 32 * kWarps + threadIdx.x; i < items; i += q.cluster * 32 * kWarps) {
-        const int r = i & 15, tile = (i >> 4) % q.wr, t = (i >> 4) / q.wr;
-        const int o = block * rows + tile * 16 + r;
-        float v = 0.f;
-        for (int c = 0; c < q.cluster; ++c) {
-          const uint32_t base = q.cluster > 1 ? mapa_shared(at0, c) : at0;
-          for (int k = 0; k < q.wk; ++k) {
-            float x;
-            const uint32_t a = base + (uint32_t)(((tile * q.wk + k) * TB + t) * PITCH + r) * 4;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
-            v += x;
+      // this CTA's share: the tokens rank, rank + C, ...; a thread a row
+      const uint32_t at0 = smem_u32(red);
+      const int r = threadIdx.x % rows, o = block * rows + r, tile = r >> 4;
+      if (o < p.O) {
+        for (int t = rank + threadIdx.x / rows * q.cluster; t < tokens; t += 32 * kWarps / rows * q.cluster) {
+          float v = 0.f;
+          const uint32_t a0 = at0 + (uint32_t)((tile * q.wk * TB + t) * PITCH + (r & 15)) * 4;
+          if (q.cluster == 1) {
+            float x[kWarps];
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k)
+              x[k] = k < q.wk ? __uint_as_float(ld_shared_u32(a0 + k * (TB * PITCH * 4))) : 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) v += x[k];
+          } else {
+            for (int k = 0; k < q.wk; ++k) {
+              float x[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                x[c] = 0.f;
+                if (c < q.cluster)
+                  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                               : "=f"(x[c]) : "r"(mapa_shared(a0 + k * (TB * PITCH * 4), c)) : "memory");
+              }
+#pragma unroll
+              for (int c = 0; c < 8; ++c) v += x[c];
+            }
           }
+          put(t, o, v);
         }
-        if (o < p.O) put(t, o, v);
       }
-      buf ^= 1;  // (the next block's results go to the other buffer, the one after waits above)
+      // before the next block's results; no CTA of a cluster leaves while another may read
+      // its shared memory
+      if (q.cluster > 1) {
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+      } else {
+        __syncthreads();
+      }
     }
   }
-  // no CTA of a cluster leaves while another may read its shared memory
-  if (!ALONE && q.cluster > 1)
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  cp_async_wait<0>();
 }
 
 template <int NT, bool BF, bool XS, bool ALONE>
@@ -363,24 +463,40 @@ cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st) {
   Plan4 q{};
   q.a = p;
   q.parts = p.K / 64;
+  constexpr int kRing = kWarps * kStages * kStage;
+  constexpr int kRoom = 220 * 1024 - kRing;  // for the tokens and the partial results
+  auto x_bytes = [](int parts, int nt) { return (long long)parts * 8 * nt * (128 + 8); };
+  auto red_bytes = [](int nt) { return kWarps * 8 * nt * 20 * 4; };
+  auto slice = [&](int c) { return round4((q.parts + c - 1) / c); };
   // tokens of a launch: as many as shared memory holds beside an eighth of K
-  constexpr int kRoom = 200 * 1024;
   int nt = 8;
   while (nt > 1 && 8 * (nt / 2) >= p.T) nt /= 2;
   if (nt == 8 && p.T <= 48) nt = 6;
-  auto per_part = [](int nt) { return 8 * nt * (128 + 8); };
-  auto red_bytes = [](int nt, bool alone) { return (alone ? 1 : 2) * kWarps * 8 * nt * 20 * 4; };
-  while (nt > 1 && (long long)round4((q.parts + 7) / 8) * per_part(nt) + red_bytes(nt, false) > kRoom)
-    nt = nt == 6 ? 4 : nt / 2;
+  while (nt > 1 && x_bytes(slice(8), nt) + red_bytes(nt) > kRoom) nt = nt == 6 ? 4 : nt / 2;
   const int tiles = (p.O + 15) / 16;
-  // CTAs of a cluster: while the slice of K does not fit, or there are fewer row tiles
-  // than two warps of every SM would take and a warp has more than four parts
-  q.cluster = 1;
-  auto slice = [&](int c) { return round4((q.parts + c - 1) / c); };
-  while (q.cluster < 8 && (long long)slice(q.cluster) * per_part(nt) + red_bytes(nt, false) > kRoom) q.cluster *= 2;
-  // slices of K in a CTA: until there are four warps for every SM's scheduler
-  q.wk = 1;
-  while (q.wk < 8 && (long long)tiles * q.wk * q.cluster < 16ll * sms && slice(q.cluster) / q.wk > 4) q.wk *= 2;
+  // The split with the least rounds x (parts of a warp + what a block costs besides, as
+  // much as 6 parts), and, where there are few blocks, the tokens' layout, which every CTA
+  // does anew (@LAYOUT@).
+  double best = 1e30;
+  for (int c = 1; c <= 8; c *= 2) {
+    if (x_bytes(slice(c), nt) + red_bytes(nt) > kRoom || (c > 1 && slice(c / 2) <= 4)) continue;
+    for (int wk = 1; wk <= kWarps; wk *= 2) {
+      if (wk > 1 && slice(c) <= 4 * wk / 2) continue;
+      const int blocks = (tiles + kWarps / wk - 1) / (kWarps / wk);
+      const int smem = (int)x_bytes(slice(c), nt) + kRing + red_bytes(nt);
+      const int per_sm = std::max(1, std::min(nt <= 4 ? 2 : 1, 227 * 1024 / (smem + 1024)));
+      // (clusters leave some SMs without a CTA)
+      const double slots = sms * per_sm / c * (c == 8 ? 0.8 : c == 4 ? 0.9 : 1.0);
+      const double rounds = std::ceil(blocks / std::max(slots, 1.0));
+      const double cost = rounds * (round4((slice(c) + wk - 1) / wk) * (1 + 0.25 * nt) + 6 + (c > 1 ? 8 : 0)) +
+                          slice(c) * nt * 0.5;
+      if (cost < best) {
+        best = cost;
+        q.cluster = c;
+        q.wk = wk;
+      }
+    }
+  }
   q.wr = kWarps / q.wk;
   q.cta_parts = slice(q.cluster);
   q.warp_parts = round4((q.cta_parts + q.wk - 1) / q.wk);
@@ -388,13 +504,12 @@ cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st) {
   q.vec = p.group == 64 && q.parts % 4 == 0;
   q.off_sum = q.cta_parts * 8 * nt * 128;
   q.off_xs = q.off_sum + q.cta_parts * 8 * nt * 4;
-  q.off_red = q.off_xs + q.cta_parts * 8 * nt * 4;
-  const int smem = q.off_red + red_bytes(nt, q.wk == 1 && q.cluster == 1);
+  q.off_ring = q.off_xs + q.cta_parts * 8 * nt * 4;
+  q.off_red = q.off_ring + kRing;
+  const int smem = q.off_red + red_bytes(nt);
   const int per_sm = std::max(1, std::min(nt <= 4 ? 2 : 1, 227 * 1024 / (smem + 1024)));
   const int most = std::max(1, sms * per_sm / q.cluster);
-  // (blocks evenly: no more CTAs than the rounds need)
-  const int rounds = (q.blocks + most - 1) / most;
-  const int grid = (q.blocks + rounds - 1) / rounds * q.cluster;
+  const int grid = std::min(q.blocks, most) * q.cluster;
   for (q.t0 = 0; q.t0 < p.T; q.t0 += 8 * nt) {
     cudaError_t e = cudaSuccess;
     switch (nt) {

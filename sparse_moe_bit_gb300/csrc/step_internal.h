@@ -37,7 +37,7 @@ struct Linear4Params {
   int x_dtype, y_dtype, bf_scale;
   int T, K, O, group, xg;
 };
-constexpr int kLinear4MaxK = 81920;
+constexpr int kLinear4MaxK = 65536;
 cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st);
 
 // ---- sampling (sample.cu)
