@@ -25,35 +25,50 @@ struct Io<__nv_bfloat16> {
   static __device__ __forceinline__ uint16_t put(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 template <>
 struct Io<__half> {
   static __device__ __forceinline__ float get(uint16_t b) { return __half2float(__ushort_as_half(b)); }
   static __device__ __forceinline__ uint16_t put(float v) { return __half_as_ushort(__float2half_rn(v)); }
+  static __device__ __forceinline__ uint32_t put2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 
-// VEC values of a row from feature i on, as fp32
+// VEC values of a row from feature i on: as they lie in memory, and as fp32
 template <typename T, int VEC>
-__device__ __forceinline__ void load_row(const void* base, long long i, float (&v)[VEC]) {
-  if constexpr (sizeof(T) == 4) {
-    const float* p = static_cast<const float*>(base) + i;
-    if constexpr (VEC == 8) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+struct Raw {
+  static constexpr int N = VEC == 1 ? 1 : VEC * (int)sizeof(T) / 4;
+  uint32_t u[N];
+  __device__ __forceinline__ void load(const void* base, long long i) {
+    const T* p = static_cast<const T*>(base) + i;
+    if constexpr (VEC == 1) {
+      if constexpr (sizeof(T) == 4) u[0] = *reinterpret_cast<const uint32_t*>(p);
+      else u[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
-      v[0] = *p;
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + i;
-    if constexpr (VEC == 8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = Io<T>::get((uint16_t)(u[e / 2] >> (16 * (e & 1))));
-    } else {
-      v[0] = Io<T>::get(*p);
+      for (int k = 0; k < N; k += 4) {
+        const uint4 a = reinterpret_cast<const uint4*>(p)[k / 4];
+        u[k] = a.x, u[k + 1] = a.y, u[k + 2] = a.z, u[k + 3] = a.w;
+      }
     }
   }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[e]);
+    else return Io<T>::get((uint16_t)(VEC == 1 ? u[0] : u[e / 2] >> (16 * (e & 1))));
+  }
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void load_row(const void* base, long long i, float (&v)[VEC]) {
+  Raw<T, VEC> r;
+  r.load(base, i);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = r[e];
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(void* base, long long i, const float (&v)[VEC]) {
@@ -70,19 +85,28 @@ __device__ __forceinline__ void store_row(void* base, long long i, const float (
     if constexpr (VEC == 8) {
       uint32_t u[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = Io<T>::put(v[2 * e]) | (uint32_t)Io<T>::put(v[2 * e + 1]) << 16;
+      for (int e = 0; e < 4; ++e) u[e] = Io<T>::put2(v[2 * e], v[2 * e + 1]);
       *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
       *p = Io<T>::put(v[0]);
     }
   }
 }
-// n / scale in 8 bits (0 where the scale is); NaN stays NaN in e4m3 and is 0 in int8,
-// whose scale says it
-__device__ __forceinline__ uint8_t put8(float n, float scale, bool e4m3) {
-  const float q = scale == 0.f ? 0.f : n / scale;
-  if (e4m3) return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-  return (uint8_t)(int8_t)min(max(__float2int_rn(q), -127), 127);
+// Eight bits: n / scale as a product with the scale's reciprocal, one division a group.
+// (`pre` keeps the reciprocal of a tiny scale in fp32's range.)  NaN stays NaN in e4m3 and
+// is 0 in int8, whose scale says it.
+struct Scaler {
+  float pre, inv;
+  __device__ explicit Scaler(float scale) {
+    pre = scale < 1e-30f ? 0x1p64f : 1.f;
+    inv = scale == 0.f ? 0.f : 1.f / (scale * pre);
+  }
+  __device__ __forceinline__ float operator()(float n) const { return n * pre * inv; }
+};
+__device__ __forceinline__ uint32_t put8x2(float a, float b, bool e4m3) {
+  if (e4m3) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const int x = min(max(__float2int_rn(a), -127), 127), y = min(max(__float2int_rn(b), -127), 127);
+  return (x & 0xff) | (y & 0xff) << 8;
 }
 
 // The sum (or the largest value) over the W warps of a row, in every thread.
@@ -109,57 +133,14 @@ template <typename T, int VEC, int W, int CH, bool Q>
 __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
     norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int ROWS = W == 1 ? kRowsCta : 1, THREADS = 32 * W;
-  __shared__ float sh_sum[W];
+  __shared__ float sh_sum[2][W];  // by turns
   extern __shared__ uint32_t row_max[];  // [ROWS][groups]
   const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x, slot = W == 1 ? threadIdx.x >> 5 : 0;
-  const long long row = (long long)blockIdx.x * ROWS + slot;
-  if (W == 1 && row >= (long long)p.T * p.H) return;
-  const int t = (int)(row / p.H), h = (int)(row - (long long)t * p.H);
-  const long long xo = t * p.x_ts + h * p.x_hs, yo = t * p.y_ts + h * p.y_hs;
-  const int d = p.d;
-  float v[CH][VEC];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (c * THREADS + tid) * VEC;
-    if (i < d) {
-      load_row<T, VEC>(p.x, xo + i, v[c]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[c][e] = 0.f;
-    }
-  }
-  if (p.r) {
-    const long long ro = t * p.r_ts + h * p.r_hs, so = t * p.s_ts + h * p.s_hs;
-    float r[CH][VEC];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * THREADS + tid) * VEC;
-      if (i < d) load_row<T, VEC>(p.r, ro + i, r[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * THREADS + tid) * VEC;
-      if (i >= d) continue;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[c][e] += r[c][e];
-      store_row<T, VEC>(p.sum, so + i, v[c]);
-    }
-  }
-  float sq = 0.f;
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) sq = fmaf(v[c][e], v[c][e], sq);
-  // (the sum's barrier also puts every read of the row ahead of the first write of y,
-  // which may be x)
-  sq = row_sum<W>(sq, sh_sum);
-  const float inv = rsqrtf(sq / (float)d + p.eps);
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (c * THREADS + tid) * VEC;
-    if (i >= d) continue;
-    float w[VEC];
-    if (!p.w) {
+  const int d = p.d, rows = p.T * p.H;
+  // The weights stay in registers over a CTA's rows where they are few.
+  constexpr bool HOLD = CH * VEC <= 16;
+  auto weights = [&](int i, float (&w)[VEC]) {
+    if (!p.w || i >= d) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) w[e] = 1.f;
     } else if (p.w_dtype == STEP_F32) {
@@ -168,69 +149,159 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
       load_row<T, VEC>(p.w, i, w);
     }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[c][e] = v[c][e] * inv * (w[e] + p.offset);
+    for (int e = 0; e < VEC; ++e) w[e] += p.offset;
+  };
+  float hold[HOLD ? CH : 1][VEC];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) weights((c * THREADS + tid) * VEC, hold[c]);
   }
-  if constexpr (!Q) {
+  int turn = 0;
+#pragma unroll 1
+  for (int row = blockIdx.x * ROWS + slot; row < rows; row += gridDim.x * ROWS) {
+    const int t = fast_div(row, p.div_h), h = row - t * p.H;
+    const long long xo = t * p.x_ts + h * p.x_hs, yo = t * p.y_ts + h * p.y_hs;
+    // (a row's loads are all in flight before the first is waited for)
+    Raw<T, VEC> x[CH];
+    float v[CH][VEC];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * THREADS + tid) * VEC;
-      if (i >= d) continue;
-      if (p.y_dtype == STEP_BF16) store_row<__nv_bfloat16, VEC>(p.y, yo + i, v[c]);
-      else if (p.y_dtype == STEP_F16) store_row<__half, VEC>(p.y, yo + i, v[c]);
-      else store_row<float, VEC>(p.y, yo + i, v[c]);
+#pragma unroll
+      for (int k = 0; k < x[c].N; ++k) x[c].u[k] = 0;
+      if (i < d) x[c].load(p.x, xo + i);
     }
-  } else {
-    const int groups = d / p.group;
-    uint32_t* mx = row_max + slot * groups;
-    for (int g = tid; g < groups; g += THREADS) mx[g] = 0;
-    if (W == 1) __syncwarp(); else __syncthreads();
-    // Lanes of a group meet in shuffles first where a power of two of them holds it.
-    const int lanes = p.group / VEC;
-    const bool even = p.group % VEC == 0 && ((lanes & (lanes - 1)) == 0 || lanes % 32 == 0);
-    const int width = min(lanes & -lanes, 32);
+    if (p.r) {
+      const long long ro = t * p.r_ts + h * p.r_hs, so = t * p.s_ts + h * p.s_hs;
+      Raw<T, VEC> r[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * THREADS + tid) * VEC;
+#pragma unroll
+        for (int k = 0; k < r[c].N; ++k) r[c].u[k] = 0;
+        if (i < d) r[c].load(p.r, ro + i);
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * THREADS + tid) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[c][e] = x[c][e] + r[c][e];
+        if (i < d) store_row<T, VEC>(p.sum, so + i, v[c]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[c][e] = x[c][e];
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sq = fmaf(v[c][e], v[c][e], sq);
+    // (the sum's barrier also puts every read of the row ahead of the first write of y,
+    // which may be x)
+    sq = row_sum<W>(sq, sh_sum[turn]);
+    turn ^= 1;
+    const float inv = rsqrtf(sq * p.inv_d + p.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = (c * THREADS + tid) * VEC;
-      if (even) {
+      float w[VEC];
+      if constexpr (!HOLD) weights((c * THREADS + tid) * VEC, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[c][e] = v[c][e] * inv * (HOLD ? hold[c][e] : w[e]);
+    }
+    if constexpr (!Q) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * THREADS + tid) * VEC;
+        if (i >= d) continue;
+        if (p.y_dtype == STEP_BF16) store_row<__nv_bfloat16, VEC>(p.y, yo + i, v[c]);
+        else if (p.y_dtype == STEP_F16) store_row<__half, VEC>(p.y, yo + i, v[c]);
+        else store_row<float, VEC>(p.y, yo + i, v[c]);
+      }
+    } else {
+      const int groups = d / p.group;
+      const bool e4m3 = p.y_dtype == STEP_E4M3;
+      const float top = e4m3 ? 448.f : 127.f;
+      float* const scales = p.scales + (long long)row * groups;
+      auto put = [&](const float (&z)[VEC], int i) {
+        uint8_t* dst = static_cast<uint8_t*>(p.y) + yo + i;
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(put8x2(z[0], z[1], e4m3) | put8x2(z[2], z[3], e4m3) << 16,
+                         put8x2(z[4], z[5], e4m3) | put8x2(z[6], z[7], e4m3) << 16);
+        else *dst = (uint8_t)put8x2(z[0], 0.f, e4m3);
+      };
+      // A group that a power of two of a warp's lanes hold: its maximum by shuffles alone.
+      const int lanes = p.group % VEC ? 0 : p.group / VEC;
+      if (lanes > 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int i = (c * THREADS + tid) * VEC;
+          uint32_t m = 0;
+          if (i < d) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) m = max(m, __float_as_uint(v[c][e]) & 0x7fffffffu);
+          }
+          for (int s = lanes / 2; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+          if (i >= d) continue;
+          const float scale = __uint_as_float(m) / top;
+          if ((tid & (lanes - 1)) == 0) scales[fast_div(i, p.div)] = scale;
+          const Scaler s(scale);
+          float z[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) z[e] = s(v[c][e]);
+          put(z, i);
+        }
+        continue;
+      }
+      uint32_t* mx = row_max + slot * groups;
+      for (int g = tid; g < groups; g += THREADS) mx[g] = 0;
+      if (W == 1) __syncwarp(); else __syncthreads();
+      const bool even = lanes > 0 && lanes % 32 == 0;  // a warp's lanes of a chunk in one group
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * THREADS + tid) * VEC;
         uint32_t m = 0;
-        if (i < d) {
+        if (i < d && lanes > 0) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) m = max(m, __float_as_uint(v[c][e]) & 0x7fffffffu);
         }
-        for (int s = width / 2; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-        if (i < d && (tid & (width - 1)) == 0) atomicMax(mx + i / p.group, m);
-      } else if (i < d) {
+        // (by shuffles: with a warp-wide reduction instruction here the first lane's own value
+        // was missing from its result)
+        if (even) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          atomicMax(mx + (i + e) / p.group, __float_as_uint(v[c][e]) & 0x7fffffffu);
-      }
-    }
-    if (W == 1) __syncwarp(); else __syncthreads();
-    const bool e4m3 = p.y_dtype == STEP_E4M3;
-    const float top = e4m3 ? 448.f : 127.f;
-    for (int g = tid; g < groups; g += THREADS)
-      p.scales[row * groups + g] = __uint_as_float(mx[g]) / top;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (c * THREADS + tid) * VEC;
-      if (i >= d) continue;
-      uint8_t* dst = static_cast<uint8_t*>(p.y) + yo + i;
-      if constexpr (VEC == 8) {
-        uint32_t q[2] = {0, 0};
-        if (p.group % VEC == 0) {
-          const float s = __uint_as_float(mx[i / p.group]) / top;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) q[e / 4] |= (uint32_t)put8(v[c][e], s, e4m3) << (8 * (e & 3));
+          for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        }
+        if (i >= d) continue;
+        if (lanes > 0) {
+          if (!even || (tid & 31) == 0) atomicMax(mx + fast_div(i, p.div), m);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
-            q[e / 4] |= (uint32_t)put8(v[c][e], __uint_as_float(mx[(i + e) / p.group]) / top, e4m3)
-                        << (8 * (e & 3));
+            atomicMax(mx + fast_div(i + e, p.div), __float_as_uint(v[c][e]) & 0x7fffffffu);
         }
-        *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
-      } else {
-        *dst = put8(v[c][0], __uint_as_float(mx[i / p.group]) / top, e4m3);
       }
+      if (W == 1) __syncwarp(); else __syncthreads();
+      for (int g = tid; g < groups; g += THREADS) scales[g] = __uint_as_float(mx[g]) / top;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int i = (c * THREADS + tid) * VEC;
+        if (i >= d) continue;
+        float z[VEC];
+        if (lanes > 0) {
+          const Scaler s(__uint_as_float(mx[fast_div(i, p.div)]) / top);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) z[e] = s(v[c][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            z[e] = Scaler(__uint_as_float(mx[fast_div(i + e, p.div)]) / top)(v[c][e]);
+        }
+        put(z, i);
+      }
+      if (W == 1) __syncwarp(); else __syncthreads();  // before the next row's maxima
     }
   }
 }
@@ -239,7 +310,10 @@ template <typename T, int VEC, int W, int CH>
 cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
   constexpr int ROWS = W == 1 ? kRowsCta : 1;
   const long long rows = (long long)p.T * p.H;
-  const dim3 grid((unsigned)((rows + ROWS - 1) / ROWS)), block(W == 1 ? 32 * ROWS : 32 * W);
+  // as many CTAs as run at once (64 warps an SM, fewer where a thread holds more), each
+  // with its share of the rows
+  const long long most = (long long)device_sms() * std::max(1, (CH * VEC <= 16 ? 48 : 32) / (W == 1 ? ROWS : W));
+  const dim3 grid((unsigned)std::min((rows + ROWS - 1) / ROWS, most)), block(W == 1 ? 32 * ROWS : 32 * W);
   if (p.y_dtype != STEP_E4M3 && p.y_dtype != STEP_I8)
     return launch_kernel(norm_kernel<T, VEC, W, CH, false>, grid, block, 0, st, p);
   const int smem = ROWS * (p.d / p.group) * 4;
@@ -255,8 +329,9 @@ bool aligned_to(const void* p, long long a, long long b, int es, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && a * es % bytes == 0 && b * es % bytes == 0;
 }
 
-// A warp to a row while a warp of every SM has one: 8192 rows of 2048 and more; eight
-// warps shorten the latency of fewer.
+// Rows of up to 256 features are a warp's.  Longer ones have four warps where there are
+// enough of them for every SM (8192 rows of 2048 with e4m3 @F@ us; a warp each, 46, two
+// 35, eight 35), eight where latency counts, and 32 past 8192.
 template <typename T>
 cudaError_t norm_by_shape(const NormParams& p, cudaStream_t st) {
   const int es = sizeof(T), ys = p.y_dtype == STEP_F32 ? 4 : p.y_dtype <= STEP_F16 ? 2 : 1;
@@ -264,17 +339,17 @@ cudaError_t norm_by_shape(const NormParams& p, cudaStream_t st) {
                    (!p.r || (aligned_to(p.r, p.r_ts, p.r_hs, es, 16) && aligned_to(p.sum, p.s_ts, p.s_hs, es, 16))) &&
                    aligned_to(p.w, 0, 0, 1, 16) &&
                    aligned_to(p.y, p.y_ts, p.y_hs, ys, ys == 1 ? 8 : 16);
-  const long long rows = (long long)p.T * p.H;
-  const bool many = rows >= 4ll * device_sms();
+  const bool many = (long long)p.T * p.H >= 4ll * device_sms();
   if (vec) {
     if (p.d <= 256) return norm_launch<T, 8, 1, 1>(p, st);
-    if (p.d <= 1024 && many) return norm_launch<T, 8, 1, 4>(p, st);
-    if (p.d <= 2048) return many ? norm_launch<T, 8, 1, 8>(p, st) : norm_launch<T, 8, 8, 1>(p, st);
+    if (p.d <= 1024 && many) return norm_launch<T, 8, 4, 1>(p, st);
+    if (p.d <= 2048) return many ? norm_launch<T, 8, 4, 2>(p, st) : norm_launch<T, 8, 8, 1>(p, st);
     if (p.d <= 8192) return norm_launch<T, 8, 8, 4>(p, st);
     return norm_launch<T, 8, 32, 4>(p, st);
   }
   if (p.d <= 256) return norm_launch<T, 1, 1, 8>(p, st);
   if (p.d <= 2048) return norm_launch<T, 1, 8, 8>(p, st);
+  if (p.d <= 8192) return norm_launch<T, 1, 32, 8>(p, st);
   return norm_launch<T, 1, 32, 32>(p, st);
 }
 

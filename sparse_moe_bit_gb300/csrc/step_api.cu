@@ -47,7 +47,7 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_ts,
     return fail(MOE_ERR_INVALID_ARG, "group of %d in rows of %d", group, d);
   if (!residual != !sum) return fail(MOE_ERR_INVALID_ARG, "residual and sum come together");
   if (d > kNormMaxD) return fail(MOE_ERR_UNSUPPORTED, "d above %d", kNormMaxD);
-  if ((long long)T * H >= (1ll << 31)) return fail(MOE_ERR_UNSUPPORTED, "T * H = %lld", (long long)T * H);
+  if ((long long)T * H >= (1ll << 31) - 4) return fail(MOE_ERR_UNSUPPORTED, "T * H = %lld", (long long)T * H);
   if (T == 0) return MOE_OK;
   if (!x || !y || (is8(y_dtype) != (scales != nullptr)))
     return fail(MOE_ERR_INVALID_ARG, "NULL tensor, or scales without an 8-bit y");
@@ -76,8 +76,11 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_ts,
   p.w_dtype = weight_dtype;
   p.y_dtype = y_dtype;
   p.group = group ? group : d;
+  p.div = make_fastdiv(p.group);
+  p.div_h = make_fastdiv(H);
   p.eps = eps;
   p.offset = unit_offset ? 1.f : 0.f;
+  p.inv_d = 1.f / (float)d;
   STEP_CK(launch_norm(p, static_cast<cudaStream_t>(stream)), "rms_norm launch");
   return MOE_OK;
 }

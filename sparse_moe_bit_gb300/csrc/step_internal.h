@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "moe_internal.h"
+#include "paged_internal.h"
 #include "step.h"
 
 namespace moe {
@@ -21,7 +22,8 @@ struct NormParams {
   long long x_ts, x_hs, r_ts, r_hs, s_ts, s_hs, y_ts, y_hs;
   int dtype, w_dtype, y_dtype;
   int group;      // of an 8-bit y
-  float eps, offset;
+  FastDiv div, div_h;  // by group, by H
+  float eps, offset, inv_d;
 };
 constexpr int kNormMaxD = 32768;
 cudaError_t launch_norm(const NormParams& p, cudaStream_t st);
