@@ -97,9 +97,10 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_str
  *   logits   BF16, F16 or F32 [B][V], rows `stride` elements apart.  NaN counts as
  *            -inf; a token at -inf is never taken; +inf share the weight evenly.
  *            A row without any other logit: token -1, logprob NaN.
- *   u, temperature, top_p, min_p  fp32 [B];  top_k int32 [B].  Any of the last
- *            four may be NULL: 1, 1, 0 and 0.  Values out of range are read as the
- *            nearest in it (NaN: as off; temperature NaN, or below 0: 0).
+ *   u, temperature, top_p, min_p  fp32 [B];  top_k int32 [B].  Where one of the
+ *            last four is NULL, all_* is every row's (temperature 1, top_k 0, top_p 1
+ *            and min_p 0 leave all tokens as they are).  Values out of range are
+ *            read as the nearest in it (NaN: as off; temperature NaN, or below 0: 0).
  *   token    int32 [B]
  *   logprob  fp32 [B], or NULL: the logarithm of the probability with which the
  *            token was drawn (0 at temperature 0)
@@ -107,7 +108,8 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_str
  */
 moe_status sample(const void* logits, int dtype, int B, int V, int64_t stride, const float* u,
                   const float* temperature, const int32_t* top_k, const float* top_p,
-                  const float* min_p, int32_t* token, float* logprob, void* cuda_stream);
+                  const float* min_p, float all_temperature, int all_top_k, float all_top_p,
+                  float all_min_p, int32_t* token, float* logprob, void* cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -534,14 +534,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int chunk = (slice + kThreads - 1) / kThreads * 32;
   const int w0 = min(warp * chunk, n), w1 = min(w0 + chunk, n);
 
-  const float temperature = p.temperature ? p.temperature[row] : 1.f;
+  const float temperature = p.temperature ? p.temperature[row] : p.all_temperature;
   const bool greedy = !(temperature > 0.f);
-  int k = p.top_k ? p.top_k[row] : 0;
+  int k = p.top_k ? p.top_k[row] : p.all_top_k;
   if (k <= 0 || k >= p.V) k = 0;
-  float top_p = p.top_p ? p.top_p[row] : 1.f;
+  float top_p = p.top_p ? p.top_p[row] : p.all_top_p;
   if (!(top_p < 1.f)) top_p = 1.f;
   top_p = fmaxf(top_p, 0.f);
-  float min_p = p.min_p ? p.min_p[row] : 0.f;
+  float min_p = p.min_p ? p.min_p[row] : p.all_min_p;
   if (!(min_p > 0.f)) min_p = 0.f;
   min_p = fminf(min_p, 1.f);
   float u = p.u[row];

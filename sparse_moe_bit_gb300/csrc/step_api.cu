@@ -134,7 +134,8 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_ts, const
 
 moe_status sample(const void* logits, int dtype, int B, int V, int64_t stride, const float* u,
                   const float* temperature, const int32_t* top_k, const float* top_p,
-                  const float* min_p, int32_t* token, float* logprob, void* cuda_stream) {
+                  const float* min_p, float all_temperature, int all_top_k, float all_top_p,
+                  float all_min_p, int32_t* token, float* logprob, void* cuda_stream) {
   if (!is_float(dtype)) return fail(MOE_ERR_INVALID_ARG, "dtype %d", dtype);
   if (B < 0 || V < 1) return fail(MOE_ERR_INVALID_ARG, "bad size (B=%d V=%d)", B, V);
   if (V > kSampleMaxV || B > (1 << 27)) return fail(MOE_ERR_UNSUPPORTED, "B=%d, V=%d (V up to %d)", B, V, kSampleMaxV);
@@ -150,6 +151,10 @@ moe_status sample(const void* logits, int dtype, int B, int V, int64_t stride, c
   p.top_k = top_k;
   p.top_p = top_p;
   p.min_p = min_p;
+  p.all_temperature = all_temperature;
+  p.all_top_k = all_top_k;
+  p.all_top_p = all_top_p;
+  p.all_min_p = all_min_p;
   p.token = token;
   p.logprob = logprob;
   p.stride = stride;

@@ -47,6 +47,8 @@ struct SampleParams {
   const void* logits;
   const float *u, *temperature, *top_p, *min_p;
   const int32_t* top_k;
+  float all_temperature, all_top_p, all_min_p;  // where there is no array
+  int all_top_k;
   int32_t* token;
   float* logprob;
   long long stride;

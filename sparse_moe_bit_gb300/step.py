@@ -8,13 +8,12 @@ one); on a given stream outputs come from that stream's pool.  Like the package'
 other calls they leave no autograd graph."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 from . import moe as _moe
-from .paged import _check, _i32, _need, _new, _placed, _stream, _torch_stream, _used
+from .paged import _check, _i32, _need, _new, _placed, _stream, _used
 
 # names of the functions include/step.h declares (checked by its ABI test)
 EXPORTS = ["rms_norm", "linear4", "sample"]
@@ -23,6 +22,7 @@ _DTYPE = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3, torch.float8_e4
           torch.int8: 5}
 _EIGHT = (torch.float8_e4m3fn, torch.int8)
 _SCALE = {torch.float16: _moe.MOE_SCALE_F16, torch.bfloat16: _moe.MOE_SCALE_BF16}
+_F32 = torch.float32
 _lib = None
 
 
@@ -35,7 +35,7 @@ def _library():
     sig = {
         "rms_norm": [P, I, I, I, I, L, L, P, L, L, P, L, L, P, I, I, F, P, I, L, L, P, I, P],
         "linear4": [P, I, I, I, L, P, I, P, P, P, I, I, I, P, I, L, P],
-        "sample": [P, I, I, I, L, P, P, P, P, P, P, P, P],
+        "sample": [P, I, I, I, L, P, P, P, P, P, F, I, F, F, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -50,17 +50,9 @@ def _rows(t, shape, name):
     if t.shape != shape:
         raise ValueError(f"{name} must be like x")
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s features must be contiguous")
-    return (st[0], st[1]) if len(shape) == 3 else (st[0], 0)
-
-
-def _dense(shape):
-    st, n = [], 1
-    for x in reversed(shape):
-        st.append(n)
-        n *= max(x, 1)
-    return tuple(reversed(st))
+    return (st[0], st[1]) if len(st) == 3 else (st[0], 0)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -75,60 +67,67 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     scales, fp32 [..., d / group], one for ``group`` features (0: a row); and behind
     them, with a residual, x + residual in x's type.  ``out`` may be x, ``sum_out``
     x or the residual (in place)."""
-    shape = x.shape
-    dt = _DTYPE.get(x.dtype, 0)
-    if dt not in (1, 2, 3) or len(shape) not in (2, 3):
+    shape, xt = x.shape, x.dtype
+    dt = _DTYPE.get(xt, 0)
+    if not 1 <= dt <= 3 or len(shape) not in (2, 3):
         raise ValueError("x must be [T, d] or [T, H, d] of bf16, fp16 or fp32")
-    T, H, d = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
     _placed(x, weight, residual, out, sum_out)
     xs = _rows(x, shape, "x")
-    if weight is not None and (weight.dim() != 1 or weight.shape[0] != d or not weight.is_contiguous()):
-        raise ValueError("weight must be dense [d]")
-    if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
-    yt = _DTYPE.get(out_dtype, 0)
-    if out is not None and out.dtype is not out_dtype:
-        raise ValueError("out must be of out_dtype")
+    if len(shape) == 2:
+        T, d = shape
+        H, dense, strides = 1, (d, 1), (d, 0)
+    else:
+        T, H, d = shape
+        dense, strides = (H * d, d, 1), (H * d, d)
+    wp = wt = 0
+    if weight is not None:
+        if weight.dim() != 1 or weight.shape[0] != d or not weight.is_contiguous():
+            raise ValueError("weight must be dense [d]")
+        wp, wt = weight.data_ptr(), _DTYPE.get(weight.dtype, 0)
     made = []
     if out is None:
-        out = _new(stream, shape, _dense(shape), out_dtype, x.device)
+        out = _new(stream, shape, dense, out_dtype or xt, x.device)
         made.append(out)
-    ys = _rows(out, shape, "out")
+        ys = strides
+    else:
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise ValueError("out must be of out_dtype")
+        ys = _rows(out, shape, "out")
+    yt = out.dtype
+    rp = sp = None
     rs = ss = (0, 0)
     if residual is not None:
-        if residual.dtype is not x.dtype:
-            raise ValueError("residual must be like x")
-        rs = _rows(residual, shape, "residual")
+        if residual.dtype is not xt or sum_out is not None and sum_out.dtype is not xt:
+            raise ValueError("residual and sum_out must be like x")
+        rs, rp = _rows(residual, shape, "residual"), residual.data_ptr()
         if sum_out is None:
-            sum_out = _new(stream, shape, _dense(shape), x.dtype, x.device)
+            sum_out = _new(stream, shape, dense, xt, x.device)
             made.append(sum_out)
-        elif sum_out.dtype is not x.dtype:
-            raise ValueError("sum_out must be like x")
-        ss = _rows(sum_out, shape, "sum_out")
+            ss = strides
+        else:
+            ss = _rows(sum_out, shape, "sum_out")
+        sp = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
-    scales = None
-    if out_dtype in _EIGHT:
+    scales = qp = None
+    if yt in _EIGHT:
         g = group or d
         if g < 1 or d % g:
             raise ValueError("group must divide the features")
-        s_shape = (*shape[:-1], d // g)
-        scales = _new(stream, s_shape, _dense(s_shape), torch.float32, x.device)
+        n = d // g
+        scales = _new(stream, (*shape[:-1], n), (n, 1) if len(shape) == 2 else (H * n, n, 1), torch.float32,
+                      x.device)
         made.append(scales)
+        qp = scales.data_ptr()
     if H == 0:
         T, H = 0, 1
-    _check(_library().rms_norm(
-        x.data_ptr(), dt, T, H, d, *xs, None if residual is None else residual.data_ptr(), *rs,
-        None if sum_out is None else sum_out.data_ptr(), *ss,
-        None if weight is None else weight.data_ptr(),
-        0 if weight is None else _DTYPE.get(weight.dtype, 0), unit_offset, eps, out.data_ptr(), yt,
-        *ys, None if scales is None else scales.data_ptr(), group, _stream(stream, x)))
+    _check(_library().rms_norm(x.data_ptr(), dt, T, H, d, *xs, rp, *rs, sp, *ss, wp or None, wt, unit_offset,
+                               eps, out.data_ptr(), _DTYPE.get(yt, 0), *ys, qp, group, _stream(stream, x)))
     if stream is not None:
         _used(stream, made, [t for t in (out, sum_out) if not any(t is m for m in made)])
-    res = (out,) if scales is None else (out, scales)
-    if residual is not None:
-        res += (sum_out,)
-    return res if len(res) > 1 else out
+    if scales is None:
+        return out if residual is None else (out, sum_out)
+    return (out, scales) if residual is None else (out, scales, sum_out)
 
 
 def linear4(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor,
@@ -185,15 +184,13 @@ def linear4(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, bias: tor
     return out
 
 
-def _setting(v, off, dtype, B, name, like):
-    """A row's setting: None where it is off for all, else a tensor [B]."""
-    if v is None or (not isinstance(v, torch.Tensor) and v == off):
-        return None
+def _setting(v, dtype, B, name):
+    """A row's setting as the address of a tensor [B], or as one number for all."""
     if not isinstance(v, torch.Tensor):
-        return torch.full((B,), v, dtype=dtype, device=like.device)
+        return None, v
     if v.dtype is not dtype or v.dim() != 1 or v.shape[0] != B or not v.is_contiguous():
         raise ValueError(f"{name} must be a number or dense {dtype} [B]")
-    return v
+    return v.data_ptr(), 0
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
@@ -210,14 +207,11 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
         raise ValueError("a row's logits must be contiguous")
     if u.dtype is not torch.float32 or u.dim() != 1 or u.shape[0] != B or not u.is_contiguous():
         raise ValueError("u must be dense fp32 [B]")
-    f32, tens = torch.float32, [t for t in (temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor)]
-    _placed(logits, u, out, *tens)
-    # (numbers become tensors of the stream that reads them)
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream)):
-        t = _setting(temperature, 1.0, f32, B, "temperature", logits)
-        k = _setting(top_k, 0, torch.int32, B, "top_k", logits)
-        p = _setting(top_p, 1.0, f32, B, "top_p", logits)
-        m = _setting(min_p, 0.0, f32, B, "min_p", logits)
+    _placed(logits, u, out, *[v for v in (temperature, top_k, top_p, min_p) if isinstance(v, torch.Tensor)])
+    t, t0 = _setting(temperature, _F32, B, "temperature")
+    k, k0 = _setting(top_k, torch.int32, B, "top_k")
+    p, p0 = _setting(top_p, _F32, B, "top_p")
+    m, m0 = _setting(min_p, _F32, B, "min_p")
     made = []
     if out is None:
         out = _new(stream, (B,), (1,), torch.int32, logits.device)
@@ -227,11 +221,11 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_
         _need(out.shape[0] == B and out.is_contiguous(), "out must be dense [B]")
     lp = None
     if return_logprobs:
-        lp = _new(stream, (B,), (1,), f32, logits.device)
+        lp = _new(stream, (B,), (1,), _F32, logits.device)
         made.append(lp)
-    ptr = lambda x: None if x is None else x.data_ptr()
     _check(_library().sample(logits.data_ptr(), _DTYPE.get(logits.dtype, 0), B, V, logits.stride(0),
-                             u.data_ptr(), ptr(t), ptr(k), ptr(p), ptr(m), out.data_ptr(), ptr(lp),
+                             u.data_ptr(), t, k, p, m, t0, max(min(k0, 0x7fffffff), -1), p0, m0,
+                             out.data_ptr(), None if lp is None else lp.data_ptr(),
                              _stream(stream, logits)))
     if stream is not None:
         _used(stream, made, () if made and made[0] is out else [out])

@@ -76,7 +76,7 @@ def test_linear4_rejects_bad_arguments(lib, kw, status):
 
 
 def _sample(lib, **kw):
-    a = dict(logits=_A, dtype=3, B=2, V=100, stride=100, u=_B, t=_C, k=_C, p=_C, m=_C, token=_D, logprob=None,
+    a = dict(logits=_A, dtype=3, B=2, V=100, stride=100, u=_B, t=_C, k=_C, p=_C, m=_C, t0=1.0, k0=0, p0=1.0, m0=0.0, token=_D, logprob=None,
              stream=None)
     a.update(kw)
     return lib.sample(*a.values())
