@@ -178,7 +178,13 @@ struct Plan {
 // a warp.
 // 256-row tiles: split over the keys only while the pairs of CTAs leave SMs
 // without work; no chunk below 512 keys.
-Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv) {
+//
+// The keys that a group shares may be read again for every 16 rows where that is little:
+// 256-row tiles take some 10 us more than small ones before their first product (4
+// continuations of 1501 keys, 16/2 heads of 256, 2 tiles of 16 rows: @FEW@).
+constexpr long long kReread = 48ll << 20;
+Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv,
+          bool group = false) {
   Plan r{};
   const int G = Hq / c.heads;
   long long mq = max_q > 0 ? max_q : b.N > 0 ? ((long long)b.T + b.N - 1) / b.N : b.T;
@@ -186,6 +192,8 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
   long long kv = max_kv > 0 ? max_kv : b.capacity;
   if (kv > b.capacity) kv = b.capacity;
   r.wide = mq * G > (max_q > 0 || b.T <= b.N ? kRowTile : kRowTile / 2);
+  if (group && r.wide)
+    r.wide = (mq * G + kRowTile - 1) / kRowTile * b.N * kv * c.heads * c.dim * 4 > kReread;
   r.row_tile = mq * G <= 8 ? 8 : kRowTile;
   const long long rows = r.wide ? kPairRows : r.row_tile;
   long long span = kv;
@@ -254,7 +262,7 @@ SharedPlan plan_shared(const CacheView& c, const BatchView& b, int Hq, int G, in
   SharedPlan r{};
   BatchView gb = b;
   gb.N = G;
-  r.g = plan(c, gb, Hq, 0, max_group, max_shared);
+  r.g = plan(c, gb, Hq, 0, max_group, max_shared, true);
   r.p = plan(c, b, Hq, 0, max_q, max_tail);
   const size_t rows = (size_t)b.T * Hq, row = (size_t)c.dim * 4 + 8;
   for (Plan* x : {&r.g, &r.p}) {
@@ -266,7 +274,7 @@ SharedPlan plan_shared(const CacheView& c, const BatchView& b, int Hq, int G, in
   r.whole_g = r.at_p + up256(r.p.ws);
   r.whole_p = r.whole_g + (r.g.wide ? 0 : up256(rows * row));
   r.groups = r.whole_p + (r.p.wide ? 0 : up256(rows * row));
-  r.ws = r.groups + ((size_t)3 * G + 1 + b.N) * 4;
+  r.ws = r.groups + (size_t)b.T * 8 + ((size_t)3 * G + 1 + b.N) * 4;
   return r;
 }
 
@@ -535,7 +543,8 @@ moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int
   gv.cu_group = cu_group;
   gv.shared = shared;
   gv.G = groups;
-  gv.cu = reinterpret_cast<int32_t*>(ws + r.groups);
+  gv.of_token = reinterpret_cast<int2*>(ws + r.groups);
+  gv.cu = reinterpret_cast<int32_t*>(ws + r.groups + (size_t)p.b.T * 8);
   gv.len = gv.cu + groups + 1;
   gv.rows = gv.len + groups;
   gv.skip = gv.rows + groups;
@@ -563,11 +572,12 @@ moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int
   const bool bf = cache->dtype == PAGED_BF16;
   PAGED_CK(launch_paged_groups(p.b, gv, st), "paged_attention_shared groups launch");
   p.b.skip = gv.skip;
+  p.late = 1;
   PAGED_CK(r.g.wide ? launch_paged_chunk(g, bf, st) : launch_paged_rows(g, bf, st),
            "paged_attention_shared launch");
   PAGED_CK(r.p.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
            "paged_attention_shared launch");
-  PAGED_CK(launch_paged_join_shared(p, g, bf, st), "paged_attention_shared join launch");
+  PAGED_CK(launch_paged_join_shared(p, g, gv.of_token, bf, st), "paged_attention_shared join launch");
   return MOE_OK;
 }
 

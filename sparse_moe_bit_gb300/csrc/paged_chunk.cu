@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       tmem_dealloc_pair(*tmem_slot, 512);
     }
+    late_wait(p);
   };
 
   int bid = blockIdx.x >> 1;
@@ -948,13 +949,15 @@ cudaError_t chunk_launch_t(const ChunkParams& cp, cudaStream_t st) {
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = C::SMEM;
   c.stream = st;
-  cudaLaunchAttribute a[1];
+  cudaLaunchAttribute a[2];
   a[0].id = cudaLaunchAttributeClusterDimension;
   a[0].val.clusterDim.x = 2;
   a[0].val.clusterDim.y = 1;
   a[0].val.clusterDim.z = 1;
+  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[1].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
-  c.numAttrs = 1;
+  c.numAttrs = p.late ? 2 : 1;
   return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF, TMA>, cp);
 }
 

@@ -134,8 +134,15 @@ struct AttnParams {
   // covers leave theirs here, [T * Hq] (NULL: the warp writes o and lse)
   float* whole_o;
   float2* whole_ml;
+  // this kernel may start while the one before it in the stream still runs, which it
+  // depends on in nothing: it waits for that one before it ends, so that who waits for
+  // this kernel has waited for both
+  int late;
   int* err;
 };
+__device__ __forceinline__ void late_wait(const AttnParams& p) {
+  if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 // The first key in a query's window.  (A query before position 0 sees none; its
 // position less a window near 2^31 would not fit.)
 __device__ __forceinline__ int window_begin(int pos, int window) { return max(pos, 0) - window + 1; }
@@ -168,15 +175,17 @@ cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st);
 // The join of two attentions' partial results: over the keys that groups of sequences
 // share (`g`, its batch the groups) and over the sequences' own (`p`).
-cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, bool bf16,
-                                     cudaStream_t st);
+cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, const int2* of_token,
+                                     bool bf16, cudaStream_t st);
 // The groups of a batch made safe (paged_shared.cu): cu [G + 1], len [G] and rows [G]
 // are the groups as a batch of sequences (their tokens, shared keys, a member's row of
-// the table), skip [N] the members' first own key.
+// the table), skip [N] the members' first own key, of_token [T] each new token's
+// sequence and group (-1: none; what no sequence holds is not written).
 struct GroupView {
   const int32_t *cu_group, *shared;
   int G;
   int32_t *cu, *len, *rows, *skip;
+  int2* of_token;
 };
 cudaError_t launch_paged_groups(const BatchView& b, const GroupView& g, cudaStream_t st);
 

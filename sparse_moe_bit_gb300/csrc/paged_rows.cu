@@ -231,7 +231,10 @@ __global__ void __launch_bounds__(32 * kWarps)
   // (no more warps than groups: each of them then has a part of every item
   // between its first and its last)
   const int W = (int)min((long long)(gridDim.x * kWarps), U), w = blockIdx.x * kWarps + warp;
-  if (w >= W) return;
+  if (w >= W) {
+    late_wait(p);
+    return;
+  }
   const long long u0 = share_of(U, W, w);
   const int steps = (int)(share_of(U, W, w + 1) - u0);
 
@@ -662,6 +665,83 @@ __global__ void __launch_bounds__(32 * kWarps)
   } else {
     cp_async_wait<0>();
   }
+  late_wait(p);
+}
+
+// Join of a row's parts, in their order: warp w of the row's CTA takes parts
+// w, w + W, ...; the warps' sums meet in shared memory.
+template <int D, bool BF, int W>
+__global__ void __launch_bounds__(32 * W) paged_join_kernel(const AttnParams p) {
+  constexpr int E = D / 32;  // features of a lane
+  __shared__ float sh_o[W][D];
+  __shared__ float sh_l[W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long rid = blockIdx.x;
+  const int t = (int)(rid / p.Hq), head = (int)(rid - (long long)t * p.Hq);
+  // (the batch's arrays were there before the partial results)
+  const int n = find_seq(p.b, t);
+  const Seq s = load_seq(p.b, max(n, 0));
+  // The partial results are there behind this wait.  No CTA leaves before it: this
+  // grid must not be over before the first one, whose workspace may be another's
+  // from then on.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // new tokens outside every sequence have no partial results
+  if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
+  // part c of this row: slot (c ? rest + c * step : at), in rows
+  long long at, rest, step;
+  int parts;
+  if (p.split) {
+    at = rest = rid * p.chunks;
+    step = 1;
+    parts = p.chunks;
+  } else {
+    const int r = (t - s.t0) * p.G + head % p.G, tile = r / p.row_tile;
+    const Extent e = extent_of(p, s, RowsCfg<D>::KG, p.row_tile);
+    const long long U = p.before[p.b.N];
+    const long long u = p.before[n] + (long long)(tile * p.c.heads + head / p.G) * e.groups;
+    const int warps = (int)min((long long)p.warps, U);
+    const int w0 = owner_of(U, warps, u), w1 = owner_of(U, warps, u + e.groups - 1);
+    if (w0 == w1) return;  // written by its warp
+    at = (2ll * w0 + 1) * kRowTile + r % p.row_tile;
+    rest = 2ll * w0 * kRowTile + r % p.row_tile;
+    step = 2 * kRowTile;
+    parts = w1 - w0 + 1;
+  }
+  auto slot = [&](int c) { return c == 0 ? at : rest + c * step; };
+  float m = kNegInf;
+  for (int c = lane; c < parts; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float u = m == kNegInf ? 0.f : m;
+  float l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int c = warp; c < parts; c += W) {
+    const float2 x = p.part_ml[slot(c)];
+    const float* po = p.part_o + slot(c) * D;
+    const float a = exp2_approx(x.x - u);
+    l += a * x.y;
+    if (x.y != 0.f) {  // (a part without keys need not hold numbers; NaN sums pass)
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += a * po[e * 32 + lane];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = acc[e];
+  if (lane == 0) sh_l[warp] = l;
+  __syncthreads();
+  float total = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) total += sh_l[w];
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  for (int f = threadIdx.x; f < D; f += 32 * W) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += sh_o[w][f];
+    p.o[t * p.o_ts + head * p.o_hs + f] = pack1<BF>(v * inv);
+  }
+  if (threadIdx.x == 0 && p.lse) p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
 }
 
 // A row's partial results: part c lies in slot (c ? rest + c * step : at).
@@ -705,36 +785,32 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, int n, const Seq&
   return r;
 }
 
-// Join of a row's parts, in their order: warp w of the row's CTA takes parts
-// w, w + W, ...; the warps' sums meet in shared memory.  SHARED: the parts over the
-// group's keys (g), then those over the sequence's own.
-template <int D, bool BF, int W, bool SHARED>
+// Where groups of sequences share keys (g: the groups as a batch): the parts over the
+// group's keys, then those over the sequence's own.  Every row of a sequence is written here.
+struct SharedJoin {
+  AttnParams p, g;
+  const int2* of_token;  // a new token's sequence and group
+};
+template <int D, bool BF, int W>
 __global__ void __launch_bounds__(32 * W)
-    paged_join_kernel(const AttnParams p, const __grid_constant__ AttnParams g) {
-  constexpr int E = D / 32;  // features of a lane
+    paged_join_shared_kernel(const __grid_constant__ SharedJoin jp) {
+  constexpr int E = D / 32;
   __shared__ float sh_o[W][D];
   __shared__ float sh_l[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const AttnParams &p = jp.p, &g = jp.g;
   const long long rid = blockIdx.x;
   const int t = (int)(rid / p.Hq), head = (int)(rid - (long long)t * p.Hq);
-  // (the batch's arrays were there before the partial results)
-  const int n = find_seq(p.b, t);
-  const Seq s = load_seq(p.b, max(n, 0));
-  // The partial results are there behind this wait.  No CTA leaves before it: this
-  // grid must not be over before the first one, whose workspace may be another's
-  // from then on.
+  // (what no sequence holds has any number here: it is looked at before it is used)
+  const int2 of = jp.of_token[t];
+  const int n = of.x >= 0 && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
+  const Seq s = load_seq(p.b, max(n, 0)), gs = load_seq(g.b, max(k, 0));
+  // (as above: no CTA leaves before it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Parts own = parts_of<D>(p, n, s, t, head);
-  Parts grp{nullptr, nullptr, 0, 0, 0, 0};
-  if constexpr (SHARED) {
-    if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
-    const int k = find_seq(g.b, t);
-    grp = parts_of<D>(g, k, load_seq(g.b, max(k, 0)), t, head);
-  }
-  const int parts = grp.n + own.n;
-  // new tokens outside every sequence have no partial results, nor those that a warp wrote
-  if (!SHARED && parts == 0) return;
-  auto ml = [&](int c) { return c < grp.n ? grp.ml[grp.slot(c)] : own.ml[own.slot(c - grp.n)]; };
+  if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
+  const Parts own = parts_of<D>(p, n, s, t, head), grp = parts_of<D>(g, k, gs, t, head);
+  const int first = grp.n, parts = first + own.n;
+  auto ml = [&](int c) { return c < first ? grp.ml[grp.slot(c)] : own.ml[own.slot(c - first)]; };
   float m = kNegInf;
   for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml(c).x);
 #pragma unroll
@@ -746,7 +822,7 @@ __global__ void __launch_bounds__(32 * W)
 #pragma unroll 8
   for (int c = warp; c < parts; c += W) {
     const float2 x = ml(c);
-    const float* po = c < grp.n ? grp.o + grp.slot(c) * D : own.o + own.slot(c - grp.n) * D;
+    const float* po = c < first ? grp.o + grp.slot(c) * D : own.o + own.slot(c - first) * D;
     const float a = exp2_approx(x.x - u);
     l += a * x.y;
     if (x.y != 0.f) {  // (a part without keys need not hold numbers; NaN sums pass)
@@ -768,7 +844,8 @@ __global__ void __launch_bounds__(32 * W)
     for (int w = 0; w < W; ++w) v += sh_o[w][f];
     p.o[t * p.o_ts + head * p.o_hs + f] = pack1<BF>(v * inv);
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
+  if (threadIdx.x == 0 && p.lse)
+    p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
 }
 
 template <int D, int NB, bool BF, bool TMA>
@@ -777,8 +854,17 @@ cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem((const void*)paged_rows_kernel<D, NB, BF, TMA>, C::SMEM, allowed);
   if (e != cudaSuccess) return e;
-  return launch_kernel(paged_rows_kernel<D, NB, BF, TMA>, dim3(rp.a.warps / kWarps), dim3(32 * kWarps),
-                       C::SMEM, st, rp);
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(rp.a.warps / kWarps);
+  c.blockDim = dim3(32 * kWarps);
+  c.dynamicSmemBytes = C::SMEM;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = rp.a.late ? 1 : 0;
+  return cudaLaunchKernelEx(&c, paged_rows_kernel<D, NB, BF, TMA>, rp);
 }
 
 template <int D, bool BF>
@@ -796,32 +882,34 @@ cudaError_t rows_launch(const AttnParams& p, cudaStream_t st) {
   return tma ? rows_launch_t<D, 2, BF, true>(rp, st) : rows_launch_t<D, 2, BF, false>(rp, st);
 }
 
-template <int D, bool BF, int W, bool SHARED>
-cudaError_t join_w(const AttnParams& p, const AttnParams& g, cudaStream_t st) {
+// A CTA a row, set up while the partial results are still being computed.
+template <typename P>
+cudaError_t join_w(void (*kern)(P), int warps, const AttnParams& p, const P& params, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)((long long)p.b.T * p.Hq));
-  c.blockDim = dim3(32 * W);
+  c.blockDim = dim3(32 * warps);
   c.stream = st;
-  // set up while the partial results are still being computed
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, paged_join_kernel<D, BF, W, SHARED>, p, g);
+  return cudaLaunchKernelEx(&c, kern, params);
 }
 
 template <int D, bool BF>
 cudaError_t join_launch(const AttnParams& p, cudaStream_t st) {
   // a warp for four parts or so: a row's parts, a kilobyte each at D = 256, are
   // read in as many rounds of latency as a warp has parts
-  if (p.parts <= 16) return join_w<D, BF, 4, false>(p, p, st);
-  return join_w<D, BF, 32, false>(p, p, st);
+  if (p.parts <= 16) return join_w(paged_join_kernel<D, BF, 4>, 4, p, p, st);
+  return join_w(paged_join_kernel<D, BF, 32>, 32, p, p, st);
 }
 template <int D, bool BF>
-cudaError_t join_shared_launch(const AttnParams& p, const AttnParams& g, cudaStream_t st) {
-  if (p.parts + g.parts <= 32) return join_w<D, BF, 4, true>(p, g, st);
-  return join_w<D, BF, 32, true>(p, g, st);
+cudaError_t join_shared_launch(const AttnParams& p, const AttnParams& g, const int2* of_token,
+                               cudaStream_t st) {
+  const SharedJoin jp{p, g, of_token};
+  if (p.parts + g.parts <= 32) return join_w(paged_join_shared_kernel<D, BF, 4>, 4, p, jp, st);
+  return join_w(paged_join_shared_kernel<D, BF, 32>, 32, p, jp, st);
 }
 
 }  // namespace
@@ -840,9 +928,9 @@ cudaError_t launch_paged_rows(const AttnParams& p, bool bf16, cudaStream_t st) {
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st) {
   PAGED_BY_DIM(join_launch, p, st);
 }
-cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, bool bf16,
-                                     cudaStream_t st) {
-  PAGED_BY_DIM(join_shared_launch, p, g, st);
+cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, const int2* of_token,
+                                     bool bf16, cudaStream_t st) {
+  PAGED_BY_DIM(join_shared_launch, p, g, of_token, st);
 }
 
 }  // namespace moe

@@ -33,12 +33,14 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BatchView b, con
   }
   __syncthreads();
   const int len = sh_with < 2 ? 0 : max(min(g.shared[me], sh_least), 0);
-  for (int n = n0 + threadIdx.x; n < n1; n += kThreads) g.skip[n] = len;
-  // (sequences of no group)
-  if (me == 0)
-    for (int n = threadIdx.x; n < n0; n += kThreads) g.skip[n] = 0;
-  if (me == g.G - 1)
-    for (int n = n1 + threadIdx.x; n < b.N; n += kThreads) g.skip[n] = 0;
+  // the first and the last group's CTA also take the sequences of no group
+  const int a0 = me == 0 ? 0 : n0, a1 = me == g.G - 1 ? b.N : n1;
+  for (int n = a0 + threadIdx.x; n < a1; n += kThreads) {
+    const bool in = n >= n0 && n < n1;
+    g.skip[n] = in ? len : 0;
+    const Seq s = load_seq(b, n);
+    for (int t = s.t0; t < s.t0 + s.nq; ++t) g.of_token[t] = make_int2(n, in ? me : -1);
+  }
   if (threadIdx.x == 0) {
     g.len[me] = len;
     g.rows[me] = min(sh_first, b.N - 1);
