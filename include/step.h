@@ -73,9 +73,10 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *   group   a multiple of 64 that divides K
  *   y       BF16, F16 or F32 [T][O], rows y_token_stride elements apart; may not
  *           overlap x
- * Any T; the weights are read once for every 64 tokens (every 32 to 8 where K is
- * above 6144), so a prompt's products are better served by a matrix product of
- * 16-bit weights.  K up to 65536.  The result does not depend on timing.
+ * Every 16 tokens read the weights anew (one after another from L2), so a prompt's
+ * products are better served by a matrix product of 16-bit weights.  K up to 36864,
+ * T up to 524280.  The result does not depend on timing, nor a token's on the others in
+ * the call beyond the split that T chooses.
  */
 moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_stride,
                    const float* x_scale, int x_group, const void* codes, const void* scale,

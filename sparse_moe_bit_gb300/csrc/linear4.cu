@@ -11,20 +11,23 @@
 // An 8-bit x has its own scale applied after a 64-wide part (or at the end, where a
 // token has one).
 //
-// Bound: HBM (half a byte a weight plus four a group), and few instructions a byte to
-// reach it.  A warp has 16 rows of weights as the wide side of mma.sync (m16n8k16) and
-// 8 NT tokens as the narrow one, so that up to 64 tokens share one reading.  Lane (g, j)
-// of a warp takes rows g and g + 8 and of each part of 64 weights the codes 16 j .. 16 j
-// + 15, 8 bytes a row, which shifts turn into operands in the order 0 4 1 5 2 6 3 7; the
-// tokens are laid out in shared memory in that order once.  A warp's rows come through a
-// ring of its own by 16-byte copies, four parts a stage (2.3 KB), two stages ahead and
-// across blocks of rows, so that a CTA that walks many never drains.  (The same loads
-// into registers took 123 instructions a part of 16 x 64 weights, and 70 us where this
-// takes @VOC@: 130001 x 2048 weights, 8 tokens.)
+// Bound: HBM (half a byte a weight plus four a group) for one token, beyond that the
+// instructions that turn codes into operands (some 95 a part of 16 x 64 weights, tokens up
+// to 8; 47 % of the ALU and 56 % of the issue slots).  A warp has 16 rows of weights as the
+// wide side of mma.sync (m16n8k16) and 8 or 16 tokens as the narrow one; more tokens are
+// further CTAs' (up to 64 of a warp were slower at every size: registers and reads of the
+// tokens).  Lane (g, j) of a warp takes rows g and g + 8 and of each part of 64 weights the
+// codes 16 j .. 16 j + 15, 8 bytes a row, which shifts turn into operands in the order
+// 0 4 1 5 2 6 3 7; the tokens are laid out in shared memory in that order once.  A warp's rows
+// come through a ring of its own by 16-byte copies, four parts a stage (2.3 KB), two stages
+// ahead and across blocks of rows, so that a CTA that walks many never drains.  (The same
+// loads into registers took 123 instructions a part, and 70 us for 130001 x 2048 weights
+// and 8 tokens.)
 //
-// Split: a CTA holds WR row tiles x WK slices of K (WR WK = 8 warps), and a cluster of C
-// CTAs splits K again where there are few rows or the tokens of all of K do not fit
-// shared memory; partial sums meet in shared memory, in the order of K.
+// Split: a CTA, one an SM, holds WR row tiles x WK slices of K (WR WK = 16 warps), and a
+// cluster of C CTAs splits K again where the tokens of all of K do not fit shared memory;
+// partial sums meet in shared memory, in a fixed order.
+// Measured (GPU time, weights not in L2): @FIG@
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -36,7 +39,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kStages = 3;
 constexpr int kPitch = 160;                   // bytes of a row of a stage: no bank conflicts
 constexpr int kStage = 16 * kPitch + 16 * 16;  // codes of 16 rows x 4 parts, scales and biases
@@ -47,40 +50,50 @@ struct Plan4 {
   int parts;            // 64-wide parts of K
   int cta_parts, warp_parts;  // ... of a CTA's and of a warp's slice (multiples of 4)
   int blocks;           // of 16 wr rows
-  int t0;               // this launch's first token
   int off_sum, off_xs, off_ring, off_red;  // shared memory: x, its sums and scales, the rest
   int vec;              // a row's scales can be read four at a time
 };
 
-template <bool BF>
+// c = a b + c, or a b alone.  (Not volatile: the products of a stage's parts, which do not
+// depend on one another, may pass each other.)
+template <bool BF, bool ADD>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
+  const float z[4] = {ADD ? c[0] : 0.f, ADD ? c[1] : 0.f, ADD ? c[2] : 0.f, ADD ? c[3] : 0.f};
   if constexpr (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]),
+          "f"(z[3]));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z[0]), "f"(z[1]), "f"(z[2]),
+          "f"(z[3]));
 }
 // codes p and p + 4 of a word of eight as a pair of operands
 template <bool BF>
-__device__ __forceinline__ uint32_t codes_of(uint32_t w, int p) {
-  if constexpr (BF) {
-    // (one operation, not an AND and an OR: the constants have to be in registers)
+struct Codes {
+  uint32_t mask, lead;  // (in registers: as literals they take an AND and an OR, or moves)
+  __device__ Codes() {
+    asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x41804180;" : "=r"(lead));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, int p) const {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(r) : "r"(p == 0 ? w << 3 : w >> (4 * p - 3)), "r"(0x00780078u), "r"(0x41804180u));
+        : "=r"(r) : "r"(p == 0 ? w << 3 : w >> (4 * p - 3)), "r"(mask), "r"(lead));
     return r;
-  } else {
+  }
+};
+template <>
+struct Codes<false> {
+  __device__ __forceinline__ uint32_t operator()(uint32_t w, int p) const {
     return (w >> (4 * p)) & 0x000f000fu;
   }
-}
+};
 __device__ __forceinline__ float value16(uint16_t b, bool bf) {
   return bf ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
 }
@@ -116,7 +129,7 @@ __device__ __forceinline__ void unpack_x8(int dtype, uint4 a, uint16_t (&v)[8]) 
 // NT blocks of 8 tokens.  XS: an 8-bit x with scales below a token (else p.xs, if any,
 // holds one a token).  ALONE: a warp's sums are whole (WK = C = 1).
 template <int NT, bool BF, bool XS, bool ALONE>
-__global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kWarps, 1)
     linear4_kernel(const __grid_constant__ Plan4 q) {
   constexpr int TB = 8 * NT;
   const Linear4Params& p = q.a;
@@ -129,7 +142,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
   const int g = lane >> 2, j = lane & 3;
   const int rank = blockIdx.x % q.cluster, first = blockIdx.x / q.cluster;
   const int stride = gridDim.x / q.cluster;  // of blocks of rows
-  const int tokens = min(p.T - q.t0, TB);
+  const int t0 = blockIdx.y * TB, tokens = min(p.T - t0, TB);
   const int part0 = rank * q.cta_parts, cta_parts = max(min(q.cta_parts, q.parts - part0), 0);
   const int wk = warp % q.wk, wr = warp / q.wk;
   const int my0 = wk * q.warp_parts;                                   // within the CTA's slice
@@ -150,8 +163,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
   const int code_dst = (lane >> 3) * kPitch + (lane & 7) * 16;
   const int part_first = part0 + my0;
   int row_left = 0;  // rows of the block behind this lane's first
+  // the first row of this warp's tile of a block
+  auto row_of = [&](int block) {
+    return ALONE ? ((block - first) * kWarps + wr * stride + first) * 16 : block * rows + wr * 16;
+  };
   auto enter = [&]() {
-    const int o0 = fb * rows + wr * 16;
+    const int o0 = row_of(fb);
     row_left = p.O - o0 - (lane >> 3);
     code_src = p.codes + (o0 + (lane >> 3)) * code_pitch + (long long)part_first * 32 + (lane & 7) * 16;
     scale_src = (lane & 1 ? p.bias : p.scale) + (long long)min(o0 + (lane >> 1), p.O - 1) * sgroups;
@@ -219,8 +236,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
       raw[a] = make_uint4(0, 0, 0, 0);
       z[a] = 0.f;
       if (i < items && t < tokens) {
-        raw[a] = raw_x8(p, (q.t0 + t) * p.x_ts + part * 64 + e8 * 8);
-        if (XS && e8 == 0) z[a] = __ldg(p.xs + (long long)(q.t0 + t) * (p.K / p.xg) + part * 64 / p.xg);
+        raw[a] = raw_x8(p, (t0 + t) * p.x_ts + part * 64 + e8 * 8);
+        if (XS && e8 == 0) z[a] = __ldg(p.xs + (long long)(t0 + t) * (p.K / p.xg) + part * 64 / p.xg);
       }
     }
 #pragma unroll
@@ -264,6 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
   const float* const sum_lane = ssum + 2 * j;
   const float* const xs_lane = sxs + 2 * j;
   const int code_lane = g * kPitch + j * 8;
+  const Codes<BF> codes;
   auto compute = [&](const uint8_t* st, int quad, int left, auto full) {
     constexpr bool FULL = decltype(full)::value;
     const int part0 = my0 + quad * 4;
@@ -271,30 +289,37 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
     const float* const sq = sum_lane + part0 * TB;
     [[maybe_unused]] const float* const zq = xs_lane + part0 * TB;
     float s[4][2], b[4][2];  // of rows g and g + 8
+    uint32_t u[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint4 v = *reinterpret_cast<const uint4*>(st + 16 * kPitch + (g + 8 * h) * 16);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      if (bf_scale) {
+      u[h][0] = v.x, u[h][1] = v.y, u[h][2] = v.z, u[h][3] = v.w;
+    }
+    if (bf_scale) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s[i][h] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
-          b[i][h] = __uint_as_float(i & 1 ? u[2 + i / 2] & 0xffff0000u : u[2 + i / 2] << 16);
+          s[i][h] = __uint_as_float(i & 1 ? u[h][i / 2] & 0xffff0000u : u[h][i / 2] << 16);
+          b[i][h] = __uint_as_float(i & 1 ? u[h][2 + i / 2] & 0xffff0000u : u[h][2 + i / 2] << 16);
         }
-      } else {
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[i / 2]));
-          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[2 + i / 2]));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[h][i / 2]));
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[h][2 + i / 2]));
           s[i][h] = x.x, s[i + 1][h] = x.y, b[i][h] = y.x, b[i + 1][h] = y.y;
         }
-      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (BF) b[i][h] = fmaf(-16.f, s[i][h], b[i][h]);
         else s[i][h] *= 16777216.f;
       }
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!FULL && i >= left) break;
@@ -302,25 +327,22 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
       const uint2 c1 = *reinterpret_cast<const uint2*>(st + code_lane + 8 * kPitch + i * 32);
       float acc[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint32_t w0 = half ? c0.y : c0.x, w1 = half ? c1.y : c1.x;
         uint32_t a[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          a[k][0] = codes_of<BF>(w0, 2 * k);
-          a[k][1] = codes_of<BF>(w1, 2 * k);
-          a[k][2] = codes_of<BF>(w0, 2 * k + 1);
-          a[k][3] = codes_of<BF>(w1, 2 * k + 1);
+          a[k][0] = codes(w0, 2 * k);
+          a[k][1] = codes(w1, 2 * k);
+          a[k][2] = codes(w0, 2 * k + 1);
+          a[k][3] = codes(w1, 2 * k + 1);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint4 x = *reinterpret_cast<const uint4*>(xq + (i * 2 + half) * (TB * 64) + n * 512);
-          mma16816<BF>(acc[n], a[0], x.x, x.y);
-          mma16816<BF>(acc[n], a[1], x.z, x.w);
+          if (half == 0) mma16816<BF, false>(acc[n], a[0], x.x, x.y);
+          else mma16816<BF, true>(acc[n], a[0], x.x, x.y);
+          mma16816<BF, true>(acc[n], a[1], x.z, x.w);
         }
       }
 #pragma unroll
@@ -343,8 +365,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
 
   // y of a block: `parts` partial results at `src` (a warp's own, a CTA's, the cluster's)
   auto put = [&](int t, int o, float v) {
-    if (!XS && p.xs) v *= __ldg(p.xs + q.t0 + t);
-    const long long at = (q.t0 + t) * p.y_ts + o;
+    if (!XS && p.xs) v *= __ldg(p.xs + t0 + t);
+    const long long at = (t0 + t) * p.y_ts + o;
     if (p.y_dtype == STEP_BF16) static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
     else if (p.y_dtype == STEP_F16) static_cast<__half*>(p.y)[at] = __float2half_rn(v);
     else static_cast<float*>(p.y)[at] = v;
@@ -352,6 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
 
   int slot = 0;
   for (int block = first; block < q.blocks; block += stride) {
+    if (ALONE && row_of(block) >= p.O) break;  // (nor has this warp a tile in later blocks)
     for (int quad = 0; quad < quads; ++quad) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // the stage is there for all lanes, and the one before has been read
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
       }
     if constexpr (ALONE) {
       __syncwarp();
-      const int o = block * rows + wr * 16 + (lane & 15);
+      const int o = row_of(block) + (lane & 15);
       if (o < p.O)
         for (int t = lane >> 4; t < tokens; t += 2) put(t, o, out[t * PITCH + (lane & 15)]);
       __syncwarp();
@@ -427,12 +450,12 @@ __global__ void __launch_bounds__(32 * kWarps, NT <= 4 ? 2 : 1)
 }
 
 template <int NT, bool BF, bool XS, bool ALONE>
-cudaError_t launch_t(const Plan4& q, int grid, int smem, cudaStream_t st) {
+cudaError_t launch_t(const Plan4& q, dim3 grid, int smem, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem((const void*)linear4_kernel<NT, BF, XS, ALONE>, 232448 - 1024, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)grid);
+  c.gridDim = grid;
   c.blockDim = dim3(32 * kWarps);
   c.dynamicSmemBytes = smem;
   c.stream = st;
@@ -446,7 +469,7 @@ cudaError_t launch_t(const Plan4& q, int grid, int smem, cudaStream_t st) {
   return cudaLaunchKernelEx(&c, linear4_kernel<NT, BF, XS, ALONE>, q);
 }
 template <int NT>
-cudaError_t launch_nt(const Plan4& q, int grid, int smem, cudaStream_t st) {
+cudaError_t launch_nt(const Plan4& q, dim3 grid, int smem, cudaStream_t st) {
   const bool alone = q.wk == 1 && q.cluster == 1, bf = q.a.x_dtype == STEP_BF16;
   const bool xs = q.a.xs && q.a.xg < q.a.K;
   if (bf) return alone ? launch_t<NT, true, false, true>(q, grid, smem, st) : launch_t<NT, true, false, false>(q, grid, smem, st);
@@ -464,39 +487,25 @@ cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st) {
   q.a = p;
   q.parts = p.K / 64;
   constexpr int kRing = kWarps * kStages * kStage;
-  constexpr int kRoom = 220 * 1024 - kRing;  // for the tokens and the partial results
-  auto x_bytes = [](int parts, int nt) { return (long long)parts * 8 * nt * (128 + 8); };
-  auto red_bytes = [](int nt) { return kWarps * 8 * nt * 20 * 4; };
+  constexpr int kRoom = 226 * 1024 - kRing;  // for the tokens and the partial results
   auto slice = [&](int c) { return round4((q.parts + c - 1) / c); };
-  // tokens of a launch: as many as shared memory holds beside an eighth of K
-  int nt = 8;
-  while (nt > 1 && 8 * (nt / 2) >= p.T) nt /= 2;
-  if (nt == 8 && p.T <= 48) nt = 6;
-  while (nt > 1 && x_bytes(slice(8), nt) + red_bytes(nt) > kRoom) nt = nt == 6 ? 4 : nt / 2;
+  auto bytes = [&](int c, int nt) {
+    return (long long)slice(c) * 8 * nt * (128 + 8) + kWarps * 8 * nt * 20 * 4;
+  };
+  // 8 or 16 tokens a CTA (8 where an eighth of K leaves no room for more)
+  const int nt = p.T <= 8 || bytes(8, 2) > kRoom ? 1 : 2, groups = (p.T + 8 * nt - 1) / (8 * nt);
+  const int red = kWarps * 8 * nt * 20 * 4;
   const int tiles = (p.O + 15) / 16;
-  // The split with the least rounds x (parts of a warp + what a block costs besides, as
-  // much as 6 parts), and, where there are few blocks, the tokens' layout, which every CTA
-  // does anew (@LAYOUT@).
-  double best = 1e30;
-  for (int c = 1; c <= 8; c *= 2) {
-    if (x_bytes(slice(c), nt) + red_bytes(nt) > kRoom || (c > 1 && slice(c / 2) <= 4)) continue;
-    for (int wk = 1; wk <= kWarps; wk *= 2) {
-      if (wk > 1 && slice(c) <= 4 * wk / 2) continue;
-      const int blocks = (tiles + kWarps / wk - 1) / (kWarps / wk);
-      const int smem = (int)x_bytes(slice(c), nt) + kRing + red_bytes(nt);
-      const int per_sm = std::max(1, std::min(nt <= 4 ? 2 : 1, 227 * 1024 / (smem + 1024)));
-      // (clusters leave some SMs without a CTA)
-      const double slots = sms * per_sm / c * (c == 8 ? 0.8 : c == 4 ? 0.9 : 1.0);
-      const double rounds = std::ceil(blocks / std::max(slots, 1.0));
-      const double cost = rounds * (round4((slice(c) + wk - 1) / wk) * (1 + 0.25 * nt) + 6 + (c > 1 ? 8 : 0)) +
-                          slice(c) * nt * 0.5;
-      if (cost < best) {
-        best = cost;
-        q.cluster = c;
-        q.wk = wk;
-      }
-    }
-  }
+  // CTAs of a cluster while their slice of the tokens does not fit; slices of K in a CTA
+  // until the CTAs fill more than half of the SMs, or a warp has four parts left (GPU time:
+  // 2047 x 4096, one token, 16 slices 11.4 us, 8 slices 13.4, one 25.8; 12288 x 2048 2 and
+  // 96 CTAs 13.4, one 17.5, 4 15.5; 32768 x 2048 one 17.6, 2 19.6).
+  q.cluster = 1;
+  while (q.cluster < 8 && bytes(q.cluster, nt) > kRoom) q.cluster *= 2;
+  q.wk = 1;
+  while (q.wk < kWarps && slice(q.cluster) > 4 * q.wk &&
+         (long long)tiles * q.wk * q.cluster * groups * 10 < 6ll * sms * kWarps)
+    q.wk *= 2;
   q.wr = kWarps / q.wk;
   q.cta_parts = slice(q.cluster);
   q.warp_parts = round4((q.cta_parts + q.wk - 1) / q.wk);
@@ -506,22 +515,12 @@ cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st) {
   q.off_xs = q.off_sum + q.cta_parts * 8 * nt * 4;
   q.off_ring = q.off_xs + q.cta_parts * 8 * nt * 4;
   q.off_red = q.off_ring + kRing;
-  const int smem = q.off_red + red_bytes(nt);
-  const int per_sm = std::max(1, std::min(nt <= 4 ? 2 : 1, 227 * 1024 / (smem + 1024)));
-  const int most = std::max(1, sms * per_sm / q.cluster);
-  const int grid = std::min(q.blocks, most) * q.cluster;
-  for (q.t0 = 0; q.t0 < p.T; q.t0 += 8 * nt) {
-    cudaError_t e = cudaSuccess;
-    switch (nt) {
-      case 1: e = launch_nt<1>(q, grid, smem, st); break;
-      case 2: e = launch_nt<2>(q, grid, smem, st); break;
-      case 4: e = launch_nt<4>(q, grid, smem, st); break;
-      case 6: e = launch_nt<6>(q, grid, smem, st); break;
-      default: e = launch_nt<8>(q, grid, smem, st); break;
-    }
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const int smem = q.off_red + red;
+  const int ctas = std::min(q.blocks, std::max(1, sms / q.cluster / groups));
+  // (a warp alone takes every so many row tiles, so that the last round is every SM's)
+  if (q.wk == 1 && q.cluster == 1) q.blocks = (tiles + kWarps * ctas - 1) / (kWarps * ctas) * ctas;
+  const dim3 grid(ctas * q.cluster, groups);
+  return nt == 1 ? launch_nt<1>(q, grid, smem, st) : launch_nt<2>(q, grid, smem, st);
 }
 
 }  // namespace moe

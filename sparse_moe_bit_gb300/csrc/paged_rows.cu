@@ -786,65 +786,79 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, int n, const Seq&
 }
 
 // Where groups of sequences share keys (g: the groups as a batch): the parts over the
-// group's keys, then those over the sequence's own.  Every row of a sequence is written here.
+// group's keys, then those over the sequence's own.  Every row of a sequence is written
+// here, by W warps; where one is enough for a row's parts a CTA has four rows.
 struct SharedJoin {
   AttnParams p, g;
   const int2* of_token;  // a new token's sequence and group
 };
 template <int D, bool BF, int W>
-__global__ void __launch_bounds__(32 * W)
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
     paged_join_shared_kernel(const __grid_constant__ SharedJoin jp) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, ROWS = W == 1 ? 4 : 1;  // features of a lane; rows of a CTA
   __shared__ float sh_o[W][D];
   __shared__ float sh_l[W];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
   const AttnParams &p = jp.p, &g = jp.g;
-  const long long rid = blockIdx.x;
-  const int t = (int)(rid / p.Hq), head = (int)(rid - (long long)t * p.Hq);
+  const long long rid = (long long)blockIdx.x * ROWS + (W == 1 ? threadIdx.x >> 5 : 0);
+  const bool any = rid < (long long)p.b.T * p.Hq;
+  const int t = any ? (int)(rid / p.Hq) : 0, head = any ? (int)(rid - (long long)t * p.Hq) : 0;
   // (what no sequence holds has any number here: it is looked at before it is used)
   const int2 of = jp.of_token[t];
-  const int n = of.x >= 0 && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
+  const int n = any && of.x >= 0 && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
   const Seq s = load_seq(p.b, max(n, 0)), gs = load_seq(g.b, max(k, 0));
   // (as above: no CTA leaves before it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
-  const Parts own = parts_of<D>(p, n, s, t, head), grp = parts_of<D>(g, k, gs, t, head);
-  const int first = grp.n, parts = first + own.n;
-  auto ml = [&](int c) { return c < first ? grp.ml[grp.slot(c)] : own.ml[own.slot(c - first)]; };
+  const Parts grp = parts_of<D>(g, k, gs, t, head), own = parts_of<D>(p, n, s, t, head);
   float m = kNegInf;
-  for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml(c).x);
+  for (int c = lane; c < grp.n; c += 32) m = fmaxf(m, grp.ml[grp.slot(c)].x);
+  for (int c = lane; c < own.n; c += 32) m = fmaxf(m, own.ml[own.slot(c)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   const float u = m == kNegInf ? 0.f : m;
   float l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int c = warp; c < parts; c += W) {
-    const float2 x = ml(c);
-    const float* po = c < first ? grp.o + grp.slot(c) * D : own.o + own.slot(c - first) * D;
-    const float a = exp2_approx(x.x - u);
-    l += a * x.y;
-    if (x.y != 0.f) {  // (a part without keys need not hold numbers; NaN sums pass)
+  auto add = [&](const Parts& x, int first) {
+#pragma unroll 4
+    for (int c = first; c < x.n; c += W) {
+      const float2 y = x.ml[x.slot(c)];
+      const float* po = x.o + x.slot(c) * D;
+      const float a = exp2_approx(y.x - u);
+      l += a * y.y;
+      if (y.y != 0.f) {  // (a part without keys need not hold numbers; NaN sums pass)
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += a * po[e * 32 + lane];
+        for (int e = 0; e < E; ++e) acc[e] += a * po[e * 32 + lane];
+      }
+    }
+  };
+  add(grp, warp);
+  add(own, (warp + W - grp.n % W) % W);
+  float total = l;
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) sh_l[warp] = l;
+    __syncthreads();
+    total = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) total += sh_l[w];
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  uint16_t* const o = p.o + t * p.o_ts + head * p.o_hs;
+  if constexpr (W == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e * 32 + lane] = pack1<BF>(acc[e] * inv);
+  } else {
+    for (int f = threadIdx.x; f < D; f += 32 * W) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += sh_o[w][f];
+      o[f] = pack1<BF>(v * inv);
     }
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) sh_l[warp] = l;
-  __syncthreads();
-  float total = 0.f;
-#pragma unroll
-  for (int w = 0; w < W; ++w) total += sh_l[w];
-  const float inv = total == 0.f ? 0.f : 1.f / total;
-  for (int f = threadIdx.x; f < D; f += 32 * W) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v += sh_o[w][f];
-    p.o[t * p.o_ts + head * p.o_hs + f] = pack1<BF>(v * inv);
-  }
-  if (threadIdx.x == 0 && p.lse)
+  if ((W == 1 ? lane : threadIdx.x) == 0 && p.lse)
     p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
 }
 
@@ -882,11 +896,11 @@ cudaError_t rows_launch(const AttnParams& p, cudaStream_t st) {
   return tma ? rows_launch_t<D, 2, BF, true>(rp, st) : rows_launch_t<D, 2, BF, false>(rp, st);
 }
 
-// A CTA a row, set up while the partial results are still being computed.
+// set up while the partial results are still being computed
 template <typename P>
-cudaError_t join_w(void (*kern)(P), int warps, const AttnParams& p, const P& params, cudaStream_t st) {
+cudaError_t join_w(void (*kern)(P), long long ctas, int warps, const P& params, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)((long long)p.b.T * p.Hq));
+  c.gridDim = dim3((unsigned)ctas);
   c.blockDim = dim3(32 * warps);
   c.stream = st;
   cudaLaunchAttribute a[1];
@@ -901,15 +915,19 @@ template <int D, bool BF>
 cudaError_t join_launch(const AttnParams& p, cudaStream_t st) {
   // a warp for four parts or so: a row's parts, a kilobyte each at D = 256, are
   // read in as many rounds of latency as a warp has parts
-  if (p.parts <= 16) return join_w(paged_join_kernel<D, BF, 4>, 4, p, p, st);
-  return join_w(paged_join_kernel<D, BF, 32>, 32, p, p, st);
+  const long long rows = (long long)p.b.T * p.Hq;
+  if (p.parts <= 16) return join_w(paged_join_kernel<D, BF, 4>, rows, 4, p, st);
+  return join_w(paged_join_kernel<D, BF, 32>, rows, 32, p, st);
 }
 template <int D, bool BF>
 cudaError_t join_shared_launch(const AttnParams& p, const AttnParams& g, const int2* of_token,
                                cudaStream_t st) {
   const SharedJoin jp{p, g, of_token};
-  if (p.parts + g.parts <= 32) return join_w(paged_join_shared_kernel<D, BF, 4>, 4, p, jp, st);
-  return join_w(paged_join_shared_kernel<D, BF, 32>, 32, p, jp, st);
+  const long long rows = (long long)p.b.T * p.Hq;
+  const int parts = p.parts + g.parts;
+  if (parts <= 8) return join_w(paged_join_shared_kernel<D, BF, 1>, (rows + 3) / 4, 4, jp, st);
+  if (parts <= 32) return join_w(paged_join_shared_kernel<D, BF, 8>, rows, 8, jp, st);
+  return join_w(paged_join_shared_kernel<D, BF, 32>, rows, 32, jp, st);
 }
 
 }  // namespace

@@ -102,7 +102,8 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_ts, const
   if (x_group > 0 && x_group != K && x_group % 64)
     return fail(MOE_ERR_UNSUPPORTED, "x_group of %d (a multiple of 64 is supported)", x_group);
   if (K > kLinear4MaxK) return fail(MOE_ERR_UNSUPPORTED, "K above %d", kLinear4MaxK);
-  if (O > (1 << 30) || T > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "O or T above 2^30");
+  if (O > (1 << 30) || T > kLinear4MaxT)
+    return fail(MOE_ERR_UNSUPPORTED, "O above 2^30 or T above %d", kLinear4MaxT);
   if (T == 0) return MOE_OK;
   if (!x || !codes || !scale || !bias || !y || is8(x_dtype) != (x_scale != nullptr))
     return fail(MOE_ERR_INVALID_ARG, "NULL tensor, or x_scale without an 8-bit x");

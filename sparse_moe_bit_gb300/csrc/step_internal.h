@@ -39,7 +39,7 @@ struct Linear4Params {
   int x_dtype, y_dtype, bf_scale;
   int T, K, O, group, xg;
 };
-constexpr int kLinear4MaxK = 65536;
+constexpr int kLinear4MaxK = 36864, kLinear4MaxT = 8 * 65535;
 cudaError_t launch_linear4(const Linear4Params& p, cudaStream_t st);
 
 // ---- sampling (sample.cu)

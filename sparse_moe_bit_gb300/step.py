@@ -139,7 +139,7 @@ def linear4(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, bias: tor
 
     x is bf16 or fp16 (y of its type unless ``out_dtype`` says otherwise), or e4m3 or int8
     with ``x_scale`` fp32 [T, K / x_group] (y is bf16 unless told), as rms_norm returns
-    them.  Made for a decode batch: the weights are read once for every 64 tokens."""
+    them.  Made for a decode batch: every 16 tokens read the weights anew."""
     if x.dim() != 2 or codes.dim() != 2 or scale.dim() != 2:
         raise ValueError("x, codes and scale must have two axes")
     T, K = x.shape

@@ -58,7 +58,7 @@ def test_sizes(K, O):
 
 
 @pytest.mark.parametrize("T,K,O", [(1, 2048, 5120), (37, 4096, 2047), (8, 2048, 20001), (64, 4096, 300), (64, 8192, 130),
-                                   (50, 6208, 130), (5, 65536, 40), (9, 65536, 17), (1, 128, 40000), (40, 64, 20000)])
+                                   (50, 6208, 130), (5, 36864, 40), (9, 36864, 17), (1, 128, 40000), (40, 64, 20000)])
 def test_splits_of_rows_and_of_k(T, K, O):
     _case(T, K, O)
 

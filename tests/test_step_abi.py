@@ -69,7 +69,8 @@ def _linear(lib, **kw):
     (dict(K=100, group=50), 2), (dict(x_group=64), 1), (dict(x_dtype=4), 1), (dict(x_scale=_D), 1),
     (dict(x_dtype=4, x_scale=_D, x_group=96), 1), (dict(x_dtype=5, x_scale=_D, x_group=32), 2),
     (dict(x_dtype=4, x_scale=_D + 2), 1), (dict(x=_A + 8), 1), (dict(x_ts=260), 1), (dict(codes=_B + 8), 1),
-    (dict(scale=_C + 2), 1), (dict(y=0x50001), 1), (dict(K=65600), 2), (dict(O=(1 << 30) + 1), 2)])
+    (dict(scale=_C + 2), 1), (dict(y=0x50001), 1), (dict(K=36928), 2), (dict(O=(1 << 30) + 1), 2),
+    (dict(T=524281), 2)])
 def test_linear4_rejects_bad_arguments(lib, kw, status):
     assert _linear(lib, **kw) == status, lib.moe_last_error()
     assert lib.moe_last_error()
