@@ -181,8 +181,10 @@ struct Plan {
 //
 // The keys that a group shares may be read again for every 16 rows where that is little:
 // 256-row tiles take some 10 us more than small ones before their first product (4
-// continuations of 1501 keys, 16/2 heads of 256, 2 tiles of 16 rows: @FEW@).
-constexpr long long kReread = 48ll << 20;
+// continuations of 1501 keys, 16/2 heads of 256, 2 tiles of 16 rows: 25 us a call's
+// kernels, 30 with 256-row tiles).  Their split over the keys goes by the tiles that are
+// likely there (5 groups, 57 sequences, 24/8 heads of 128: 84 us, 92 without).
+constexpr double kReread = 48 << 20;
 Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q, int max_kv,
           bool group = false) {
   Plan r{};
@@ -193,7 +195,7 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
   if (kv > b.capacity) kv = b.capacity;
   r.wide = mq * G > (max_q > 0 || b.T <= b.N ? kRowTile : kRowTile / 2);
   if (group && r.wide)
-    r.wide = (mq * G + kRowTile - 1) / kRowTile * b.N * kv * c.heads * c.dim * 4 > kReread;
+    r.wide = (double)((mq * G + kRowTile - 1) / kRowTile) * b.N * kv * c.heads * c.dim * 4 > kReread;
   r.row_tile = mq * G <= 8 ? 8 : kRowTile;
   const long long rows = r.wide ? kPairRows : r.row_tile;
   long long span = kv;
@@ -206,6 +208,10 @@ Plan plan(const CacheView& c, const BatchView& b, int Hq, int window, int max_q,
     if (tiles < 1) tiles = 1;
     const long long items = tiles * c.heads;
     long long chunks = device_sms() / 2 / items;
+    if (group) {  // (of the tiles that each group may have beyond its rows half are there)
+      const long long likely = (((long long)b.T * G + rows - 1) / rows + b.N / 2) * c.heads;
+      chunks = (device_sms() / 2 + likely / 2) / likely;
+    }
     if (chunks < 1) chunks = 1;
     long long chunk = (span + chunks - 1) / chunks;
     chunk = (chunk + 127) / 128 * 128;
