@@ -44,7 +44,7 @@ enum { STEP_BF16 = 1, STEP_F16 = 2, STEP_F32 = 3, STEP_E4M3 = 4, STEP_I8 = 5 };
  *           residual is.  sum may be residual or x, and y may be x, with the same
  *           type and strides (in place); otherwise no output may overlap another
  *           array.
- *   weight  dtype or fp32 [d], or NULL (ones)
+ *   weight  dtype or fp32 [d], or NULL (ones; without unit_offset)
  *   y       y_dtype, any of the five
  *   scales  fp32 [T][H][d / group] dense for an 8-bit y, else NULL
  *   group   divides d for an 8-bit y (0: d), else 0
@@ -69,7 +69,7 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *   x_scale fp32 [T][K / x_group] dense for an 8-bit x, else NULL; x_group: K or
  *           a multiple of 64 that divides K (0: K)
  *   codes   uint8 [O][K / 2], scale and bias 16-bit (MOE_SCALE_F16 or _BF16)
- *           [O][K / group], all dense, 16-byte aligned
+ *           [O][K / group], all dense, 16-byte aligned; scales below 2^100
  *   group   a multiple of 64 that divides K
  *   y       BF16, F16 or F32 [T][O], rows y_token_stride elements apart; may not
  *           overlap x

@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
   __shared__ float sh_sum[2][W];  // by turns
   extern __shared__ uint32_t row_max[];  // [ROWS][groups]
   const int tid = W == 1 ? threadIdx.x & 31 : threadIdx.x, slot = W == 1 ? threadIdx.x >> 5 : 0;
-  const int d = p.d, rows = p.T * p.H;
+  const int d = p.d;
+  const unsigned rows = (unsigned)p.T * (unsigned)p.H;  // below 2^31 - 4
   // The weights stay in registers over a CTA's rows where they are few.
   constexpr bool HOLD = CH * VEC <= 16;
   auto weights = [&](int i, float (&w)[VEC]) {
@@ -158,7 +159,8 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
   }
   int turn = 0;
 #pragma unroll 1
-  for (int row = blockIdx.x * ROWS + slot; row < rows; row += gridDim.x * ROWS) {
+  for (unsigned at = blockIdx.x * ROWS + slot; at < rows; at += gridDim.x * ROWS) {
+    const int row = (int)at;
     const int t = fast_div(row, p.div_h), h = row - t * p.H;
     const long long xo = t * p.x_ts + h * p.x_hs, yo = t * p.y_ts + h * p.y_hs;
     // (a row's loads are all in flight before the first is waited for)

@@ -41,6 +41,7 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_ts,
   if (!size_of(y_dtype)) return fail(MOE_ERR_INVALID_ARG, "y_dtype %d", y_dtype);
   if (weight && weight_dtype != dtype && weight_dtype != STEP_F32)
     return fail(MOE_ERR_INVALID_ARG, "weight_dtype %d", weight_dtype);
+  if (!weight && unit_offset) return fail(MOE_ERR_INVALID_ARG, "unit_offset without a weight");
   if (T < 0 || H < 1 || d < 1) return fail(MOE_ERR_INVALID_ARG, "bad size (T=%d H=%d d=%d)", T, H, d);
   if (!(eps >= 0) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and not negative");
   if (is8(y_dtype) ? group < 0 || (group > 0 && d % group) : group != 0)

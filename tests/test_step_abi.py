@@ -49,7 +49,8 @@ def _norm(lib, **kw):
     (dict(y_dtype=5, scales=_B + 0x90000, group=-1), 1), (dict(scales=_B + 0x90000), 1), (dict(r=None), 1),
     (dict(s=None), 1), (dict(x=_A + 1), 1), (dict(w=_D + 1), 1), (dict(y=_A, y_ts=256), 1),
     (dict(y=_A, y_dtype=3), 1), (dict(y=_A, s=_A), 1), (dict(y=_C), 1), (dict(y=_B), 1), (dict(s=_B, s_ts=64), 1),
-    (dict(s=_A, s_hs=128), 1), (dict(T=1 << 30, H=4), 2)])
+    (dict(s=_A, s_hs=128), 1), (dict(T=1 << 30, H=4), 2),
+    (dict(w=None, unit=1), 1), (dict(T=(1 << 31) - 4, H=1), 2)])
 def test_norm_rejects_bad_arguments(lib, kw, status):
     assert _norm(lib, **kw) == status, lib.moe_last_error()
     assert lib.moe_last_error()
