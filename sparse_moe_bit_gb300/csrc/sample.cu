@@ -460,8 +460,10 @@ __device__ bool settle_n(Shared& sh, const Row& r, const View& w, int k, float t
 __device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top_p, unsigned long long total,
                        unsigned long long above, uint32_t& thr, int& cut) {
   __syncthreads();
-  return w.n <= kThreads ? settle_n<1>(sh, r, w, k, top_p, total, above, thr, cut)
-                         : settle_n<kList / kThreads>(sh, r, w, k, top_p, total, above, thr, cut);
+  static_assert(kList == 4 * kThreads, "tokens of a thread");
+  if (w.n <= kThreads) return settle_n<1>(sh, r, w, k, top_p, total, above, thr, cut);
+  if (w.n <= 2 * kThreads) return settle_n<2>(sh, r, w, k, top_p, total, above, thr, cut);
+  return settle_n<4>(sh, r, w, k, top_p, total, above, thr, cut);
 }
 
 // what is kept: tokens above `thr`, of its own the ones up to index `cut`, and none of a
@@ -905,6 +907,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t sample_launch(const SampleParams& p, cudaStream_t st) {
+  // CTAs of a row: until two slices fit an SM, and while they are no more than run at once
+  // with half as many for each (48 rows of 65521: 8 CTAs each 34 us, although the last rows
+  // wait for the first; 4 each 39)
   const int sms = device_sms();
   int cluster = 1;
   while (cluster < kMaxCluster && (p.V > 24576 * cluster || (p.V > 2048 * cluster && (long long)p.B * cluster < 2 * sms)))
