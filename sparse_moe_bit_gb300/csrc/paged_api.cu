@@ -559,6 +559,7 @@ moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int
   g.split = r.g.wide;
   g.causal = 0;
   g.flat = 1;
+  g.early = 1;
   g.b.N = groups;
   g.b.cu = gv.cu;
   g.b.kv_len = gv.len;

@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Bars<D> B{sm + C::OFF_BAR};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -375,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     late_wait(p);
   };
 
+  early_wait(p);
   int bid = blockIdx.x >> 1;
   const int ck = bid % p.chunks;
   bid /= p.chunks;
@@ -957,7 +957,7 @@ cudaError_t chunk_launch_t(const ChunkParams& cp, cudaStream_t st) {
   a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[1].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
-  c.numAttrs = p.late ? 2 : 1;
+  c.numAttrs = p.late || p.early ? 2 : 1;
   return cudaLaunchKernelEx(&c, paged_chunk_kernel<D, BF, TMA>, cp);
 }
 

@@ -138,10 +138,17 @@ struct AttnParams {
   // depends on in nothing: it waits for that one before it ends, so that who waits for
   // this kernel has waited for both
   int late;
+  // ... this kernel is set up while the one before it still runs, whose results it reads
+  int early;
   int* err;
 };
 __device__ __forceinline__ void late_wait(const AttnParams& p) {
   if (p.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The kernel behind may start from here on: what it reads of the one before this is there.
+__device__ __forceinline__ void early_wait(const AttnParams& p) {
+  if (p.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // The first key in a query's window.  (A query before position 0 sees none; its
 // position less a window near 2^31 would not fit.)

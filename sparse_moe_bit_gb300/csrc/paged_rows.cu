@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ long long sh_warp[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the join may be set up while this grid runs
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  early_wait(p);
 
   // ---- groups before each slice of `per` sequences; CTA 0 leaves the sums for
   // the join
@@ -877,7 +877,7 @@ cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
-  c.numAttrs = rp.a.late ? 1 : 0;
+  c.numAttrs = rp.a.late || rp.a.early ? 1 : 0;
   return cudaLaunchKernelEx(&c, paged_rows_kernel<D, NB, BF, TMA>, rp);
 }
 

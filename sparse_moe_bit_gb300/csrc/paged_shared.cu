@@ -12,6 +12,8 @@ constexpr int kThreads = 128;
 // where fewer than two of them have new tokens.
 __global__ void __launch_bounds__(kThreads) groups_kernel(const BatchView b, const GroupView g) {
   __shared__ int sh_first, sh_least, sh_with, sh_at;
+  // the attention over the shared keys may be set up meanwhile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int me = blockIdx.x;
   if (threadIdx.x == 0) {
     sh_first = b.N;
