@@ -328,6 +328,16 @@ __device__ __forceinline__ void tma_box_pair(uint32_t dst, const CUtensorMap* tm
       : "memory");
 }
 
+// A sector of memory at once: lanes that write a row each, rows apart, fill no sector
+// with 16-byte stores, and the second half of each is a write of its own (48 continuations of
+// 16384 shared keys, 768 rows of 25 parts: 53.5 us so, 49.6 by sectors).  A workspace may lie
+// between two sectors: it is asked at the store.
+__device__ __forceinline__ void st_sector(float* d, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // TMA: whole boxes of the cache are copied by the tensor memory accelerator;
 // otherwise (pages that no box of 8 rows divides) by 16-byte copies alone.
 template <int D, bool BF, bool TMA>
@@ -901,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a part of a row: for a join that divides by the sum of the l)
       const float inv = l == 0.f ? 0.f : (p.split ? l : 1.f) / (l + extra);
       const float mlog = fmaf(m, c, -kShift<BF>);  // (-inf: no key seen)
+      const bool sectors = reinterpret_cast<uintptr_t>(p.part_o) % 32 == 0;
 #pragma unroll 1
       for (int f0 = 0; f0 < D / 4; f0 += 16) {
         const int f = part * (D / 4) + f0;
@@ -909,11 +920,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         if (!valid) continue;
         if (p.split) {
-          float4* d4 = reinterpret_cast<float4*>(p.part_o + (rid * p.chunks + ck) * D + f);
+          float* const d = p.part_o + (rid * p.chunks + ck) * D + f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            d4[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          if (sectors) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) st_sector(d + i, o + i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(d + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
         } else {
           uint16_t* dst = p.o + (s.t0 + tok) * p.o_ts + head * p.o_hs + f;
 #pragma unroll

@@ -234,6 +234,23 @@ def test_workspace_of_the_caller():
         attend(b, workspace=ws[:n.value - 1])
 
 
+@pytest.mark.parametrize("dim", [64, 256])
+def test_a_workspace_at_any_sixteen_bytes(dim):
+    """Parts are written a sector at once where the workspace lies on one, in halves elsewhere."""
+    b, new, kv = batch(23, [40], [3000], 30, 4, 16, 2, dim, BF, 16)
+    plain = [b[x] for x in ("q", "k", "v", "table", "cu", "kv_len")]
+    first = attend(b, **hints(b, new, kv))[0], M.paged_attention(*plain)
+    ws = torch.zeros((64 << 20) + 64, dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 32 == 0
+    for at in (0, 16, 32, 48):
+        o, _ = attend(b, workspace=ws[at:], **hints(b, new, kv))
+        assert torch.equal(o, first[0])
+        assert torch.equal(M.paged_attention(*plain, workspace=ws[at:]), first[1])
+    torch.cuda.synchronize()
+    assert M.paged_device_error() == 0
+    check(b, kv, workspace=ws[16:], **hints(b, new, kv))
+
+
 def test_next_to_fork_and_reserve():
     """The serving path: a prompt is forked, pages reserved and copied on write, new keys
     appended, and the continuations attend together."""
