@@ -38,7 +38,8 @@ enum { STEP_BF16 = 1, STEP_F16 = 2, STEP_F32 = 3, STEP_E4M3 = 4, STEP_I8 = 5 };
  *   nearest, ties to even;  y = 0 and scale = 0 where the group is all zeros
  * so that y * scale stands for n.  NaN and infinities reach the group's scale
  * (the scale of a group with either is not finite).  Squares are fp32's: of
- * magnitudes above 1e19 the mean is infinite and n is 0.
+ * magnitudes above 1e19 the mean is infinite and n is 0, of rows below 1e-22 it is 0
+ * and n goes by eps alone (with eps 0 an infinity, and NaN where s is 0).
  *   x, residual, sum  `dtype` (BF16, F16 or F32) [T][H][d]; features contiguous,
  *           token and head strides in elements.  sum: NULL exactly where
  *           residual is.  sum may be residual or x, and y may be x, with the same
@@ -66,6 +67,9 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *   x       [T][K]: BF16 or F16, or E4M3 or I8 with scales: x stands for
  *           x * x_scale[t][k / x_group].  Rows x_token_stride elements apart,
  *           16-byte aligned (the base and every row).
+ *           Magnitudes below 2^110; a token that holds a NaN or an infinity has a
+ *           y without finite numbers (NaN also where the formula has an infinity)
+ *           and changes no other token's.
  *   x_scale fp32 [T][K / x_group] dense for an 8-bit x, else NULL; x_group: K or
  *           a multiple of 64 that divides K (0: K)
  *   codes   uint8 [O][K / 2], scale and bias 16-bit (MOE_SCALE_F16 or _BF16)

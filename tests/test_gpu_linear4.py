@@ -116,6 +116,27 @@ def test_extreme_values():
     check(M.linear4(big, *w, out_dtype=FP), big, None, w, FP)
 
 
+@pytest.mark.parametrize("dtype,xg", [(BF, 0), (HF, 0), (E8, 0), (E8, 64), (I8, 64)], ids=str)
+@pytest.mark.parametrize("T,K,O", [(3, 256, 100), (12, 2048, 40)])
+def test_a_token_that_is_not_finite_is_alone(dtype, xg, T, K, O):
+    """(codes, scales and biases of zero among them)"""
+    codes, scale, bias = [t.cuda() for t in weights4(31, O, K, 64, BF)]
+    codes[0], scale[1], bias[2] = 0, 0, 0
+    scale[3], bias[3] = 0, 0
+    x, xs = _x(32, T, K, dtype, xg)
+    want = M.linear4(x, codes, scale, bias, x_scale=xs, out_dtype=FP)
+    bad = {1: float("nan"), 2: float("inf")}
+    for t, v in bad.items():
+        if dtype in (BF, HF) or (dtype is E8 and t == 1):
+            x[t, K - 5 * t] = v
+        else:
+            xs[t, -1] = v
+    y = M.linear4(x, codes, scale, bias, x_scale=xs, out_dtype=FP)
+    assert not torch.isfinite(y[1:3]).any()
+    keep = [t for t in range(T) if t not in bad]
+    assert torch.equal(y[keep], want[keep])
+
+
 def test_norm_and_product_in_eight_bits():
     """A layer's entry as it is used: the norm's 8 bits go into the product."""
     g = torch.Generator(device="cuda").manual_seed(9)
