@@ -27,7 +27,9 @@
 // Split: a CTA, one an SM, holds WR row tiles x WK slices of K (WR WK = 16 warps), and a
 // cluster of C CTAs splits K again where the tokens of all of K do not fit shared memory;
 // partial sums meet in shared memory, in a fixed order.
-// Measured (GPU time, weights not in L2): @FIG@
+// Measured (a graph replay's time, weights not in L2, of which some 5 us are the method's):
+// 5120 x 2048, one token 11.4 us, 8 13.4, 64 23.7; 2047 x 4096, 37 tokens of e4m3 21.6;
+// 130001 x 2048 (150 MB), one token 40, 8 42 (4.1 TB/s), 16 50, 256 597.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

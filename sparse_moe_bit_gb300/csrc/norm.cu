@@ -4,10 +4,13 @@
 //   with a scale for each group of features).
 //
 // Bound: HBM (x, r, s and y once, some 5 operations an element); a call of a few rows
-// is one launch's latency.  A row is read once and stays in registers, W warps to a
-// row: one where there are many short rows (no barrier, a row's loads all in flight at
-// once), eight or 32 where rows are few or long.  A group's largest magnitude is kept
-// as the bits of a non-negative number, whose order as integers puts NaN above
+// is one launch's latency.  A row is read once and stays in registers, two vectors of
+// eight a thread, W warps to a row; a CTA walks over rows with the weights in registers
+// and reads its next row before it is done with one.  Measured (x + r, L2 warm): 8192 rows
+// of 2048 in bf16 22.7 us (134 MB, 5.9 TB/s), to e4m3 25 (117 MB, 4.7 TB/s), fp32 49.5
+// (268 MB, 5.4 TB/s); 4096 of 4096 22.6; 65552 heads of 256, no sum, 12.5; one row 4.3.
+// A group's largest magnitude is kept as the bits of a non-negative number, whose order as
+// integers puts NaN above
 // infinity, so that neither is lost in a maximum.
 #include <algorithm>
 
@@ -130,7 +133,7 @@ constexpr int kRowsCta = 4;  // rows of a CTA whose rows are a warp's each
 // Q: y is 8-bit (row_max: the largest magnitudes of a row's groups, for W > 1 and for
 // groups that a warp's lanes do not divide evenly).
 template <typename T, int VEC, int W, int CH, bool Q>
-__global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
+__global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W, W >= 8 && CH * VEC <= 16 ? 32 / W : 1)
     norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int ROWS = W == 1 ? kRowsCta : 1, THREADS = 32 * W;
   __shared__ float sh_sum[2][W];  // by turns
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
   const int d = p.d;
   const unsigned rows = (unsigned)p.T * (unsigned)p.H;  // below 2^31 - 4
   // The weights stay in registers over a CTA's rows where they are few.
-  constexpr bool HOLD = CH * VEC <= 16;
+  constexpr bool HOLD = CH * VEC <= 16, PIPE = HOLD && CH > 1;
   auto weights = [&](int i, float (&w)[VEC]) {
     if (!p.w || i >= d) {
 #pragma unroll
@@ -157,15 +160,12 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
 #pragma unroll
     for (int c = 0; c < CH; ++c) weights((c * THREADS + tid) * VEC, hold[c]);
   }
-  int turn = 0;
-#pragma unroll 1
-  for (unsigned at = blockIdx.x * ROWS + slot; at < rows; at += gridDim.x * ROWS) {
-    const int row = (int)at;
-    const int t = fast_div(row, p.div_h), h = row - t * p.H;
-    const long long xo = t * p.x_ts + h * p.x_hs, yo = t * p.y_ts + h * p.y_hs;
-    // (a row's loads are all in flight before the first is waited for)
-    Raw<T, VEC> x[CH];
-    float v[CH][VEC];
+  // A row's loads are all in flight before the first is waited for; where a thread holds
+  // little, the next row's before this one's sum.
+  Raw<T, VEC> x[CH], r[CH];
+  auto load = [&](unsigned at) {
+    const int t = fast_div((int)at, p.div_h), h = (int)at - t * p.H;
+    const long long xo = t * p.x_ts + h * p.x_hs, ro = t * p.r_ts + h * p.r_hs;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * THREADS + tid) * VEC;
@@ -173,16 +173,27 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
       for (int k = 0; k < x[c].N; ++k) x[c].u[k] = 0;
       if (i < d) x[c].load(p.x, xo + i);
     }
+    if (!p.r) return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * THREADS + tid) * VEC;
+#pragma unroll
+      for (int k = 0; k < r[c].N; ++k) r[c].u[k] = 0;
+      if (i < d) r[c].load(p.r, ro + i);
+    }
+  };
+  unsigned at = blockIdx.x * ROWS + slot;
+  if (PIPE && at < rows) load(at);
+  int turn = 0;
+#pragma unroll 1
+  for (; at < rows; at += gridDim.x * ROWS) {
+    const int row = (int)at;
+    const int t = fast_div(row, p.div_h), h = row - t * p.H;
+    const long long yo = t * p.y_ts + h * p.y_hs;
+    if (!PIPE) load(at);
+    float v[CH][VEC];
     if (p.r) {
-      const long long ro = t * p.r_ts + h * p.r_hs, so = t * p.s_ts + h * p.s_hs;
-      Raw<T, VEC> r[CH];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int i = (c * THREADS + tid) * VEC;
-#pragma unroll
-        for (int k = 0; k < r[c].N; ++k) r[c].u[k] = 0;
-        if (i < d) r[c].load(p.r, ro + i);
-      }
+      const long long so = t * p.s_ts + h * p.s_hs;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = (c * THREADS + tid) * VEC;
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[c][e] = x[c][e];
     }
+    if (PIPE && at + gridDim.x * ROWS < rows) load(at + gridDim.x * ROWS);
     float sq = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -312,11 +324,21 @@ template <typename T, int VEC, int W, int CH>
 cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
   constexpr int ROWS = W == 1 ? kRowsCta : 1;
   const long long rows = (long long)p.T * p.H;
-  // as many CTAs as run at once (64 warps an SM, fewer where a thread holds more), each
-  // with its share of the rows
-  const long long most = (long long)device_sms() * std::max(1, (CH * VEC <= 16 ? 48 : 32) / (W == 1 ? ROWS : W));
-  const dim3 grid((unsigned)std::min((rows + ROWS - 1) / ROWS, most)), block(W == 1 ? 32 * ROWS : 32 * W);
-  if (p.y_dtype != STEP_E4M3 && p.y_dtype != STEP_I8)
+  const bool q = p.y_dtype == STEP_E4M3 || p.y_dtype == STEP_I8;
+  const dim3 block(W == 1 ? 32 * ROWS : 32 * W);
+  // as many CTAs as run at once, each with its share of the rows: it prefetches its next
+  // (8192 x 2048 to e4m3: 25 us; twice as many 26.7, a CTA a row 36)
+  static std::atomic<int> fit[2]{};
+  int each = fit[q].load(std::memory_order_relaxed);
+  if (each == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &each, q ? norm_kernel<T, VEC, W, CH, true> : norm_kernel<T, VEC, W, CH, false>, (int)block.x, 0);
+    if (e != cudaSuccess) return e;
+    each = std::max(each, 1);
+    fit[q].store(each, std::memory_order_relaxed);
+  }
+  const dim3 grid((unsigned)std::min((rows + ROWS - 1) / ROWS, (long long)each * device_sms()));
+  if (!q)
     return launch_kernel(norm_kernel<T, VEC, W, CH, false>, grid, block, 0, st, p);
   const int smem = ROWS * (p.d / p.group) * 4;
   static std::atomic<uint64_t> allowed{0};
@@ -331,9 +353,11 @@ bool aligned_to(const void* p, long long a, long long b, int es, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && a * es % bytes == 0 && b * es % bytes == 0;
 }
 
-// Rows of up to 256 features are a warp's.  Longer ones have four warps where there are
-// enough of them for every SM (8192 rows of 2048 with e4m3 @F@ us; a warp each, 46, two
-// 35, eight 35), eight where latency counts, and 32 past 8192.
+// As few warps a row as hold it in two vectors a thread (8192 x 2048 to e4m3, four warps
+// 27 us, two with four vectors 33, eight with one 34; 4096 x 4096 eight warps 24, four 27,
+// sixteen with one vector 27; 65536 x 512 one warp 46, two 47, four 56).  Where SMs have
+// few rows a thread has one vector, eight warps up to 2048 features (16 x 2048 4.3 us, 6.3
+// with four).
 template <typename T>
 cudaError_t norm_by_shape(const NormParams& p, cudaStream_t st) {
   const int es = sizeof(T), ys = p.y_dtype == STEP_F32 ? 4 : p.y_dtype <= STEP_F16 ? 2 : 1;
@@ -344,9 +368,13 @@ cudaError_t norm_by_shape(const NormParams& p, cudaStream_t st) {
   const bool many = (long long)p.T * p.H >= 4ll * device_sms();
   if (vec) {
     if (p.d <= 256) return norm_launch<T, 8, 1, 1>(p, st);
-    if (p.d <= 1024 && many) return norm_launch<T, 8, 4, 1>(p, st);
-    if (p.d <= 2048) return many ? norm_launch<T, 8, 4, 2>(p, st) : norm_launch<T, 8, 8, 1>(p, st);
-    if (p.d <= 8192) return norm_launch<T, 8, 8, 4>(p, st);
+    if (p.d <= 2048 && !many) return norm_launch<T, 8, 8, 1>(p, st);
+    if (p.d <= 512) return norm_launch<T, 8, 1, 2>(p, st);
+    if (p.d <= 1024) return norm_launch<T, 8, 2, 2>(p, st);
+    if (p.d <= 2048) return norm_launch<T, 8, 4, 2>(p, st);
+    if (p.d <= 4096) return norm_launch<T, 8, 8, 2>(p, st);
+    if (p.d <= 8192) return norm_launch<T, 8, 16, 2>(p, st);
+    if (p.d <= 16384) return norm_launch<T, 8, 32, 2>(p, st);
     return norm_launch<T, 8, 32, 4>(p, st);
   }
   if (p.d <= 256) return norm_launch<T, 1, 1, 8>(p, st);

@@ -122,6 +122,26 @@ def test_residual_in_place():
         assert torch.equal(a if target == "residual" else b, x if target == "residual" else r)
 
 
+@pytest.mark.parametrize("rows,d", [(9001, 384), (5003, 1000), (3001, 2048), (1999, 4096), (1203, 8192), (611, 16384),
+                                    (3001, 301), (1300, 4103)])
+def test_many_rows_of_a_block(rows, d):
+    """A block reads its next row before it has written one, in place too."""
+    x, r, w = _inputs((rows, d), BF, 4)
+    n, total = SO.rms_norm(values(x), values(w), values(r))
+    y, s = M.rms_norm(x, w, residual=r)
+    check(y, n, d, BF)
+    assert np.all(np.abs(values(s) - total) <= rounded_bar(total, BF) + 2.0 ** -24 * np.abs(total))
+    z, scale, s2 = M.rms_norm(x, w, residual=r, out_dtype=torch.int8)
+    check8(z, scale, n, d, d)
+    assert torch.equal(s2, s)
+    a, b = x.clone(), r.clone()
+    y2, _ = M.rms_norm(a, w, residual=b, out=a, sum_out=b)
+    assert torch.equal(a, y) and torch.equal(b, s) and y2.data_ptr() == a.data_ptr()
+    y3 = M.rms_norm(x, w)
+    M.rms_norm(x, w, out=x)
+    assert torch.equal(x, y3)
+
+
 def test_zeros_nan_and_infinity():
     x = torch.ones(6, 256, dtype=BF, device="cuda")
     x[1] = 0
