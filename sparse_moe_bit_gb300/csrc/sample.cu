@@ -27,10 +27,15 @@
 // comes from histograms over the whole row of the ordered bits (11, 11, 10 of them), of
 // counts or of weights, each level among the tokens of the bin before.
 //
-// Bound: latency for a few rows, HBM and the weights' arithmetic (some 50 operations an
-// element, once) for many.  A cluster of up to eight CTAs takes a row: each holds a slice
-// of it in shared memory, read from HBM once, and histograms, sums and positions meet
-// through distributed shared memory.
+// Bound: latency for a few rows; for many the chain of a row's steps (read, maximum,
+// histogram, its sums over the CTAs, the pass, the threshold, the draw), of which an SM has
+// two CTAs' at once, and the weights' arithmetic (some 45 instructions an element, once).
+// A cluster of up to eight CTAs takes a row: each holds a slice of it in shared memory, read
+// from HBM once, and histograms, sums and positions meet through distributed shared memory.
+// Measured (fp32 logits, a graph's replay): one row of 130001, top-k 50 and top-p 0.95
+// 18.7 us; 48 of 65521 bf16, settings of their own 34; 256 of 131072 (134 MB) greedy 66,
+// top-k 50 146, nuclei 265 to 285.  (One CTA a row after another with the next row's read
+// ahead 325, CTAs of 1024 threads 299, when this stood at 301.)
 #include <algorithm>
 
 #include "paged_internal.h"
@@ -72,8 +77,8 @@ __device__ const unsigned long long kTable1024[32] = {
     0x7d98c9e62113e1faull, 0x7d8308216b594720ull, 0x7d6d4a218cd895e5ull, 0x7d578fe5de6e95a0ull};
 
 struct __align__(16) Shared {
-  unsigned long long table[1024];  // 2^(-i/1024) in units of 2^-45
-  float tablef[1024];
+  unsigned long long table[1024];  // 2^(-i/1024) in units of 2^-46
+  float tablef[1024];              // ... of 2^-41
   union {
     unsigned long long hist[kBins];
     struct {
@@ -181,11 +186,11 @@ struct Row {
   float quarter, c_hi, c_lo;
   float bins;   // bins of x for a unit of logits
 };
+// (No branch: a weight too small to count, of a logit of -inf too, comes out as 0 at x = 47,
+// where the correction is at most 2^-10 of the table's, whatever its sum is by then.)
 __device__ __forceinline__ unsigned long long weight_of(const Shared& sh, const Row& r, float v) {
-  if (v == r.max) return kOne;
   const dflt d = df_two_sum(0.25f * v, -r.quarter);
-  const float p = d.hi * r.c_hi;  // -x
-  if (!(p > -46.f)) return 0;
+  const float p = fmaxf(d.hi * r.c_hi, -47.f);  // -x
   const float lo = fmaf(d.hi, r.c_lo, fmaf(d.lo, r.c_hi, fmaf(d.hi, r.c_hi, -p)));
   // the nearest whole number of 1024ths: in the last bits of a sum with 1.5 2^23
   const float t = fmaf(p, 1024.f, 12582912.f);
@@ -197,8 +202,10 @@ __device__ __forceinline__ unsigned long long weight_of(const Shared& sh, const 
   const float q = fmaf(lo, kLn2, fmaf(z, kLn2Lo, y * y * fmaf(y, 0x1.555556p-3f, 0.5f)));
   const float e = fmaf(z, kLn2, q);
   const int i = j & 1023, n = j >> 10;
-  const long long add = (long long)__float2int_rn(sh.tablef[i] * e * 0x1p41f) << 4;
-  return (sh.table[i] + add + (1ull << n >> 1)) >> n;
+  // twice the weight, rounded down, and then to the nearest
+  const unsigned long long w2 = sh.table[i] + (unsigned long long)((long long)__float2int_rn(sh.tablef[i] * e) << 5);
+  const unsigned long long w = ((w2 >> n) + 1) >> 1;
+  return v == r.max ? kOne : w;
 }
 // where x lies among the bins (monotone in v)
 __device__ __forceinline__ float place_of(const Row& r, float v) {
@@ -479,8 +486,8 @@ __device__ bool settle(Shared& sh, const Row& r, const View& w, int k, float top
 // Of a list of tokens in bins `first_bin` .. `last_bin`, those of the 1024th of that span in
 // which the weights reach `target`, where they do; `above` is with the weights before it.
 // (Sorting 2000 tokens takes some 12 us, this and a sort of what is left 3: 256 rows of
-// 131072, nucleus of 0.99 at temperature 2, 353 -> 308 us; where lists are short there is
-// nothing in it, and below 128 tokens a loss: 48 rows of settings of their own 35 -> 38.)
+// 131072, nucleus of 0.99 at temperature 2, 353 -> 308 us then; where lists are short there is
+// nothing in it, and from 64 tokens on a loss: 48 rows of settings of their own 35 -> 38.)
 __device__ void narrow(Shared& sh, const Row& r, View& w, int first_bin, int last_bin, unsigned long long target,
                        unsigned long long& above) {
   constexpr int E = kList / kThreads, FINE = 2 * kThreads;
@@ -640,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (tid + j * kThreads < vecs) load(tid + j * kThreads, ahead[j]);
   for (int i = tid; i < 1024; i += kThreads) {
     const unsigned long long t = __umul64hi(kTable32[i >> 5], kTable1024[i & 31]);  // 2^62 x
-    sh.tablef[i] = (float)t * 0x1p-62f;
-    sh.table[i] = (t + (1ull << (61 - kOneBit))) >> (62 - kOneBit);
+    sh.tablef[i] = (float)t * 0x1p-21f;
+    sh.table[i] = (t + (1ull << (60 - kOneBit))) >> (61 - kOneBit);
   }
   float best = -INFINITY;
   int best_at = 0x7fffffff;
@@ -882,18 +889,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if ((int)place_of(r, v) <= last_bin) take(i, v);
         }
       } else {
-#pragma unroll 2
-        for (int i = w0 + lane; i < w1; i += 32) {
-          const float v = vals[i];
-          const int b = (int)place_of(r, v);
-          const unsigned long long w = weight_of(sh, r, v);
-          sum += w;
-          if (b < first_bin) {
-            above += w;
-            if (w >= keep.least) kept += w;
-          } else if (b <= last_bin) {
-            take(i, v);
+        // (places against the band's borders as numbers: floor is monotone)
+        const float first_place = (float)first_bin, end_place = (float)(last_bin + 1);
+        auto pass = [&](auto minimum) {
+#pragma unroll 4
+          for (int i = w0 + lane; i < w1; i += 32) {
+            const float v = vals[i], x = place_of(r, v);
+            const unsigned long long w = weight_of(sh, r, v);
+            sum += w;
+            above += x < first_place ? w : 0;
+            if (minimum()) kept += x < first_place && w >= keep.least ? w : 0;
+            if (x >= first_place && x < end_place) take(i, v);
           }
+        };
+        if (keep.least > 1) {
+          pass([] { return true; });
+        } else {
+          pass([] { return false; });
+          kept = above;
         }
         sum = warp_sum(sum);
         above = warp_sum(above);
