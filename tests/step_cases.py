@@ -28,9 +28,9 @@ def weights4(seed, O, K, group, dtype):
 def linear4_bar(x, codes, scale, bias, ref, dtype, bf16):
     """Products exact; a part of 64 sums its products in four steps of 17 terms, each off by at
     most 2^-23 of their magnitudes, then three roundings a part and one a part for the sum.
-    (bf16: the codes carry 128, which scale and bias take out again.)"""
+    (bf16: the codes carry 16, which scale and bias take out again.)"""
     K = x.shape[1]
-    off = 128.0 if bf16 else 0.0
+    off = 16.0 if bf16 else 0.0
     c = np.empty((codes.shape[0], K))
     c[:, 0::2], c[:, 1::2] = codes & 15, codes >> 4
     rep = K // scale.shape[1]
