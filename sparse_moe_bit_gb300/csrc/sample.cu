@@ -977,8 +977,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (k > 0 || top_p < 1.f) {
     if (p.V + VEC <= kList) settle(sh, r, whole, k, top_p, 0, 0, keep.thr, keep.cut);
     else filter(whole);
+    work.chunk_sums(whole, kept_weight, sh.warp_kept);
+  } else {
+    unsigned long long sum = 0;
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const unsigned long long w = weight_of(sh, r, vals[i]);
+      sum += w >= keep.least ? w : 0;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) sh.warp_kept[warp] = sum;
+    __syncthreads();
   }
-  work.chunk_sums(whole, kept_weight, sh.warp_kept);
   const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
   if (rank == 0 && tid == 0) put(token, total, value);
 }
