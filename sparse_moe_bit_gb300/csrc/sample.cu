@@ -596,6 +596,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   float* vals = reinterpret_cast<float*>(smem + sizeof(Shared));
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (shared memory of another CTA is there once that has begun: waited for below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // The slices begin at 16-byte boundaries of memory: the first one's up to VEC - 1 places
   // before the row are filled with -inf, which no filter ever draws from.
   constexpr int VEC = 16 / sizeof(T);
@@ -680,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (lane == 0) sh.warp[warp] = first;
   if (tid == 0) sh.listed = sh.taken = 0;
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (tid < cluster) {
     unsigned long long m = 0;
     for (int w = 0; w < kWarps; ++w) m = max(m, sh.warp[w]);

@@ -110,6 +110,22 @@ def test_nuclei_of_all_sizes(V, scale):
     run(z.to(BF), u, p=torch.tensor([0.3, 0.8, 0.95, 0.999]), m=torch.tensor([0.0, 1e-3, 0.2, 0.0]))
 
 
+@pytest.mark.parametrize("V", [2100, 50000])
+@pytest.mark.parametrize("offset", [-20000.0, -515.0, -30.0, 30.0, 517.0, 1040.0, 3e5])
+def test_rows_far_from_zero_wide_ones_and_masked_ones(V, offset):
+    """The bins are made before a row's largest logit is known."""
+    z, u = logits(V, 5, V)
+    z = z + offset
+    z[1] = offset + (z[1] - offset) * 12        # wider than the bins of one circle
+    z[2, ::3] = float("-inf")
+    z[3, 1::2] = torch.finfo(FP).min
+    z[4, 5:] = torch.finfo(FP).min              # five tokens are left
+    for kw in (dict(p=0.9), dict(p=0.5, t=3.0), dict(k=40), dict(k=1500, p=0.95), dict(p=0.99, t=0.05),
+               dict(p=0.7, t=200.0), dict(k=V - 1, p=0.9, t=0.6)):
+        run(z, u, **kw)
+    run(z.clamp(min=-6e4).to(BF), u, p=0.9)
+
+
 def test_top_k_of_all_sizes():
     z, u = logits(9, 4, 40000)
     for k in (1, 2, 100, 1000, 2047, 2048, 2049, 3000, 39999, 40000):
