@@ -34,7 +34,7 @@
 // from HBM once, and histograms, sums and positions meet through distributed shared memory.
 // Measured (fp32 logits, a graph's replay): one row of 130001, top-k 50 and top-p 0.95
 // 18.7 us; 48 of 65521 bf16, settings of their own 34; 256 of 131072 (134 MB) greedy 66,
-// top-k 50 146, nuclei 265 to 285.  (One CTA a row after another with the next row's read
+// no filter 152, top-k 50 142, nuclei 258 to 278.  (One CTA a row after another with the next row's read
 // ahead 325, CTAs of 1024 threads 299, when this stood at 301.)
 #include <algorithm>
 
