@@ -256,11 +256,16 @@ void set_plan(AttnParams* p, const Plan& r, void* workspace) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// An attention over shared keys: two plans, of the groups as a batch and of the
-// sequences' own keys, whose results are partial, whatever their split; behind them the
-// results that a warp of the small tiles has whole, and the groups.
+// An attention over shared keys: plans of the groups as a batch and of the sequences' own
+// keys, whose results are partial, whatever their split; behind them the results that a
+// warp of the small tiles has whole, and the groups.
 struct SharedPlan {
   Plan g, p;
+  // small tiles for both: one batch of the groups and the sequences, one launch (g is its
+  // plan; 4 continuations of 1501 keys, 16/2 heads of 256: 29 us a call, 33 with a launch
+  // for each; groups of 1, 2 and 3 sequences 29 and 66)
+  bool one;
+  int N;  // sequences of the batch that g is of
   size_t at_p, whole_g, whole_p, groups, ws;
 };
 SharedPlan plan_shared(const CacheView& c, const BatchView& b, int Hq, int G, int max_q, int max_group,
@@ -271,6 +276,20 @@ SharedPlan plan_shared(const CacheView& c, const BatchView& b, int Hq, int G, in
   r.g = plan(c, gb, Hq, 0, max_group, max_shared, true);
   r.p = plan(c, b, Hq, 0, max_q, max_tail);
   const size_t rows = (size_t)b.T * Hq, row = (size_t)c.dim * 4 + 8;
+  r.one = !r.g.wide && !r.p.wide && (long long)G + b.N < 0x7ffffff0;
+  r.N = r.one ? G + 1 + b.N : G;
+  if (r.one) {
+    const int most = kRowWarps * device_sms();
+    r.g.warps = r.g.warps + r.p.warps < most ? r.g.warps + r.p.warps : most;
+    r.g.row_tile = r.g.row_tile > r.p.row_tile ? r.g.row_tile : r.p.row_tile;
+    r.g.parts = (r.g.parts + r.p.parts + 1) / 2;
+    r.g.ml = (size_t)2 * r.g.warps * kRowTile * c.dim * 4;
+    r.g.before = up256(r.g.ml + (size_t)2 * r.g.warps * kRowTile * 8);
+    r.whole_g = up256(r.g.before + ((size_t)r.N + 1) * 8);
+    r.groups = r.whole_g + up256(2 * rows * row);
+    r.ws = r.groups + (size_t)b.T * 8 + ((size_t)4 * r.N + 1) * 4;
+    return r;
+  }
   for (Plan* x : {&r.g, &r.p}) {
     if (!x->wide || x->chunks > 1) continue;
     x->ml = rows * c.dim * 4;
@@ -551,22 +570,33 @@ moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int
   gv.G = groups;
   gv.of_token = reinterpret_cast<int2*>(ws + r.groups);
   gv.cu = reinterpret_cast<int32_t*>(ws + r.groups + (size_t)p.b.T * 8);
-  gv.len = gv.cu + groups + 1;
-  gv.rows = gv.len + groups;
-  gv.skip = gv.rows + groups;
+  gv.len = gv.cu + r.N + 1;
+  gv.rows = gv.len + r.N;
+  gv.skip = gv.rows + r.N;
+  gv.own = r.one ? groups + 1 : 0;
   AttnParams g = p;
   set_plan(&g, r.g, ws);
   g.split = r.g.wide;
-  g.causal = 0;
-  g.flat = 1;
+  g.causal = r.one && causal;
+  g.flat = groups;
   g.early = 1;
-  g.b.N = groups;
+  g.b.N = r.N;
   g.b.cu = gv.cu;
   g.b.kv_len = gv.len;
   g.b.rows = gv.rows;
   if (!r.g.wide) {
     g.whole_o = reinterpret_cast<float*>(ws + r.whole_g);
-    g.whole_ml = reinterpret_cast<float2*>(ws + r.whole_g + whole_ml);
+    g.whole_ml = reinterpret_cast<float2*>(ws + r.whole_g + (r.one ? 2 : 1) * whole_ml);
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf = cache->dtype == PAGED_BF16;
+  PAGED_CK(launch_paged_groups(p.b, gv, st), "paged_attention_shared groups launch");
+  if (r.one) {
+    g.flat_rows = (long long)rows;
+    g.b.skip = gv.skip;
+    PAGED_CK(launch_paged_rows(g, bf, st), "paged_attention_shared launch");
+    PAGED_CK(launch_paged_join_shared(g, g, gv.of_token, gv.own, bf, st), "paged_attention_shared join launch");
+    return MOE_OK;
   }
   set_plan(&p, r.p, ws + r.at_p);
   p.causal = causal != 0;
@@ -575,16 +605,13 @@ moe_status paged_attention_shared(const void* q, int64_t q_ts, int64_t q_hs, int
     p.whole_o = reinterpret_cast<float*>(ws + r.whole_p);
     p.whole_ml = reinterpret_cast<float2*>(ws + r.whole_p + whole_ml);
   }
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = cache->dtype == PAGED_BF16;
-  PAGED_CK(launch_paged_groups(p.b, gv, st), "paged_attention_shared groups launch");
   p.b.skip = gv.skip;
   p.late = 1;
   PAGED_CK(r.g.wide ? launch_paged_chunk(g, bf, st) : launch_paged_rows(g, bf, st),
            "paged_attention_shared launch");
   PAGED_CK(r.p.wide ? launch_paged_chunk(p, bf, st) : launch_paged_rows(p, bf, st),
            "paged_attention_shared launch");
-  PAGED_CK(launch_paged_join_shared(p, g, gv.of_token, bf, st), "paged_attention_shared join launch");
+  PAGED_CK(launch_paged_join_shared(p, g, gv.of_token, 0, bf, st), "paged_attention_shared join launch");
   return MOE_OK;
 }
 

@@ -117,7 +117,10 @@ struct AttnParams {
   BatchView b;
   float scale_log2;  // scale * log2(e)
   int causal, window;
-  int flat;  // every row sees every key (a group's rows and the keys that it shares)
+  // the first `flat` sequences are groups: every row sees every key (their rows and the
+  // keys that they share); their whole results begin flat_rows behind the others'
+  int flat;
+  long long flat_rows;
   // 256-row tiles: `tiles` of the batch; chunk c of a tile covers the keys
   // [c, c+1) * chunk behind its first visible one, the last goes to the end.
   // Partial results [T * Hq][chunks] where `split`.
@@ -182,17 +185,22 @@ cudaError_t launch_paged_chunk(const AttnParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st);
 // The join of two attentions' partial results: over the keys that groups of sequences
 // share (`g`, its batch the groups) and over the sequences' own (`p`).
+// (first: the number of p's first sequence of the batch)
 cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, const int2* of_token,
-                                     bool bf16, cudaStream_t st);
+                                     int first, bool bf16, cudaStream_t st);
 // The groups of a batch made safe (paged_shared.cu): cu [G + 1], len [G] and rows [G]
 // are the groups as a batch of sequences (their tokens, shared keys, a member's row of
 // the table), skip [N] the members' first own key, of_token [T] each new token's
-// sequence and group (-1: none; what no sequence holds is not written).
+// sequence and group (-1: none; what no sequence holds is not written).  In one batch
+// of both, an empty sequence lies between the groups and the sequences, G + 1 on.
 struct GroupView {
   const int32_t *cu_group, *shared;
   int G;
   int32_t *cu, *len, *rows, *skip;
   int2* of_token;
+  // 0, or where the batch's own sequences stand behind the groups in one batch of both
+  // (cu, len, rows and skip have room for them)
+  int own;
 };
 cudaError_t launch_paged_groups(const BatchView& b, const GroupView& g, cudaStream_t st);
 

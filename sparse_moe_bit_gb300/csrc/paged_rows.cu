@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       const int pos0 = use.s.kv - use.s.nq;
       auto vis = [&](int r, int& a, int& b) {
         const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
-        b = !p.flat && (p.causal || pos < 0) ? min(use.s.kv, pos + 1) : use.s.kv;
+        b = use.n >= p.flat && (p.causal || pos < 0) ? min(use.s.kv, pos + 1) : use.s.kv;
         a = p.window > 0 ? max(use.s.lo, window_begin(pos, p.window)) : use.s.lo;
       };
 #pragma unroll
@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(32 * kWarps)
           const int tok = fast_div(r0 + r, p.divG);
           const int head = use.h * p.G + (r0 + r - tok * p.G);
           if (!whole || p.whole_o) {
-            const long long at = whole ? (long long)(use.s.t0 + tok) * p.Hq + head : slot * kRowTile + r;
+            const long long at = whole ? (long long)(use.s.t0 + tok) * p.Hq + head + (use.n < p.flat ? p.flat_rows : 0)
+                                       : slot * kRowTile + r;
             float* dst = (whole ? p.whole_o : p.part_o) + at * D + g;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
@@ -774,7 +775,7 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, int n, const Seq&
   if (w0 == w1) {  // one warp's: written, or left whole
     r.o = p.whole_o;
     r.ml = p.whole_ml;
-    r.at = rid;
+    r.at = rid + (n < p.flat ? p.flat_rows : 0);
     r.n = p.whole_o ? 1 : 0;
     return r;
   }
@@ -791,6 +792,7 @@ __device__ __forceinline__ Parts parts_of(const AttnParams& p, int n, const Seq&
 struct SharedJoin {
   AttnParams p, g;
   const int2* of_token;  // a new token's sequence and group
+  int first;             // p's first sequence of the batch
 };
 template <int D, bool BF, int W>
 __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
   const int t = any ? (int)(rid / p.Hq) : 0, head = any ? (int)(rid - (long long)t * p.Hq) : 0;
   // (what no sequence holds has any number here: it is looked at before it is used)
   const int2 of = jp.of_token[t];
-  const int n = any && of.x >= 0 && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
+  const int n = any && of.x >= jp.first && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
   const Seq s = load_seq(p.b, max(n, 0)), gs = load_seq(g.b, max(k, 0));
   // (as above: no CTA leaves before it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -921,8 +923,8 @@ cudaError_t join_launch(const AttnParams& p, cudaStream_t st) {
 }
 template <int D, bool BF>
 cudaError_t join_shared_launch(const AttnParams& p, const AttnParams& g, const int2* of_token,
-                               cudaStream_t st) {
-  const SharedJoin jp{p, g, of_token};
+                               int first, cudaStream_t st) {
+  const SharedJoin jp{p, g, of_token, first};
   const long long rows = (long long)p.b.T * p.Hq;
   const int parts = p.parts + g.parts;
   if (parts <= 8) return join_w(paged_join_shared_kernel<D, BF, 1>, (rows + 3) / 4, 4, jp, st);
@@ -947,8 +949,8 @@ cudaError_t launch_paged_join(const AttnParams& p, bool bf16, cudaStream_t st) {
   PAGED_BY_DIM(join_launch, p, st);
 }
 cudaError_t launch_paged_join_shared(const AttnParams& p, const AttnParams& g, const int2* of_token,
-                                     bool bf16, cudaStream_t st) {
-  PAGED_BY_DIM(join_shared_launch, p, g, of_token, st);
+                                     int first, bool bf16, cudaStream_t st) {
+  PAGED_BY_DIM(join_shared_launch, p, g, of_token, first, st);
 }
 
 }  // namespace moe

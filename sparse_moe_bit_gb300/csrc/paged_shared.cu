@@ -39,15 +39,26 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BatchView b, con
   const int a0 = me == 0 ? 0 : n0, a1 = me == g.G - 1 ? b.N : n1;
   for (int n = a0 + threadIdx.x; n < a1; n += kThreads) {
     const bool in = n >= n0 && n < n1;
-    g.skip[n] = in ? len : 0;
+    const int at = g.own + n;
+    g.skip[at] = in ? len : 0;
+    if (g.own) {
+      g.cu[at] = b.cu[n];
+      if (n == b.N - 1) g.cu[at + 1] = b.cu[n + 1];
+      g.len[at] = b.kv_len[n];
+      g.rows[at] = n;
+    }
     const Seq s = load_seq(b, n);
-    for (int t = s.t0; t < s.t0 + s.nq; ++t) g.of_token[t] = make_int2(n, in ? me : -1);
+    for (int t = s.t0; t < s.t0 + s.nq; ++t) g.of_token[t] = make_int2(at, in ? me : -1);
   }
   if (threadIdx.x == 0) {
     g.len[me] = len;
     g.rows[me] = min(sh_first, b.N - 1);
     g.cu[me] = b.cu[n0];
     if (me == g.G - 1) g.cu[g.G] = b.cu[n1];
+    if (g.own) {
+      g.skip[me] = 0;
+      if (me == g.G - 1) g.len[g.G] = g.rows[g.G] = g.skip[g.G] = 0;
+    }
   }
 }
 
