@@ -33,8 +33,8 @@
 // A cluster of up to eight CTAs takes a row: each holds a slice of it in shared memory, read
 // from HBM once, and histograms, sums and positions meet through distributed shared memory.
 // Measured (fp32 logits, a graph's replay): one row of 130001, top-k 50 and top-p 0.95
-// 18.7 us; 48 of 65521 bf16, settings of their own 34; 256 of 131072 (134 MB) greedy 66,
-// no filter 152, top-k 50 142, nuclei 258 to 278.  (One CTA a row after another with the next row's read
+// 16.9 us; 48 of 65521 bf16, settings of their own 33; 256 of 131072 (134 MB) greedy 58,
+// no filter 145, top-k 50 129, nuclei 243 to 263.  (One CTA a row after another with the next row's read
 // ahead 325, CTAs of 1024 threads 299, when this stood at 301.)
 #include <algorithm>
 
@@ -622,7 +622,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   u = fminf(u, 0x1.fffffep-1f);
 
   // ---- the slice into shared memory, the largest logit and its first index
-  constexpr int AHEAD = 32 / VEC;  // vectors of a thread in flight
+  // vectors of a thread in flight (four times as many, which fp32 registers cannot hold
+  // beside the rest: 256 x 131072 267 us for 255, one row of 130001 18.7 for 16.9)
+  constexpr int AHEAD = 8 / VEC;
   const int vecs = (n + VEC - 1) / VEC;
   auto load = [&](int i, uint4& v) {
     const int at = begin + i * VEC;
