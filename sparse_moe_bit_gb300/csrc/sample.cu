@@ -34,7 +34,7 @@
 // from HBM once, and histograms, sums and positions meet through distributed shared memory.
 // Measured (fp32 logits, a graph's replay): one row of 130001, top-k 50 and top-p 0.95
 // 16.9 us; 48 of 65521 bf16, settings of their own 33; 256 of 131072 (134 MB) greedy 58,
-// no filter 145, top-k 50 129, nuclei 243 to 263.  (One CTA a row after another with the next row's read
+// no filter 142, top-k 50 128, nuclei 240 to 262.  (One CTA a row after another with the next row's read
 // ahead 325, CTAs of 1024 threads 299, when this stood at 301.)
 #include <algorithm>
 
@@ -325,11 +325,11 @@ struct Worker {
   }
 
   // The first token at which the sum of f(key, index), in order of index, passes
-  // `target(total)`, where `sums` are the warps' sums; its index, the total, and f there.
-  template <typename F, typename G>
-  __device__ int locate(const View& w, F f, G target_of, const unsigned long long* sums,
-                        unsigned long long& total, unsigned long long& value) {
-    unsigned long long all = 0, at;
+  // `target(total)`, where `sums` are the warps' sums: the thread that has it calls
+  // found(index, total, f there).
+  template <typename F, typename G, typename H>
+  __device__ void locate(const View& w, F f, G target_of, const unsigned long long* sums, H found) {
+    unsigned long long all = 0, at, total;
     for (int x = 0; x < kWarps; ++x) all += sums[x];
     totals(w, all, at, total);
     const unsigned long long target = target_of(total);
@@ -351,19 +351,13 @@ struct Worker {
         for (int i = i0; i < i1; ++i) {
           const unsigned long long v = f(w.key_at(i), w.index(i));
           if (target < at + v) {
-            for (int c = 0; c < w.cluster; ++c) {
-              peer_put(&sh.found[0], w.cluster > 1 ? c : w.rank, (unsigned long long)w.index(i));
-              peer_put(&sh.found[1], w.cluster > 1 ? c : w.rank, v);
-            }
+            found(w.index(i), total, v);
             break;
           }
           at += v;
         }
       }
     }
-    w.sync();
-    value = sh.found[1];
-    return (int)sh.found[0];
   }
 };
 
@@ -756,16 +750,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (cut) {
       keep.cut = 0x7fffffff;
       if (of_equal < equal) {
-        unsigned long long total, value;
         const uint32_t thr = keep.thr;
         auto is = [thr](uint32_t key, int) -> unsigned long long { return key == thr; };
         work.chunk_sums(w, is, sh.warp_kept);
-        keep.cut = work.locate(w, is, [of_equal](unsigned long long) { return of_equal - 1; }, sh.warp_kept,
-                               total, value);
+        work.locate(w, is, [of_equal](unsigned long long) { return of_equal - 1; }, sh.warp_kept,
+                    [&](int i, unsigned long long, unsigned long long) {
+                      for (int c = 0; c < w.cluster; ++c)
+                        peer_put(&sh.found[0], w.cluster > 1 ? c : w.rank, (unsigned long long)i);
+                    });
+        w.sync();
+        keep.cut = (int)sh.found[0];
       }
     }
   };
-  unsigned long long total, value;
 
   if (p.V + VEC > kList && (k > 0 || top_p < 1.f)) {
     // ---- counts and mean places in the bins of x: a token is 2^place_bits + its place in
@@ -969,8 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             if (w) add_wide(&sh.warp_kept[at / chunk], w);
           }
           __syncthreads();
-          const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
-          if (rank == 0 && tid == 0) put(token, total, value);
+          work.locate(whole, kept_weight, draw, sh.warp_kept, put);
           return;
         }
         keep.thr = kLowest;
@@ -994,8 +990,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (lane == 0) sh.warp_kept[warp] = sum;
     __syncthreads();
   }
-  const int token = work.locate(whole, kept_weight, draw, sh.warp_kept, total, value);
-  if (rank == 0 && tid == 0) put(token, total, value);
+  work.locate(whole, kept_weight, draw, sh.warp_kept, put);
 }
 
 template <typename T>
