@@ -34,8 +34,9 @@ enum { STEP_BF16 = 1, STEP_F16 = 2, STEP_F32 = 3, STEP_E4M3 = 4, STEP_I8 = 5 };
  * all in fp32; `sum` takes s rounded to x's type, y takes n.  n is computed from
  * s before that rounding.  With an 8-bit y, the features of a row in groups of
  * `group` share a scale:
- *   scale = max|n| / 448 (e4m3) or / 127 (int8),  y = n / scale rounded to
- *   nearest, ties to even;  y = 0 and scale = 0 where the group is all zeros
+ *   scale = max|n| / 448 (e4m3) or / 127 (int8) in fp32 (below 2^-126 rounded up, so
+ *           that y stays in its range; 0 where the group is all zeros, and only there)
+ *   y       = fp32's quotient n / scale rounded to nearest, ties to even (0 where scale is)
  * so that y * scale stands for n.  NaN and infinities reach the group's scale
  * (the scale of a group with either is not finite).  Squares are fp32's: of
  * magnitudes above 1e19 the mean is infinite and n is 0, of rows below 1e-22 it is 0

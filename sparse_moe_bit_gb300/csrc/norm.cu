@@ -95,16 +95,30 @@ __device__ __forceinline__ void store_row(void* base, long long i, const float (
     }
   }
 }
-// Eight bits: n / scale as a product with the scale's reciprocal, one division a group.
-// (`pre` keeps the reciprocal of a tiny scale in fp32's range.)  NaN stays NaN in e4m3 and
-// is 0 in int8, whose scale says it.
+// A group's scale: its largest magnitude (as bits) / top, rounded to nearest; below fp32's
+// normal numbers upwards, so that no quotient passes the type's end and no group but one of
+// zeros has a scale of 0.
+__device__ __forceinline__ float scale_of(uint32_t m, float top) {
+  const float v = __uint_as_float(m), scale = v / top;
+  return scale < 0x1p-126f ? __fdiv_ru(v, top) : scale;
+}
+// Eight bits: the quotient n / scale, one division a group: a product with the scale's
+// reciprocal, corrected by its remainder (Markstein), so that a quotient on a border between two
+// values is on it.  (The product alone is up to 1.5 steps of fp32 off.  `pre` keeps a tiny
+// scale's reciprocal and remainders in fp32's range; with an infinite scale there is no
+// remainder.)  NaN stays NaN in e4m3 and is 0 in int8, whose scale says it.
 struct Scaler {
-  float pre, inv;
+  float pre, by, inv;
   __device__ explicit Scaler(float scale) {
-    pre = scale < 1e-30f ? 0x1p64f : 1.f;
-    inv = scale == 0.f ? 0.f : 1.f / (scale * pre);
+    pre = scale < 1e-20f ? 0x1p64f : 1.f;
+    by = scale * pre;
+    inv = scale == 0.f ? 0.f : 1.f / by;
+    if (by == INFINITY) by = 0.f;
   }
-  __device__ __forceinline__ float operator()(float n) const { return n * pre * inv; }
+  __device__ __forceinline__ float operator()(float n) const {
+    const float m = n * pre, q = m * inv;
+    return fmaf(-fmaf(q, by, -m), inv, q);
+  }
 };
 __device__ __forceinline__ uint32_t put8x2(float a, float b, bool e4m3) {
   if (e4m3) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -260,7 +274,7 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W, W >= 8 && CH 
           }
           for (int s = lanes / 2; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
           if (i >= d) continue;
-          const float scale = __uint_as_float(m) / top;
+          const float scale = scale_of(m, top);
           if ((tid & (lanes - 1)) == 0) scales[fast_div(i, p.div)] = scale;
           const Scaler s(scale);
           float z[VEC];
@@ -298,20 +312,20 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W, W >= 8 && CH 
         }
       }
       if (W == 1) __syncwarp(); else __syncthreads();
-      for (int g = tid; g < groups; g += THREADS) scales[g] = __uint_as_float(mx[g]) / top;
+      for (int g = tid; g < groups; g += THREADS) scales[g] = scale_of(mx[g], top);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = (c * THREADS + tid) * VEC;
         if (i >= d) continue;
         float z[VEC];
         if (lanes > 0) {
-          const Scaler s(__uint_as_float(mx[fast_div(i, p.div)]) / top);
+          const Scaler s(scale_of(mx[fast_div(i, p.div)], top));
 #pragma unroll
           for (int e = 0; e < VEC; ++e) z[e] = s(v[c][e]);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
-            z[e] = Scaler(__uint_as_float(mx[fast_div(i + e, p.div)]) / top)(v[c][e]);
+            z[e] = Scaler(scale_of(mx[fast_div(i + e, p.div)], top))(v[c][e]);
         }
         put(z, i);
       }
