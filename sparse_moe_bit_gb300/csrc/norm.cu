@@ -288,23 +288,31 @@ __global__ void __launch_bounds__(W == 1 ? 32 * kRowsCta : 32 * W, W >= 8 && CH 
       for (int g = tid; g < groups; g += THREADS) mx[g] = 0;
       if (W == 1) __syncwarp(); else __syncthreads();
       const bool even = lanes > 0 && lanes % 32 == 0;  // a warp's lanes of a chunk in one group
+// All of a warp's maxima by shuffles before the first lane goes its own way.  (One
+      // chunk after another with a warp-wide reduction instruction in place of the shuffles,
+      // compiled for 64 registers, lost groups' maxima, with a __syncwarp before it too; for as many
+      // registers as it likes, or in a loop of its own like this one, the same was right.)
+      uint32_t m[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        m[c] = 0;
+        if ((c * THREADS + tid) * VEC < d && lanes > 0) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) m[c] = max(m[c], __float_as_uint(v[c][e]) & 0x7fffffffu);
+        }
+      }
+      if (even) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int s = 16; s; s >>= 1) m[c] = max(m[c], __shfl_xor_sync(0xffffffffu, m[c], s));
+      }
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int i = (c * THREADS + tid) * VEC;
-        uint32_t m = 0;
-        if (i < d && lanes > 0) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) m = max(m, __float_as_uint(v[c][e]) & 0x7fffffffu);
-        }
-        // (by shuffles: with a warp-wide reduction instruction here the first lane's own value
-        // was missing from its result)
-        if (even) {
-#pragma unroll
-          for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-        }
         if (i >= d) continue;
         if (lanes > 0) {
-          if (!even || (tid & 31) == 0) atomicMax(mx + fast_div(i, p.div), m);
+          if (!even || (tid & 31) == 0) atomicMax(mx + fast_div(i, p.div), m[c]);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e)

@@ -1,5 +1,5 @@
 """Edges of include/step.h's operators: quotients on a border between two 8-bit values,
-scales below fp32's normal numbers."""
+scales below fp32's normal numbers, groups of many warps."""
 import numpy as np
 import pytest
 import torch
@@ -89,3 +89,24 @@ def test_an_infinite_scale():
         assert (np.delete(y[:128], 7) == 0).all() and (y[128:] == TOP[out]).all()
         if out is E8:
             assert np.isnan(y[7])
+
+
+@pytest.mark.parametrize("d,group", [(512, 512), (768, 768), (3072, 768), (2048, 0), (4096, 0), (4096, 1024), (6144, 768),
+                                     (8192, 0), (8192, 512), (16384, 0), (24576, 1536), (32768, 0), (32768, 4096)])
+@pytest.mark.parametrize("out", [E8, I8], ids=["e4m3", "int8"])
+def test_the_largest_of_a_group_in_any_lane(d, group, out):
+    """Groups of whole warps, enough rows that a block takes several: the largest magnitude is
+    every lane's, chunk's and warp's in turn."""
+    rows, vectors = 1300, d // 8
+    x = torch.randn(rows, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(d)).to(BF)
+    at = torch.arange(rows, device="cuda")
+    x[at, at * 37 % vectors * 8 + at % 8] = 30.0
+    x[at, at * 32 % vectors * 8] = -29.0          # a first lane's
+    n = values(M.rms_norm(x, out_dtype=FP)).reshape(rows, -1, group or d)
+    y, s = M.rms_norm(x, out_dtype=out, group=group)
+    want = np.abs(n).max(-1) / TOP[out]
+    # (the quotient's rounding, and n's last bit)
+    assert np.all(np.abs(values(s) - want) <= 2.0 ** -22 * want)
+    got = y.float().double().cpu().numpy().reshape(n.shape) * values(s)[..., None]
+    half = 0.5 * want[..., None] if out is I8 else np.maximum(np.abs(n) * 2.0 ** -4, want[..., None] * 2.0 ** -10)
+    assert np.all(np.abs(got - n) <= half * (1 + 1e-5) + 2.0 ** -21 * np.abs(n))
