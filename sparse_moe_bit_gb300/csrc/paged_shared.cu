@@ -6,6 +6,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kFew = 8;  // tokens of a sequence that one thread maps
 
 // A CTA a group.  What a group can share: no more than its members all have before their
 // new tokens, so that every one of these keys is visible to all of its rows, and nothing
@@ -37,18 +38,32 @@ __global__ void __launch_bounds__(kThreads) groups_kernel(const BatchView b, con
   const int len = sh_with < 2 ? 0 : max(min(g.shared[me], sh_least), 0);
   // the first and the last group's CTA also take the sequences of no group
   const int a0 = me == 0 ? 0 : n0, a1 = me == g.G - 1 ? b.N : n1;
-  for (int n = a0 + threadIdx.x; n < a1; n += kThreads) {
-    const bool in = n >= n0 && n < n1;
-    const int at = g.own + n;
-    g.skip[at] = in ? len : 0;
-    if (g.own) {
-      g.cu[at] = b.cu[n];
-      if (n == b.N - 1) g.cu[at + 1] = b.cu[n + 1];
-      g.len[at] = b.kv_len[n];
-      g.rows[at] = n;
+  const int lane = threadIdx.x & 31;
+  for (int base = a0 + (int)threadIdx.x - lane; base < a1; base += kThreads) {
+    const int n = base + lane, at = g.own + n;
+    const bool there = n < a1, in = n >= n0 && n < n1;
+    const Seq s = load_seq(b, min(n, b.N - 1));
+    const int group = in ? me : -1;
+    if (there) {
+      g.skip[at] = in ? len : 0;
+      if (g.own) {
+        g.cu[at] = b.cu[n];
+        if (n == b.N - 1) g.cu[at + 1] = b.cu[n + 1];
+        g.len[at] = b.kv_len[n];
+        g.rows[at] = n;
+      }
     }
-    const Seq s = load_seq(b, n);
-    for (int t = s.t0; t < s.t0 + s.nq; ++t) g.of_token[t] = make_int2(at, in ? me : -1);
+    // a sequence's tokens: a few by its own thread, a chunk's by the warp (a call over one of
+    // 8192: 467 us, 502 with a thread for all)
+    const bool chunk = there && s.nq > kFew;
+    if (there && !chunk)
+      for (int t = s.t0; t < s.t0 + s.nq; ++t) g.of_token[t] = make_int2(at, group);
+    for (unsigned left = __ballot_sync(0xffffffffu, chunk); left; left &= left - 1) {
+      const int src = __ffs((int)left) - 1;
+      const int t0 = __shfl_sync(0xffffffffu, s.t0, src), t1 = t0 + __shfl_sync(0xffffffffu, s.nq, src);
+      const int2 of = make_int2(g.own + base + src, __shfl_sync(0xffffffffu, group, src));
+      for (int t = t0 + lane; t < t1; t += 32) g.of_token[t] = of;
+    }
   }
   if (threadIdx.x == 0) {
     g.len[me] = len;
