@@ -29,13 +29,17 @@
 //
 // Bound: latency for a few rows; for many the chain of a row's steps (read, maximum,
 // histogram, its sums over the CTAs, the pass, the threshold, the draw), of which an SM has
-// two CTAs' at once, and the weights' arithmetic (some 45 instructions an element, once).
+// two CTAs' at once where a slice is at most 16400 logits (rows of up to some 131190), else one's;
+// and the weights' arithmetic (some 45 instructions an element, once).
 // A cluster of up to eight CTAs takes a row: each holds a slice of it in shared memory, read
 // from HBM once, and histograms, sums and positions meet through distributed shared memory.
 // Measured (fp32 logits, a graph's replay): one row of 130001, top-k 50 and top-p 0.95
-// 16.9 us; 48 of 65521 bf16, settings of their own 33; 256 of 131072 (134 MB) greedy 58,
-// no filter 142, top-k 50 128, nuclei 240 to 262.  (One CTA a row after another with the next row's read
-// ahead 325, CTAs of 1024 threads 299, when this stood at 301.)
+// 16.9 us; 48 of 65521 bf16, settings of their own 33; 256 of 131072 (134 MB) greedy 52, no
+// filter 141, top-k 50 127, nuclei 240 to 262; of 151936, one CTA an SM, 105, 216, 213 and 444;
+// of 131072 where a mask leaves 30 tokens, top-k 50 295, with a nucleus of 0.95 453: fewer
+// tokens than k, so that the threshold is -inf, and all levels of the histograms are walked.
+// (One CTA a row after another with the next row's read ahead 325, CTAs of 1024 threads 299,
+// when this stood at 301.)
 #include <algorithm>
 
 #include "paged_internal.h"
@@ -995,16 +999,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t sample_launch(const SampleParams& p, cudaStream_t st) {
-  // CTAs of a row: until two slices fit an SM, and while they are no more than run at once
-  // with half as many for each (48 rows of 65521: 8 CTAs each 34 us, although the last rows
-  // wait for the first; 4 each 39)
+  // CTAs of a row: until two fit an SM (256 rows, top-p 0.9: of 40000 logits 4 CTAs of a row 90
+  // us, 2 that have an SM each 99; 49152 100 and 111; 98304 8 CTAs 216, 4 226; 70000 184 and 181,
+  // with L2 cold 196 and 200), and while they are no more than run at once with half as many for
+  // each (48 rows of 65521: 8 CTAs each 34 us, although the last rows wait for the first; 4
+  // each 39)
+  constexpr int kOfSm = 228 * 1024, kOfCta = 1024;  // shared memory; what a CTA takes beside its own
   const int sms = device_sms();
-  int cluster = 1;
-  while (cluster < kMaxCluster && (p.V > 24576 * cluster || (p.V > 2048 * cluster && (long long)p.B * cluster < 2 * sms)))
-    cluster *= 2;
   // (the row may begin up to seven places behind a 16-byte boundary)
-  const int slice = ((p.V + 7 + cluster - 1) / cluster + 7) / 8 * 8;
-  const int smem = (int)sizeof(Shared) + slice * 4;
+  auto slice_of = [&](int c) { return ((p.V + 7 + c - 1) / c + 7) / 8 * 8; };
+  auto bytes_of = [&](int c) { return (int)sizeof(Shared) + slice_of(c) * 4; };
+  int cluster = 1;
+  while (cluster < kMaxCluster && (2 * (bytes_of(cluster) + kOfCta) > kOfSm ||
+                                   (p.V > 2048 * cluster && (long long)p.B * cluster < 2 * sms)))
+    cluster *= 2;
+  const int slice = slice_of(cluster), smem = bytes_of(cluster);
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem((const void*)sample_kernel<T>, 232448 - 1024, allowed);
   if (e != cudaSuccess) return e;
