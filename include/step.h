@@ -45,7 +45,7 @@ enum { STEP_BF16 = 1, STEP_F16 = 2, STEP_F32 = 3, STEP_E4M3 = 4, STEP_I8 = 5 };
  *           token and head strides in elements.  sum: NULL exactly where
  *           residual is.  sum may be residual or x, and y may be x, with the same
  *           type and strides (in place); otherwise no output may overlap another
- *           array.
+ *           array, nor a row of it another row.
  *   weight  dtype or fp32 [d], or NULL (ones; without unit_offset)
  *   y       y_dtype, any of the five
  *   scales  fp32 [T][H][d / group] dense for an 8-bit y, else NULL
@@ -77,7 +77,7 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *           [O][K / group], all dense, 16-byte aligned; scales below 2^100
  *   group   a multiple of 64 that divides K
  *   y       BF16, F16 or F32 [T][O], rows y_token_stride elements apart; may not
- *           overlap x
+ *           overlap x, nor one row another
  * Every 16 tokens read the weights anew (one after another from L2), so a prompt's
  * products are better served by a matrix product of 16-bit weights.  K up to 36864,
  * T up to 524280.  The result does not depend on timing, nor a token's on the others in

@@ -27,6 +27,8 @@ int size_of(int dtype) {
 }
 bool is8(int dtype) { return dtype == STEP_E4M3 || dtype == STEP_I8; }
 bool is_float(int dtype) { return dtype >= STEP_BF16 && dtype <= STEP_F32; }
+// whether n rows of `width` elements, `stride` apart, write over one another
+bool overlap(int n, int64_t stride, int width) { return n > 1 && stride < width && stride > -(int64_t)width; }
 
 }  // namespace
 
@@ -61,6 +63,8 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_ts,
   if (sum && (y == sum || y == residual || (sum == x && (s_ts != x_ts || s_hs != x_hs)) ||
               (sum == residual && (s_ts != r_ts || s_hs != r_hs))))
     return fail(MOE_ERR_INVALID_ARG, "sum in place with other strides, or y over it");
+  if (overlap(T, y_ts, d) || overlap(H, y_hs, d) || (sum && (overlap(T, s_ts, d) || overlap(H, s_hs, d))))
+    return fail(MOE_ERR_INVALID_ARG, "rows of y or sum overlap");
   NormParams p{};
   p.x = x;
   p.r = residual;
@@ -113,6 +117,7 @@ moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_ts, const
   if (!aligned(codes, 16) || !aligned(scale, 16) || !aligned(bias, 16) || !aligned(x_scale, 4) ||
       !aligned(y, size_of(y_dtype)))
     return fail(MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (overlap(T, y_ts, O)) return fail(MOE_ERR_INVALID_ARG, "rows of y overlap");
   Linear4Params p{};
   p.x = x;
   p.xs = x_scale;
