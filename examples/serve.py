@@ -52,6 +52,11 @@ class Server:
             step = torch.full((o, k // 64), (12 / k) ** 0.5 / 15, dtype=torch.float16, device="cuda")
             return codes, step, -7.5 * step
 
+        def dense(codes, step, bias):
+            """The same weights in 16 bits, for the products of a prompt."""
+            c = torch.stack([codes & 15, codes >> 4], -1).view(codes.shape[0], -1, 64)
+            return (c * step[..., None].float() + bias[..., None].float()).flatten(1).bfloat16()
+
         def norm():
             return (1 + 0.1 * torch.randn(s.d, device="cuda", generator=g)).bfloat16()
 
@@ -59,6 +64,8 @@ class Server:
         self.w_qkv = [weights(s.d, (s.hq + 2 * s.hk) * s.dim) for _ in range(s.layers)]
         self.w_out = [weights(s.hq * s.dim, s.d) for _ in range(s.layers)]
         self.w_head = weights(s.d, s.vocab)
+        self.prompt_qkv = [dense(*w) for w in self.w_qkv]
+        self.prompt_out = [dense(*w) for w in self.w_out]
         self.norms = [(norm(), norm()) for _ in range(s.layers)]
         self.last_norm = norm()
         shape = gen.MoEShape(d=s.d, E=16, k=2, I=128)
@@ -107,14 +114,26 @@ class Server:
         # the stream, and what is added to it next: every norm does that
         x = self.embedding[torch.cat(tokens).long()]
         more = torch.zeros_like(x)
+        # Beyond 16 tokens linear4 reads the weights more than once; without a fork's slots
+        # next to one another there are no keys to read together.
+        prompt, lone = x.shape[0] > 16, len(first) == len(slots)
         for l in range(s.layers):
-            y, scale, x = M.rms_norm(more, self.norms[l][0], residual=x, out_dtype=torch.int8, group=64)
-            qkv = M.linear4(y, *self.w_qkv[l], x_scale=scale).view(-1, s.hq + 2 * s.hk, s.dim)
-            q, k, v = qkv.split([s.hq, s.hk, s.hk], 1)
+            if prompt:
+                y, x = M.rms_norm(more, self.norms[l][0], residual=x)
+                qkv = y @ self.prompt_qkv[l].T
+            else:
+                y, scale, x = M.rms_norm(more, self.norms[l][0], residual=x, out_dtype=torch.int8, group=64)
+                qkv = M.linear4(y, *self.w_qkv[l], x_scale=scale)
+            q, k, v = qkv.view(-1, s.hq + 2 * s.hk, s.dim).split([s.hq, s.hk, s.hk], 1)
             kp, vp = self.cache[2 * l], self.cache[2 * l + 1]
             q = M.rope_append(q, k, v, kp, vp, table, cu, kv_len, self.freq, mscale=self.mscale)
-            o = M.paged_attention_shared(q, kp, vp, table, cu, kv_len, groups, shared, **hints)
-            o = M.linear4(o.view(-1, s.hq * s.dim), *self.w_out[l])
+            if lone:
+                o = M.paged_attention(q, kp, vp, table, cu, kv_len, max_q=max(new),
+                                      max_kv=max(self.held[i] for i in slots))
+            else:
+                o = M.paged_attention_shared(q, kp, vp, table, cu, kv_len, groups, shared, **hints)
+            o = o.view(-1, s.hq * s.dim)
+            o = o @ self.prompt_out[l].T if prompt else M.linear4(o, *self.w_out[l])
             y, x = M.rms_norm(o, self.norms[l][1], residual=x)
             more = self.moe[l].forward(y)
         y, _ = M.rms_norm(more, self.last_norm, residual=x)
