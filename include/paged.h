@@ -164,6 +164,12 @@ moe_status paged_attention(const void* q, int64_t q_token_stride, int64_t q_head
  * first keys (the continuations of one prompt, pages_fork): a group's shared
  * keys are read once for all of its new tokens.  Results are paged_attention's
  * (without a window), up to the rounding of another order of sums.
+ * paged_attention reads the keys of a group's later sequences from L2, and is the faster one
+ * (by up to a half of this call's time) until the shared keys and values, counted once for each
+ * sequence, are about L2's size: some 150 MB, in groups of four and more (32 sequences, 16/2
+ * heads of 256, bf16: 1200 shared keys, 79 MB, 27 us plain and 34 shared; 2500 37 and 30; 48 of
+ * 16384 219 and 44).  A batch that shares nothing is paged_attention's: here every row's results
+ * are partial ones, joined behind (a chunk of 4096 new tokens alone 181 us, 115 plain).
  *   cu_group  int32 [groups + 1]: group g holds the sequences cu_group[g] ..
  *             cu_group[g+1]-1; read clamped into [0, N] and non-decreasing.
  *             Sequences outside every group share nothing.

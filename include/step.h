@@ -41,6 +41,8 @@ enum { STEP_BF16 = 1, STEP_F16 = 2, STEP_F32 = 3, STEP_E4M3 = 4, STEP_I8 = 5 };
  * (the scale of a group with either is not finite).  Squares are fp32's: of
  * magnitudes above 1e19 the mean is infinite and n is 0, of rows below 1e-22 it is 0
  * and n goes by eps alone (with eps 0 an infinity, and NaN where s is 0).
+ * A row's squares are added in an order that goes by d, alignment and whether T * H is below
+ * four rows an SM: between a small and a large batch a row's n may differ in fp32's last bits.
  *   x, residual, sum  `dtype` (BF16, F16 or F32) [T][H][d]; features contiguous,
  *           token and head strides in elements.  sum: NULL exactly where
  *           residual is.  sum may be residual or x, and y may be x, with the same
@@ -78,9 +80,12 @@ moe_status rms_norm(const void* x, int dtype, int T, int H, int d, int64_t x_tok
  *   group   a multiple of 64 that divides K
  *   y       BF16, F16 or F32 [T][O], rows y_token_stride elements apart; may not
  *           overlap x, nor one row another
- * Every 16 tokens read the weights anew (one after another from L2), so a prompt's
- * products are better served by a matrix product of 16-bit weights.  K up to 36864,
- * T up to 524280.  The result does not depend on timing, nor a token's on the others in
+ * Every 16 tokens (8 where K is above 16384) read the weights anew, one after another from
+ * L2, and turn them into operands anew.  A matrix product of 16-bit weights, where a caller keeps
+ * those too, is the faster one beyond 16 tokens for a projection (2048 -> 5120, weights in L2,
+ * 8 tokens 8.6 us here and 6.6 there, 40 13.5 and 6.6, 256 35 and 10), beyond 32 for a vocabulary
+ * (2048 -> 131072, 8 tokens 37 and 82, 32 82 and 86, 64 153 and 97, 256 606 and 109): a prompt's
+ * products are better served so.  K up to 36864, T up to 524280.  The result does not depend on timing, nor a token's on the others in
  * the call beyond the split that T chooses.
  */
 moe_status linear4(const void* x, int x_dtype, int T, int K, int64_t x_token_stride,

@@ -11,9 +11,12 @@
 // An 8-bit x has its own scale applied after a 64-wide part (or at the end, where a
 // token has one).
 //
-// Bound: HBM (half a byte a weight plus four a group) for one token, beyond that the
-// instructions that turn codes into operands (some 95 a part of 16 x 64 weights, tokens up
-// to 8; 47 % of the ALU and 56 % of the issue slots).  A warp has 16 rows of weights as the
+// Floor: HBM (half a byte a weight plus four a group).  For up to 8 tokens over a vocabulary no
+// unit is full: DRAM 52 %, the ALU 48 % and the issue slots 58 % of the cycles in which an SM
+// works, with 16 warps of 116 registers an SM (22 % of what it holds) to hide one another's
+// waits.  From 16 tokens on it is the instructions that turn codes into operands, some 95 a part of
+// 16 x 64 weights, done anew for every 16 tokens (8 where K is above 16384, whose tokens no eighth
+// of K leaves room for).  A warp has 16 rows of weights as the
 // wide side of mma.sync (m16n8k16) and 8 or 16 tokens as the narrow one; more tokens are
 // further CTAs' (up to 64 of a warp were slower at every size: registers and reads of the
 // tokens).  Lane (g, j) of a warp takes rows g and g + 8 and of each part of 64 weights the
@@ -29,7 +32,8 @@
 // partial sums meet in shared memory, in a fixed order.
 // Measured (a graph replay's time, weights not in L2, of which some 5 us are the method's):
 // 5120 x 2048, one token 11.4 us, 8 13.4, 64 23.7; 2047 x 4096, 37 tokens of e4m3 21.6;
-// 130001 x 2048 (150 MB), one token 40, 8 42 (4.1 TB/s), 16 50, 256 597.
+// 130001 x 2048 (150 MB), one token 42, 8 42 (4.1 TB/s), 16 56, 32 87, 64 157, 256 605; a product
+// of 16-bit weights, 131072 of them, by the library 97, 97, 100, 100, 110 and 118.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

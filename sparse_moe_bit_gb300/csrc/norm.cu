@@ -7,8 +7,10 @@
 // is one launch's latency.  A row is read once and stays in registers, two vectors of
 // eight a thread, W warps to a row; a CTA walks over rows with the weights in registers
 // and reads its next row before it is done with one.  Measured (x + r, L2 warm): 8192 rows
-// of 2048 in bf16 22.7 us (134 MB, 5.9 TB/s), to e4m3 25 (117 MB, 4.7 TB/s), fp32 49.5
-// (268 MB, 5.4 TB/s); 4096 of 4096 22.6; 65552 heads of 256, no sum, 12.5; one row 4.3.
+// of 2048 in bf16 22.7 us (134 MB, 5.9 TB/s), to e4m3 26.8 (117 MB, 4.4 TB/s), fp32 51
+// (268 MB, 5.2 TB/s); 4096 of 4096 23, to e4m3 27; 65552 heads of 256, no sum, 12.5 (67 MB, of
+// which L2 holds most: 15 with L2 cold), of 128 as long, since half of a warp's lanes have no
+// features; 2000 of 8191, which start anywhere and take one feature a load, 41; one row 4.2.
 // A group's largest magnitude is kept as the bits of a non-negative number, whose order as
 // integers puts NaN above
 // infinity, so that neither is lost in a maximum.
@@ -349,7 +351,7 @@ cudaError_t norm_launch(const NormParams& p, cudaStream_t st) {
   const bool q = p.y_dtype == STEP_E4M3 || p.y_dtype == STEP_I8;
   const dim3 block(W == 1 ? 32 * ROWS : 32 * W);
   // as many CTAs as run at once, each with its share of the rows: it prefetches its next
-  // (8192 x 2048 to e4m3: 25 us; twice as many 26.7, a CTA a row 36)
+  // (8192 x 2048 to e4m3, when this stood at 25 us: twice as many 26.7, a CTA a row 36)
   static std::atomic<int> fit[2]{};
   int each = fit[q].load(std::memory_order_relaxed);
   if (each == 0) {
@@ -379,7 +381,8 @@ bool aligned_to(const void* p, long long a, long long b, int es, int bytes) {
 // 27 us, two with four vectors 33, eight with one 34; 4096 x 4096 eight warps 24, four 27,
 // sixteen with one vector 27; 65536 x 512 one warp 46, two 47, four 56).  Where SMs have
 // few rows a thread has one vector, eight warps up to 2048 features (16 x 2048 4.3 us, 6.3
-// with four).
+// with four).  The launch bounds keep 64 registers where a thread has two vectors and a row eight
+// warps or more, which spills 48 bytes a thread in fp32, 80 with 8 bits out, up to 24 in bf16.
 template <typename T>
 cudaError_t norm_by_shape(const NormParams& p, cudaStream_t st) {
   const int es = sizeof(T), ys = p.y_dtype == STEP_F32 ? 4 : p.y_dtype <= STEP_F16 ? 2 : 1;

@@ -39,7 +39,7 @@
 // of 131072 where a mask leaves 30 tokens, top-k 50 295, with a nucleus of 0.95 453: fewer
 // tokens than k, so that the threshold is -inf, and all levels of the histograms are walked.
 // (One CTA a row after another with the next row's read ahead 325, CTAs of 1024 threads 299,
-// when this stood at 301.)
+// when this stood at 301.  64 registers, for two CTAs an SM, spill 20 to 24 bytes a thread.)
 #include <algorithm>
 
 #include "paged_internal.h"

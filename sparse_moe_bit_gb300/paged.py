@@ -333,7 +333,9 @@ def paged_attention_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     read through the first one's row of the table.  ``max_q``, ``max_group``, ``max_shared``
     and ``max_tail`` (the longest chunk, the most new tokens of a group, the most keys of a
     group, the most keys of a sequence behind them, if the caller knows them) choose kernels
-    and splits and bound nothing.  The rest is as for paged_attention;
+    and splits and bound nothing.  Faster than paged_attention once the shared keys and values,
+    counted once for each sequence, are some 150 MB in groups of four and more; slower below,
+    and where nothing is shared.  The rest is as for paged_attention;
     paged_attention_shared_workspace() in include/paged.h sizes ``workspace``."""
     lib = _library()
     if max(max_q, max_group, max_shared, max_tail) > 0x7fffffff:

@@ -65,7 +65,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     ``weight`` [d] of x's type or fp32 (``unit_offset``: 1 + weight).  Returns
     y of ``out_dtype`` (default x's); of torch.float8_e4m3fn or torch.int8: y and its
     scales, fp32 [..., d / group], one for ``group`` features (0: a row); and behind
-    them, with a residual, x + residual in x's type.  ``out`` may be x, ``sum_out``
+    them, with a residual, x + residual in x's type.  The last bits of a row may go by how
+    many rows the call has (include/step.h).  ``out`` may be x, ``sum_out``
     x or the residual (in place)."""
     shape, xt = x.shape, x.dtype
     dt = _DTYPE.get(xt, 0)
@@ -139,7 +140,8 @@ def linear4(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor, bias: tor
 
     x is bf16 or fp16 (y of its type unless ``out_dtype`` says otherwise), or e4m3 or int8
     with ``x_scale`` fp32 [T, K / x_group] (y is bf16 unless told), as rms_norm returns
-    them.  Made for a decode batch: every 16 tokens read the weights anew."""
+    them.  Made for a decode batch: every 16 tokens (8 where K is above 16384) read the weights
+    anew, and beyond 16 to 32 tokens a matrix product of 16-bit weights is the faster one."""
     if x.dim() != 2 or codes.dim() != 2 or scale.dim() != 2:
         raise ValueError("x, codes and scale must have two axes")
     T, K = x.shape
