@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int before = 0;
   for (int n0 = 0; n0 < p.b.N; n0 += kThreads) {
     const int n = n0 + threadIdx.x;
-    const int nt = n < p.b.N ? (load_seq(p.b, n).nq * p.G + 255) / 256 : 0;
+    const int nt = n < p.b.N ? (load_seq<true>(p.b, n).nq * p.G + 255) / 256 : 0;
     int inc = nt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int tile = sh_find[1];
-  const Seq s = load_seq(p.b, n);
+  const Seq s = load_seq<true>(p.b, n);
   const int rows = s.nq * p.G;
   const int r0 = tile * 256, r1 = min(r0 + 256, rows);
   const int2 kr = key_range(p, s, r0, r1);
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hi = ck == p.chunks - 1 ? kr.y : kr.x + (int)min(c0 + p.chunk, (long long)span);
   const int first = TMA ? lo & ~63 : lo;
   const int nb = hi > lo ? (hi - first + kTileKeys - 1) / kTileKeys : 0;
-  const int32_t* table = table_row(p.b, n);
+  const int32_t* table = table_row<true>(p.b, n);
 
   // this thread's row in the softmax warps (the other warps: unused)
   const int quarter = warp & 3, half = ((warp - kSoftWarp0) >> 2) & 1;

@@ -48,11 +48,13 @@ struct BatchView {
   long long table_stride;
   int capacity;  // min(width * page, 2^31 - 1): the longest context a table row holds
   // attention over shared keys: the sequences' rows of the table where they are not
-  // their own numbers, and the first key that each looks at (NULL: 0)
+  // their own numbers, and the first key that each looks at (NULL: 0).  Code that knows
+  // of no such batch (SHARED false) does not ask.
   const int32_t *rows, *skip;
 };
+template <bool SHARED = false>
 __device__ __forceinline__ const int32_t* table_row(const BatchView& b, int n) {
-  return b.table + (b.rows ? b.rows[n] : n) * b.table_stride;
+  return b.table + (SHARED && b.rows ? b.rows[n] : n) * b.table_stride;
 }
 
 // One sequence of a batch with its metadata made safe.
@@ -60,6 +62,7 @@ struct Seq {
   int t0, nq, kv;  // first new token, new tokens, context
   int lo;          // first key that is looked at
 };
+template <bool SHARED = false>
 __device__ __forceinline__ Seq load_seq(const BatchView& b, int n) {
   Seq s;
   const int t0 = min(max(b.cu[n], 0), b.T);
@@ -67,7 +70,7 @@ __device__ __forceinline__ Seq load_seq(const BatchView& b, int n) {
   s.t0 = t0;
   s.nq = t1 - t0;
   s.kv = min(max(b.kv_len[n], 0), b.capacity);
-  s.lo = b.skip ? b.skip[n] : 0;
+  s.lo = SHARED && b.skip ? b.skip[n] : 0;
   return s;
 }
 // The sequence of new token t: the last n with cu[n] <= t (-1: none).

@@ -179,8 +179,10 @@ __device__ __forceinline__ int owner_of(long long U, int W, long long u) {
 
 // NB: blocks of 8 rows of a tile.  TMA: a group is copied as boxes of the pages'
 // rows, a lane each; otherwise (pages that no box of 8 rows divides) by 16-byte
-// copies.
-template <int D, int NB, bool BF, bool TMA>
+// copies.  SHARED: part of an attention over shared keys (of groups, of the sequences' own
+// keys, or both), whose results are another kernel's to join; in one kernel for both, plain
+// attention's small batches took 0.2 to 0.6 us of 7 to 19 longer.
+template <int D, int NB, bool BF, bool TMA, bool SHARED>
 __global__ void __launch_bounds__(32 * kWarps)
     paged_rows_kernel(const __grid_constant__ RowsParams rp) {
   const AttnParams& p = rp.a;
@@ -193,7 +195,8 @@ __global__ void __launch_bounds__(32 * kWarps)
   __shared__ long long sh_warp[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the join may be set up while this grid runs
-  early_wait(p);
+  if constexpr (SHARED) early_wait(p);
+  else asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- groups before each slice of `per` sequences; CTA 0 leaves the sums for
   // the join
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   const int n0 = threadIdx.x * per, n1 = min(n0 + per, p.b.N);
   long long mine = 0;
   for (int n = n0; n < n1; ++n) {
-    const Extent e = extent_of(p, load_seq(p.b, n), KG, TILE);
+    const Extent e = extent_of(p, load_seq<SHARED>(p.b, n), KG, TILE);
     mine += (long long)e.items * e.groups;
   }
   long long inc = mine;
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     long long at = inc - mine;
     for (int n = n0; n < n1; ++n) {
       p.before[n] = at;
-      const Extent e = extent_of(p, load_seq(p.b, n), KG, TILE);
+      const Extent e = extent_of(p, load_seq<SHARED>(p.b, n), KG, TILE);
       at += (long long)e.items * e.groups;
     }
     if (threadIdx.x == 0) p.before[p.b.N] = U;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   // between its first and its last)
   const int W = (int)min((long long)(gridDim.x * kWarps), U), w = blockIdx.x * kWarps + warp;
   if (w >= W) {
-    late_wait(p);
+    if constexpr (SHARED) late_wait(p);
     return;
   }
   const long long u0 = share_of(U, W, w);
@@ -248,12 +251,12 @@ __global__ void __launch_bounds__(32 * kWarps)
   };
   auto enter = [&](Cursor& c) {  // the next sequence with rows, from c.n on
     for (; c.n < p.b.N; ++c.n) {
-      c.s = load_seq(p.b, c.n);
+      c.s = load_seq<SHARED>(p.b, c.n);
       c.e = extent_of(p, c.s, KG, TILE);
       if (c.e.items > 0) break;
     }
     // (behind the last group there may be none: nothing reads it)
-    c.table = table_row(p.b, min(c.n, p.b.N - 1));
+    c.table = table_row<SHARED>(p.b, min(c.n, p.b.N - 1));
   };
   auto advance = [&](Cursor& c) {
     if (++c.g < c.e.groups) return;
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(32 * kWarps)
       const int pos0 = use.s.kv - use.s.nq;
       auto vis = [&](int r, int& a, int& b) {
         const int pos = pos0 + fast_div(min(r0 + r, rows - 1), p.divG);
-        b = use.n >= p.flat && (p.causal || pos < 0) ? min(use.s.kv, pos + 1) : use.s.kv;
+        b = (!SHARED || use.n >= p.flat) && (p.causal || pos < 0) ? min(use.s.kv, pos + 1) : use.s.kv;
         a = p.window > 0 ? max(use.s.lo, window_begin(pos, p.window)) : use.s.lo;
       };
 #pragma unroll
@@ -618,16 +621,17 @@ __global__ void __launch_bounds__(32 * kWarps)
           if (r0 + r >= rows) continue;
           const int tok = fast_div(r0 + r, p.divG);
           const int head = use.h * p.G + (r0 + r - tok * p.G);
-          if (!whole || p.whole_o) {
-            const long long at = whole ? (long long)(use.s.t0 + tok) * p.Hq + head + (use.n < p.flat ? p.flat_rows : 0)
+          if (SHARED || !whole) {
+            const bool apart = SHARED && whole;
+            const long long at = apart ? (long long)(use.s.t0 + tok) * p.Hq + head + (use.n < p.flat ? p.flat_rows : 0)
                                        : slot * kRowTile + r;
-            float* dst = (whole ? p.whole_o : p.part_o) + at * D + g;
+            float* dst = (apart ? p.whole_o : p.part_o) + at * D + g;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
               dst[d * 16] = o[nb][d][i] * kDown;
               dst[d * 16 + 8] = o[nb][d][2 + i] * kDown;
             }
-            if (g == 0) (whole ? p.whole_ml : p.part_ml)[at] = make_float2(m[nb][i], sum * kDown);
+            if (g == 0) (apart ? p.whole_ml : p.part_ml)[at] = make_float2(m[nb][i], sum * kDown);
           } else {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             uint16_t* dst = p.o + (use.s.t0 + tok) * p.o_ts + head * p.o_hs + g;
@@ -666,7 +670,7 @@ __global__ void __launch_bounds__(32 * kWarps)
   } else {
     cp_async_wait<0>();
   }
-  late_wait(p);
+  if constexpr (SHARED) late_wait(p);
 }
 
 // Join of a row's parts, in their order: warp w of the row's CTA takes parts
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
   // (what no sequence holds has any number here: it is looked at before it is used)
   const int2 of = jp.of_token[t];
   const int n = any && of.x >= jp.first && of.x < p.b.N ? of.x : -1, k = of.y >= 0 && of.y < g.b.N ? of.y : -1;
-  const Seq s = load_seq(p.b, max(n, 0)), gs = load_seq(g.b, max(k, 0));
+  const Seq s = load_seq<true>(p.b, max(n, 0)), gs = load_seq<true>(g.b, max(k, 0));
   // (as above: no CTA leaves before it)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n < 0 || t < s.t0 || t >= s.t0 + s.nq) return;
@@ -864,11 +868,12 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W)
     p.lse[rid] = total == 0.f ? kNegInf : kLn2 * m + logf(total);
 }
 
-template <int D, int NB, bool BF, bool TMA>
-cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
+template <int D, int NB, bool BF, bool TMA, bool SHARED>
+cudaError_t rows_launch_s(const RowsParams& rp, cudaStream_t st) {
   using C = RowsCfg<D>;
+  const auto kern = paged_rows_kernel<D, NB, BF, TMA, SHARED>;
   static std::atomic<uint64_t> allowed{0};
-  const cudaError_t e = allow_smem((const void*)paged_rows_kernel<D, NB, BF, TMA>, C::SMEM, allowed);
+  const cudaError_t e = allow_smem((const void*)kern, C::SMEM, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(rp.a.warps / kWarps);
@@ -879,8 +884,14 @@ cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
   a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
-  c.numAttrs = rp.a.late || rp.a.early ? 1 : 0;
-  return cudaLaunchKernelEx(&c, paged_rows_kernel<D, NB, BF, TMA>, rp);
+  c.numAttrs = SHARED ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, rp);
+}
+template <int D, int NB, bool BF, bool TMA>
+cudaError_t rows_launch_t(const RowsParams& rp, cudaStream_t st) {
+  // (an attention over shared keys starts before the kernel ahead of it is over)
+  if (rp.a.late || rp.a.early) return rows_launch_s<D, NB, BF, TMA, true>(rp, st);
+  return rows_launch_s<D, NB, BF, TMA, false>(rp, st);
 }
 
 template <int D, bool BF>
